@@ -38,7 +38,9 @@ STATUS_NAMES = {0: "DCP_OK", 1: "DCP_ERR_INVALID_ARG", 2: "DCP_ERR_UNSUPPORTED_D
 EXPORTS = ("dcp_lse_pack_dim", "dcp_status_string", "dcp_last_error_message", "dcp_pack_send",
            "dcp_lse_combine", "dcp_unpack_combine", "dcp_decode_attention_workspace_size",
            "dcp_decode_attention", "dcp_decode_attention_paged", "dcp_decode_attention_noalloc",
-           "dcp_decode_attention_mla", "dcp_device_status")
+           "dcp_decode_attention_mla", "dcp_qk_norm_rope_append", "dcp_extend_attention_workspace_size",
+           "dcp_extend_attention_paged", "dcp_attention_weights_paged", "dcp_cache_evict_paged",
+           "dcp_device_status")
 
 
 class DcpError(RuntimeError):
@@ -95,6 +97,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.dcp_decode_attention_mla.restype = i32
         lib.dcp_decode_attention_mla.argtypes = ([i32] * 6 + [vp, i64, i64] + [vp, i64, i64, i64]
                                                  + lib.dcp_decode_attention.argtypes[19:])
+        f32, rows2, pool = ctypes.c_float, [vp, i64, i64], [vp, i64, i64, i64, i64]
+        rows3, table = [vp, i64, i64, i64], [i32, i32, vp, i64, i64, i32]
+        lib.dcp_qk_norm_rope_append.restype = i32
+        lib.dcp_qk_norm_rope_append.argtypes = ([i32] * 7 + rows2 * 3 + [vp, vp, f32, vp, i32, i32, i32, vp] + rows2
+                                                + pool * 2 + table + [vp, vp, i32, vp])
+        lib.dcp_extend_attention_workspace_size.restype = ctypes.c_size_t
+        lib.dcp_extend_attention_workspace_size.argtypes = [i32] * 7
+        lib.dcp_extend_attention_paged.restype = i32
+        lib.dcp_extend_attention_paged.argtypes = ([i32] * 7 + rows2 + pool * 2 + table + [vp, vp, i32, f32, i32]
+                                                   + rows3 * 2 + [i32, vp, ctypes.c_size_t, vp])
+        lib.dcp_attention_weights_paged.restype = i32
+        lib.dcp_attention_weights_paged.argtypes = ([i32] * 7 + rows2 + pool + table + [vp, vp, i32, f32] + rows2
+                                                    + [i32] + rows3 + [vp])
+        lib.dcp_cache_evict_paged.restype = i32
+        lib.dcp_cache_evict_paged.argtypes = ([i32] * 5 + pool * 2 + table + [vp, i32] + rows3 + [vp, i32, i32]
+                                              + [vp, i64, i64, i32] + rows3 * 2 + [vp])
         lib.dcp_device_status.restype = i32
         lib.dcp_device_status.argtypes = []
         _lib = lib
@@ -140,6 +158,26 @@ def dcp_decode_attention(*args) -> int:
 
 def dcp_decode_attention_mla(*args) -> int:
     return load().dcp_decode_attention_mla(*args)
+
+
+def dcp_qk_norm_rope_append(*args) -> int:
+    return load().dcp_qk_norm_rope_append(*args)
+
+
+def dcp_extend_attention_workspace_size(N: int, B: int, T: int, H: int, Hkv: int, D: int, max_seq_len: int) -> int:
+    return load().dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, max_seq_len)
+
+
+def dcp_extend_attention_paged(*args) -> int:
+    return load().dcp_extend_attention_paged(*args)
+
+
+def dcp_attention_weights_paged(*args) -> int:
+    return load().dcp_attention_weights_paged(*args)
+
+
+def dcp_cache_evict_paged(*args) -> int:
+    return load().dcp_cache_evict_paged(*args)
 
 
 def dcp_device_status() -> int:
@@ -409,6 +447,275 @@ def decode_attention_mla(q, kv, seq_lens, max_seq_len, o, lse, sm_scale, base="2
                          workspace=None, stream=None) -> None:
     prepare_decode_attention_mla(q, kv, seq_lens, max_seq_len, o, lse, sm_scale, base, split_tokens,
                                  workspace, stream)()
+
+
+# ---------------------------------------------------------------------------
+# chunk serving: append, chunk attention, accumulated weights, eviction
+# ---------------------------------------------------------------------------
+
+class _PreparedOn(_Prepared):
+    """A prepared call whose tensors live on a given device: the call runs with
+    that device current, whichever one is current where it is made."""
+
+    def __init__(self, fn_name: str, device, args: tuple, keep: tuple):
+        super().__init__(fn_name, args, keep)
+        self._device = device.index if device.type == "cuda" else None
+
+    def __call__(self) -> None:
+        if self._device is None or self._device == torch.cuda.current_device():
+            super().__call__()
+        else:
+            with torch.cuda.device(self._device):
+                super().__call__()
+
+
+def _chunk_device(q: torch.Tensor, *ts) -> torch.device:
+    """The device of the operands: `q`'s, which the other CUDA tensors share."""
+    _need_cuda(q, *ts)
+    d = q.device
+    for t in ts:
+        if t is not None and t.device != d and t.is_cuda and q.is_cuda:
+            raise ValueError(f"operands on {d} and {t.device}")
+    return d
+
+
+def _stream_on(device, stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device if device.type == "cuda" else None).cuda_stream
+    return _stream_handle(stream)
+
+
+def _int32(**ts) -> None:
+    for name, t in ts.items():
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != 1:
+            raise ValueError(f"{name} must be a contiguous 1-dim int32 tensor")
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _same_dtype(*ts) -> int:
+    for t in ts:
+        if t is not None and t.dtype != ts[0].dtype:
+            raise ValueError(f"payload tensors of types {ts[0].dtype} and {t.dtype}")
+    return _dtype_code(ts[0])
+
+
+def _pool_args(pages: torch.Tensor, N: int, Hkv: int, D: int, like: torch.Tensor | None = None):
+    if pages.dim() != 5 or pages.shape[0] != N or pages.shape[3] != Hkv or pages.shape[4] != D or (
+            like is not None and pages.shape != like.shape):
+        raise ValueError(f"pages are [N, num_pages, page_size, Hkv, D], here {(N, '..', '..', Hkv, D)}; got "
+                         f"{tuple(pages.shape)}")
+    _inner_ok(pages)
+    s = pages.stride()
+    return (pages.data_ptr(), s[0], s[1], s[2], s[3])
+
+
+def _table_args(table: torch.Tensor, N: int, B: int, name: str = "block_table"):
+    if table.dtype != torch.int32 or table.dim() != 3 or table.shape[0] != N or table.shape[1] != B or (
+            table.shape[2] > 1 and table.stride(2) != 1):
+        raise ValueError(f"{name} is int32 [N, B, max_pages] = [{N}, {B}, ..] with unit stride along the pages")
+    return (table.data_ptr(), table.stride(0), table.stride(1), table.shape[2])
+
+
+def _rows_args(t: torch.Tensor, shape: tuple, name: str, inner: bool = True):
+    """Pointer and the strides of a tensor's leading dimensions."""
+    _shape(t, shape, name)
+    s = t.stride()
+    if inner:
+        if shape[-1] > 1 and s[-1] != 1:
+            raise ValueError("the innermost (D) dimension must have stride 1")
+        s = s[:-1]
+    return (t.data_ptr(), *s)
+
+
+def prepare_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
+                                k_weight: torch.Tensor | None, eps: float, cos_sin: torch.Tensor | None,
+                                positions: torch.Tensor | None, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                block_table: torch.Tensor, query_start: torch.Tensor, seq_lens: torch.Tensor,
+                                max_seq_len: int, q_out: torch.Tensor, interleaved: bool = False,
+                                stream=None) -> _Prepared:
+    """Norm and rotation of the new tokens' queries (into q_out, which may be q)
+    and keys, and the append of keys and values to the round-robin pages.
+
+    q, q_out [T,H,D]; k, v [T,Hkv,D]; q_weight, k_weight [D] or None; cos_sin
+    [num_positions, rot_dim] fp32 (cosines, then sines) with positions [T] int32,
+    or both None; k_pages, v_pages [N,num_pages,page_size,Hkv,D]; block_table
+    [N,B,max_pages] int32; query_start [B+1], seq_lens [B] int32 (lengths with
+    the new tokens)."""
+    dev = _chunk_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
+                        seq_lens, q_out)
+    T, H, D = q.shape
+    Hkv, N, B = k.shape[1], k_pages.shape[0], seq_lens.shape[0]
+    code = _same_dtype(q, k, v, q_weight, k_weight, k_pages, v_pages, q_out)
+    _int32(query_start=query_start, seq_lens=seq_lens)
+    _shape(query_start, (B + 1,), "query_start")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _shape(w, (D,), name)
+            _inner_ok(w)
+    rot = npos = 0
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("cos_sin and positions are given together")
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin is a contiguous fp32 [num_positions, rot_dim] tensor")
+        npos, rot = cos_sin.shape
+        _int32(positions=positions)
+        _shape(positions, (T,), "positions")
+    args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_rows_args(k, (T, Hkv, D), "k"),
+            *_rows_args(v, (T, Hkv, D), "v"),
+            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            float(eps), None if cos_sin is None else cos_sin.data_ptr(), npos, rot, 1 if interleaved else 0,
+            None if positions is None else positions.data_ptr(), *_rows_args(q_out, (T, H, D), "q_out"),
+            *_pool_args(k_pages, N, Hkv, D), *_pool_args(v_pages, N, Hkv, D, k_pages), k_pages.shape[1],
+            k_pages.shape[2], *_table_args(block_table, N, B), query_start.data_ptr(), seq_lens.data_ptr(),
+            int(max_seq_len), _stream_on(dev, stream))
+    return _PreparedOn("dcp_qk_norm_rope_append", dev, args,
+                       (q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
+                        seq_lens, q_out))
+
+
+def qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table,
+                        query_start, seq_lens, max_seq_len, q_out, interleaved=False, stream=None) -> None:
+    prepare_qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table,
+                                query_start, seq_lens, max_seq_len, q_out, interleaved, stream)()
+
+
+def extend_workspace_bytes(N: int, B: int, T: int, H: int, Hkv: int, D: int, max_seq_len: int) -> int:
+    """Bytes of workspace extend_attention_paged needs on the current device."""
+    return dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, max_seq_len)
+
+
+def _scratch(nbytes: int, device, stream):
+    """Device memory for one call on `stream`; the allocator keeps it until that
+    stream has passed the call, also when it is not the current stream."""
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # on another stream than the current one: its earlier work on this memory must not be overtaken
+        if stream != torch.cuda.current_stream(device):
+            stream.wait_stream(torch.cuda.current_stream(device))
+            ws.record_stream(stream)
+    return ws
+
+
+def prepare_extend_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                   block_table: torch.Tensor, query_start: torch.Tensor, seq_lens: torch.Tensor,
+                                   max_seq_len: int, o: torch.Tensor, lse: torch.Tensor, sm_scale: float,
+                                   base: str = "e", causal: bool = True, workspace: torch.Tensor | None = None,
+                                   stream=None) -> _Prepared:
+    """Each rank's attention of the new tokens over its share of the paged caches.
+
+    q [T,H,D]; k_pages, v_pages [N,num_pages,page_size,Hkv,D]; block_table
+    [N,B,max_pages] int32; query_start [B+1], seq_lens [B] int32; o [N,T,H,D],
+    lse [N,T,H] fp32: the partials that lse_combine merges.  `workspace` (uint8,
+    device, extend_workspace_bytes() long) is allocated here when not given."""
+    dev = _chunk_device(q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace)
+    T, H, D = q.shape
+    N, B, Hkv = k_pages.shape[0], seq_lens.shape[0], k_pages.shape[3]
+    code = _same_dtype(q, k_pages, v_pages, o)
+    _int32(query_start=query_start, seq_lens=seq_lens)
+    _shape(query_start, (B + 1,), "query_start")
+    if lse.dtype != torch.float32:
+        raise ValueError("LSE tensors are fp32")
+    rows = (*_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, N, Hkv, D),
+            *_pool_args(v_pages, N, Hkv, D, k_pages), k_pages.shape[1], k_pages.shape[2],
+            *_table_args(block_table, N, B), query_start.data_ptr(), seq_lens.data_ptr(), int(max_seq_len),
+            float(sm_scale), 1 if causal else 0, *_rows_args(o, (N, T, H, D), "o"),
+            *_rows_args(lse, (N, T, H), "lse", inner=False), _base_code(base))
+    if workspace is None:
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                nbytes = extend_workspace_bytes(N, B, T, H, Hkv, D, int(max_seq_len))
+        else:
+            nbytes = extend_workspace_bytes(N, B, T, H, Hkv, D, int(max_seq_len))
+        workspace = _scratch(nbytes, dev if dev.type == "cuda" else torch.device("cuda"), stream)
+    args = (code, N, B, T, H, Hkv, D, *rows, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream_on(dev, stream))
+    return _PreparedOn("dcp_extend_attention_paged", dev, args,
+                       (q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace))
+
+
+def extend_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse, sm_scale,
+                           base="e", causal=True, workspace=None, stream=None) -> None:
+    prepare_extend_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse,
+                                   sm_scale, base, causal, workspace, stream)()
+
+
+def prepare_attention_weights_paged(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor,
+                                    query_start: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                                    lse: torch.Tensor, acc: torch.Tensor, sm_scale: float, base: str = "e",
+                                    stream=None) -> _Prepared:
+    """Adds the new tokens' attention weights to the cached tokens' sums.
+
+    q [T,H,D]; k_pages [N,num_pages,page_size,Hkv,D]; lse [T,H] fp32, the MERGED
+    log-sum-exp (lse_combine's out_lse); acc [N,B,Hkv,cap] fp32, cap >=
+    ceil(max_seq_len / N), updated in place (new tokens' entries start from 0)."""
+    dev = _chunk_device(q, k_pages, block_table, query_start, seq_lens, lse, acc)
+    T, H, D = q.shape
+    N, B, Hkv = k_pages.shape[0], seq_lens.shape[0], k_pages.shape[3]
+    code = _same_dtype(q, k_pages)
+    _int32(query_start=query_start, seq_lens=seq_lens)
+    _shape(query_start, (B + 1,), "query_start")
+    if lse.dtype != torch.float32 or acc.dtype != torch.float32:
+        raise ValueError("LSE and weight tensors are fp32")
+    if acc.dim() != 4 or acc.shape[3] * N < int(max_seq_len):
+        raise ValueError("acc is [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
+    args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, N, Hkv, D),
+            k_pages.shape[1], k_pages.shape[2], *_table_args(block_table, N, B), query_start.data_ptr(),
+            seq_lens.data_ptr(), int(max_seq_len), float(sm_scale), *_rows_args(lse, (T, H), "lse", inner=False),
+            _base_code(base), *_rows_args(acc, (N, B, Hkv, acc.shape[3]), "acc"), _stream_on(dev, stream))
+    return _PreparedOn("dcp_attention_weights_paged", dev, args,
+                       (q, k_pages, block_table, query_start, seq_lens, lse, acc))
+
+
+def attention_weights_paged(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale,
+                            base="e", stream=None) -> None:
+    prepare_attention_weights_paged(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale,
+                                    base, stream)()
+
+
+def prepare_cache_evict_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                              seq_lens: torch.Tensor, max_seq_len: int, acc: torch.Tensor, keep_lens: torch.Tensor,
+                              max_keep: int, recent: int, dst_table: torch.Tensor, kept: torch.Tensor,
+                              acc_out: torch.Tensor, stream=None) -> _Prepared:
+    """Keeps the most attended tokens of every request (and its last `recent`
+    ones) and copies their rows, in order, to the pages of dst_table.
+
+    acc [N,B,Hkv,cap] fp32; keep_lens [B] int32 (new global lengths, negative:
+    leave the request alone), at most max_keep; dst_table [N,B,pages] int32;
+    kept int32 and acc_out fp32 [N,B,Hkv,kcap], kcap >= ceil(max_keep / N): the
+    kept tokens' old local indices and their weights."""
+    dev = _chunk_device(k_pages, v_pages, block_table, seq_lens, acc, keep_lens, dst_table, kept, acc_out)
+    N, _, _, Hkv, D = k_pages.shape
+    B = seq_lens.shape[0]
+    code = _same_dtype(k_pages, v_pages)
+    _int32(seq_lens=seq_lens, keep_lens=keep_lens)
+    _shape(keep_lens, (B,), "keep_lens")
+    if acc.dtype != torch.float32 or acc_out.dtype != torch.float32 or kept.dtype != torch.int32:
+        raise ValueError("acc and acc_out are fp32, kept is int32")
+    if acc.dim() != 4 or acc.shape[3] * N < int(max_seq_len):
+        raise ValueError("acc is [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
+    if kept.dim() != 4 or kept.shape[3] * N < min(int(max_keep), int(max_seq_len)):
+        raise ValueError("kept and acc_out are [N, B, Hkv, kcap] with kcap >= ceil(max_keep / N)")
+    args = (code, N, B, Hkv, D, *_pool_args(k_pages, N, Hkv, D), *_pool_args(v_pages, N, Hkv, D, k_pages),
+            k_pages.shape[1], k_pages.shape[2], *_table_args(block_table, N, B), seq_lens.data_ptr(),
+            int(max_seq_len), *_rows_args(acc, (N, B, Hkv, acc.shape[3]), "acc"), keep_lens.data_ptr(),
+            int(max_keep), int(recent), *_table_args(dst_table, N, B, "dst_table"),
+            *_rows_args(kept, (N, B, Hkv, kept.shape[3]), "kept"),
+            *_rows_args(acc_out, (N, B, Hkv, kept.shape[3]), "acc_out"), _stream_on(dev, stream))
+    return _PreparedOn("dcp_cache_evict_paged", dev, args,
+                       (k_pages, v_pages, block_table, seq_lens, acc, keep_lens, dst_table, kept, acc_out))
+
+
+def cache_evict_paged(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
+                      dst_table, kept, acc_out, stream=None) -> None:
+    prepare_cache_evict_paged(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
+                              dst_table, kept, acc_out, stream)()
 
 
 def device_status() -> int:

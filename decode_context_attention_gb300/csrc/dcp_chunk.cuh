@@ -1,0 +1,135 @@
+// dcp_chunk.cuh -- device helpers of the chunk kernels (append, chunk
+// attention, accumulated weights, eviction): a ragged batch's requests, the
+// round-robin share of a rank, rows of the paged caches, and the split of a
+// ragged batch's attention over the CTAs.
+#pragma once
+
+#include <math.h>
+
+#include "dcp_device.cuh"
+
+namespace dcp {
+
+// Rank r's share of the first n tokens of a request (sglang PR #33926 report,
+// "关键源码片段", `get_dcp_lens`).
+__device__ __forceinline__ int rank_share(int n, int r, int N) { return n <= 0 ? 0 : n / N + (r < n % N ? 1 : 0); }
+
+struct Request {
+    int start, n, L;  // first row, new tokens, tokens in all
+};
+
+// Whatever query_start and seq_lens hold, rows stay in [0, T) and lengths in
+// [0, max_seq_len].
+__device__ __forceinline__ Request load_request(const ChunkParams& p, int b) {
+    const int s = min(max(__ldg(p.query_start + b), 0), p.T);
+    const int e = min(max(__ldg(p.query_start + b + 1), s), p.T);
+    const int L = min(max(__ldg(p.seq_lens + b), 0), p.max_seq_len);
+    return {s, e - s, L};
+}
+
+// Local tokens of rank r that new token j of the request sees.
+__device__ __forceinline__ int visible(const ChunkParams& p, const Request& q, int j, int r) {
+    return rank_share(p.causal ? q.L - q.n + j + 1 : q.L, r, p.N);
+}
+
+// Page of local token i, or -1 when the table names none of the pool's.
+__device__ __forceinline__ int page_of(const ChunkParams& p, int r, int b, int i) {
+    const int pg = __ldg(p.bt + (int64_t)r * p.bt_sn + (int64_t)b * p.bt_sb + (i >> p.page_shift));
+    return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
+}
+__device__ __forceinline__ int64_t k_offset(const ChunkParams& p, int r, int pg, int i, int hkv) {
+    return (int64_t)r * p.k_sn + (int64_t)pg * p.k_sp + (int64_t)(i & ((1 << p.page_shift) - 1)) * p.k_st +
+           (int64_t)hkv * p.k_sh;
+}
+__device__ __forceinline__ int64_t v_offset(const ChunkParams& p, int r, int pg, int i, int hkv) {
+    return (int64_t)r * p.v_sn + (int64_t)pg * p.v_sp + (int64_t)(i & ((1 << p.page_shift) - 1)) * p.v_st +
+           (int64_t)hkv * p.v_sh;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^x by ex2.approx (at most 2 ulp off; 2^-inf = 0): the exponentials of a
+// softmax, whose argument already carries a larger rounding error.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------------------
+// The split of a ragged batch's attention.  An item is (request, rank, KV head,
+// block of `tpi` new tokens); its work is the tiles of `tt` cached tokens its
+// rows see, plus a fixed part.  The items' total is cut into `ctas` equal
+// ranges: a range starts and ends inside items, so every CTA has the same work
+// whatever the mix of long and short requests, and a single request with a
+// long cache is split over all of them.  Items that are cut leave partial
+// results, at most two per CTA, that a merge joins.
+// ---------------------------------------------------------------------------
+struct ChunkPos {
+    int b, rh, qt, tile;  // request, rank * Hkv + KV head, block of new tokens, first tile; b = B at the end
+};
+__device__ __forceinline__ bool same_item(const ChunkPos& x, const ChunkPos& y) {
+    return x.b == y.b && x.rh == y.rh && x.qt == y.qt;
+}
+
+// Tiles that block qt of the request sees on rank r.
+__device__ __forceinline__ int item_tiles(const ChunkParams& p, const Request& q, int r, int qt, int tpi, int tt) {
+    const int last = min((qt + 1) * tpi, q.n) - 1;
+    return (visible(p, q, last, r) + tt - 1) / tt;
+}
+
+// The first position of the item after `x`.
+__device__ __forceinline__ ChunkPos next_item(const ChunkParams& p, const ChunkPos& x, int tpi) {
+    ChunkPos y = x;
+    y.tile = 0;
+    if (++y.qt * tpi < load_request(p, y.b).n) return y;
+    y.qt = 0;
+    if (++y.rh < p.N * p.Hkv) return y;
+    y.rh = 0;
+    do ++y.b;
+    while (y.b < p.B && load_request(p, y.b).n == 0);
+    return y;
+}
+
+// Where the partials of cut items and the ranges lie in the workspace.
+struct ChunkPartials {
+    ChunkPos* pos;  // [ctas + 1]
+    float* o;       // [2 * ctas][rows][D]
+    float* lse;     // [2 * ctas][rows], base 2
+};
+size_t chunk_partials_bytes(int ctas, int rows, int D);
+ChunkPartials chunk_partials_in(unsigned char* ws, int ctas, int rows, int D);
+// Fills pos; joins the cut items (rows of an item: tpi tokens x gq heads, at most `rows`).
+cudaError_t launch_chunk_plan(const ChunkParams& p, const ChunkPartials& ws, int tpi, int tt, int ctas,
+                              cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
+                               cudaStream_t stream);
+
+// Adds what the tokens set in `mask` (local tokens tile0 + bit, tokens whose V row
+// holds NaN or infinities and was zeroed for the product) give to a row that
+// sees them (i < lim): out[d] += p_i v_i[d] for the elements that are not
+// finite.  lse2 is the row's base-2 log-sum-exp.  One thread, a rare path.
+template <typename T, typename O>
+__device__ __noinline__ void add_nonfinite(const ChunkParams& p, int r, int b, int hkv, const T* q, int tile0,
+                                           const unsigned* mask, int words, int lim, float lse2, O* out) {
+    for (int w = 0; w < words; ++w) {
+        for (unsigned m = mask[w]; m; m &= m - 1) {
+            const int i = tile0 + 32 * w + __ffs(m) - 1;
+            if (i >= lim) return;
+            const int pg = page_of(p, r, b, i);
+            if (pg < 0) continue;
+            const T* k = reinterpret_cast<const T*>(p.k + k_offset(p, r, pg, i, hkv));
+            const T* v = reinterpret_cast<const T*>(p.v + v_offset(p, r, pg, i, hkv));
+            float s = 0.f;
+            for (int d = 0; d < p.D; ++d) s = fmaf(to_f32(q[d]), to_f32(k[d]), s);
+            const float pr = exp2f(s * p.sm_scale * kLog2e - lse2);
+            for (int d = 0; d < p.D; ++d) {
+                const float x = to_f32(v[d]);
+                if (!isfinite(x)) out[d] = from_f32<O>(to_f32(out[d]) + pr * x);
+            }
+        }
+    }
+}
+
+}  // namespace dcp

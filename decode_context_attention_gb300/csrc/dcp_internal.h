@@ -108,6 +108,69 @@ struct MlaParams {
     int stall_loads;                     // test of the bounded waits: the loads are never issued
 };
 
+// New tokens of a ragged batch and the paged round-robin caches they belong to:
+// request b owns token rows [query_start[b], query_start[b + 1]), the last of
+// its seq_lens[b] tokens; token g of a request lives on rank g % N as local
+// token g / N, in slot (g / N) % page_size of page bt[r][b][(g / N) / page_size].
+struct ChunkParams {
+    int N, B, T, H, Hkv, D, gq;          // gq = H / Hkv
+    int max_seq_len;
+    int page_shift, num_pages;
+    int causal;                          // row j sees the tokens up to itself, else all of its request
+    int base2;                           // LSE base: 0 = e, 1 = 2
+    float sm_scale;
+    const int* query_start;              // [B + 1]
+    const int* seq_lens;                 // [B]
+    const int* bt;
+    int64_t bt_sn, bt_sb;                // int32 elements
+    const unsigned char* q;
+    int64_t q_st, q_sh;                  // bytes
+    unsigned char* k;
+    int64_t k_sn, k_sp, k_st, k_sh;      // bytes
+    unsigned char* v;
+    int64_t v_sn, v_sp, v_st, v_sh;      // bytes
+    // attention: partials and their LSE
+    unsigned char* o;
+    int64_t o_sn, o_st, o_sh;            // bytes
+    float* lse;
+    int64_t l_sn, l_st, l_sh;            // fp32 words
+    unsigned char* ws;                   // schedule and split partials
+    // accumulated weights (lse is then the merged one, l_sn unused)
+    float* acc;
+    int64_t a_sn, a_sb, a_sh;            // fp32 words
+    int stall_loads;                     // test of the bounded waits (tensor-core paths): no loads issued
+};
+
+struct AppendParams {
+    ChunkParams c;                       // q, the pages and the batch
+    int rot, interleaved, num_positions;
+    float eps;
+    int groups_per_token;                // lane groups that share a token's rows
+    const unsigned char* kn;             // new keys and values
+    int64_t kn_st, kn_sh;                // bytes
+    const unsigned char* vn;
+    int64_t vn_st, vn_sh;
+    unsigned char* qo;
+    int64_t qo_st, qo_sh;
+    const unsigned char* qw;             // norm weights (NULL: no norm)
+    const unsigned char* kw;
+    const float* cos_sin;                // [num_positions][rot]: cosines, then sines
+    const int* positions;                // [T]
+};
+
+struct EvictParams {
+    ChunkParams c;                       // the pages and lengths; c.acc is read
+    int row_bytes;
+    int max_keep, recent;
+    const int* keep_lens;                // [B]
+    const int* dt;                       // destination page table
+    int64_t dt_sn, dt_sb;
+    int* kept;
+    int64_t kp_sn, kp_sb, kp_sh;
+    float* acc_out;
+    int64_t ao_sn, ao_sb, ao_sh;
+};
+
 // Records `msg` as this host thread's dcp_last_error_message() and returns s.
 dcp_status_t set_error(dcp_status_t s, const char* msg);
 
@@ -134,6 +197,13 @@ cudaError_t launch_combine_f32(const CombineParams& p, int vb, cudaStream_t stre
 cudaError_t launch_combine_f16(const CombineParams& p, int vb, cudaStream_t stream);
 cudaError_t launch_combine_bf16(const CombineParams& p, int vb, cudaStream_t stream);
 cudaError_t launch_combine_fp8(const CombineParams& p, int vb, cudaStream_t stream);
+
+cudaError_t launch_append(const AppendParams& p, int dtype, cudaStream_t stream);
+// Attention of a chunk of new tokens: bytes of workspace the kernels want, and the launch.
+size_t chunk_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len);
+cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();

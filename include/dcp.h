@@ -18,6 +18,11 @@
  *                       cores; dcp_decode_attention_mla: over an absorbed-MLA
  *                       latent cache, on the tcgen05 tensor cores).
  *
+ * and the steps around it when a request brings more than one new token:
+ *
+ *   dcp_qk_norm_rope_append, dcp_extend_attention_paged,
+ *   dcp_attention_weights_paged, dcp_cache_evict_paged
+ *
  * The cross-rank exchange itself (NCCL all-to-all, MNNVL, all-gather /
  * all-reduce) is not part of this library.  A group's N ranks can be held as
  * one stacked tensor on one device; the "received" views then address the
@@ -385,6 +390,181 @@ dcp_status_t dcp_decode_attention_mla(int dtype, int N, int B, int H, int Dk, in
                                       void* o, int64_t o_sn, int64_t o_sb, int64_t o_sh,
                                       float* lse, int64_t l_sn, int64_t l_sb, int64_t l_sh,
                                       int lse_base, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The chunk-serving entry points: what fills the paged caches that
+ * dcp_decode_attention_paged reads, attends them with more than one new token
+ * per request, and keeps a long cache within a budget.
+ *
+ * All of them share one description of a ragged batch over the caches:
+ *   query_start [B + 1] int32 (device)  request b owns token rows t in
+ *               [query_start[b], query_start[b + 1]) of the [T, ...] operands;
+ *               query_start[0] = 0, non-decreasing; a request may own none;
+ *               rows t >= query_start[B] belong to no request and are neither
+ *               read nor written (padding of a fixed-size batch).
+ *   seq_lens [B] int32 (device)  tokens of each request in the caches WITH its
+ *               new tokens: row j of request b is the token of global index
+ *               g = seq_lens[b] - Q_b + j, Q_b = query_start[b+1] - query_start[b].
+ *               Values above max_seq_len count as max_seq_len.
+ *   block_table, pages  as for dcp_decode_attention_paged: token g lives on
+ *               rank g % N as local token i = g / N, in slot i % page_size of
+ *               page block_table[r][b][i / page_size].  max_pages must cover
+ *               ceil(ceil(max_seq_len / N) / page_size) entries; only entries of
+ *               tokens that exist are read.  Rows start on 16-byte
+ *               boundaries; page_size a power of two up to 65536.
+ * With L_r(n) = n / N + (r < n % N) the rank-local share of n tokens.
+ */
+
+/*
+ * dcp_qk_norm_rope_append -- RMS norm of every query and key head, rotation by
+ * position, and the append of the new keys and values to the round-robin pages,
+ * in one pass.  (sglang PR #33926 report, "实现拆解" item 1: the KV cache of a
+ * DCP rank holds the tokens t with t % N == r; the norm and rotation in front
+ * of the append are this library's.)
+ *
+ * For each token row t of request b, x a head row of q or k, w its norm weight:
+ *     y = x * w / sqrt(mean_d x_d^2 + eps)              (w NULL: y = x)
+ *     y[0:rot_dim] rotated in pairs by the row cos_sin[positions[t]]: the
+ *       pairs are (d, d + rot_dim/2), or (2d, 2d + 1) when interleaved != 0;
+ *       (a, b) -> (a cos - b sin, b cos + a sin)
+ *     q_out[t, h] = y of q;  K page slot of token g = y of k;  V page slot = v
+ * computed in fp32 and rounded once (v is a bit copy).
+ *
+ *   q [T, H, D], k, v [T, Hkv, D]  strides (token, head); q_out the same shape
+ *                  and may be q itself (same pointer and strides)
+ *   q_weight, k_weight [D] payload type, or NULL for no norm
+ *   cos_sin [num_positions, rot_dim] fp32: rot_dim/2 cosines, then as many sines
+ *                  (NULL when rot_dim == 0)
+ *   positions [T] int32 (device; unused when rot_dim == 0).  A token whose
+ *                  position is outside [0, num_positions) is skipped: nothing is
+ *                  written for it.
+ * A token whose page index is outside [0, num_pages), or whose global index is
+ * negative, gets its q_out row but no cache entry.  Two tokens that share a
+ * slot (a page twice in the table) leave it unspecified which one is kept.
+ *
+ * dtype DCP_F16 or DCP_BF16; D and rot_dim multiples of 16, D <= 512, rot_dim <=
+ * D; every row starts on a 16-byte boundary.
+ */
+dcp_status_t dcp_qk_norm_rope_append(int dtype, int N, int B, int T, int H, int Hkv, int D,
+                                     const void* q, int64_t q_st, int64_t q_sh,
+                                     const void* k, int64_t k_st, int64_t k_sh,
+                                     const void* v, int64_t v_st, int64_t v_sh,
+                                     const void* q_weight, const void* k_weight, float eps,
+                                     const float* cos_sin, int num_positions, int rot_dim, int interleaved,
+                                     const int* positions,
+                                     void* q_out, int64_t qo_st, int64_t qo_sh,
+                                     void* k_pages, int64_t kp_sn, int64_t kp_sp, int64_t kp_st, int64_t kp_sh,
+                                     void* v_pages, int64_t vp_sn, int64_t vp_sp, int64_t vp_st, int64_t vp_sh,
+                                     int num_pages, int page_size,
+                                     const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                                     const int* query_start, const int* seq_lens, int max_seq_len, void* stream);
+
+/*
+ * dcp_extend_attention_paged -- each DCP rank's attention of the new tokens of
+ * a ragged batch over its share of the paged caches (which already hold the new
+ * tokens), producing the partials that dcp_lse_combine merges with B = T.
+ * (sglang PR #34213 report, "功能与动机": the cached-extend merge, whose partials
+ * come from an extend over each rank's slice of the cache; `get_dcp_lens`
+ * gives each new token's rank-local length.)
+ *
+ * For rank r, new token t = (b, j), query head h, s_i = sm_scale <q[t, h], k_i>
+ * over the rank's tokens i < L_r(g + 1) (causal) or i < L_r(seq_lens[b]) (not):
+ *     lse[r, t, h] = log sum_i exp(s_i)             (base e, or divided by ln 2)
+ *     o  [r, t, h] = sum_i exp(s_i - lse) v_i        (0 and -inf when no i is visible)
+ * Keys and values of tokens a row does not see never reach it, whatever they
+ * hold (NaN and infinities included).
+ *
+ *   q [T, H, D] strides (q_st, q_sh); o [N, T, H, D]; lse [N, T, H] fp32
+ * dtype DCP_F16 or DCP_BF16; D in {64, 128, 256}; 1 <= H / Hkv <= 64.  Page
+ * indices outside [0, num_pages) read as zero rows.  Probabilities enter the
+ * value product rounded to the payload type; scores, sums and outputs
+ * accumulate in fp32.  `workspace` (device, 16-byte aligned) of at least
+ * dcp_extend_attention_workspace_size(...) bytes for the current device; calls
+ * that may run at the same time need workspaces of their own, and so do graphs
+ * that may be replayed at the same time.  Waits in the tensor-core kernel are
+ * bounded (dcp_device_status()).
+ */
+size_t dcp_extend_attention_workspace_size(int N, int B, int T, int H, int Hkv, int D, int max_seq_len);
+
+dcp_status_t dcp_extend_attention_paged(int dtype, int N, int B, int T, int H, int Hkv, int D,
+                                        const void* q, int64_t q_st, int64_t q_sh,
+                                        const void* k_pages, int64_t k_sn, int64_t k_sp, int64_t k_st, int64_t k_sh,
+                                        const void* v_pages, int64_t v_sn, int64_t v_sp, int64_t v_st, int64_t v_sh,
+                                        int num_pages, int page_size,
+                                        const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                                        const int* query_start, const int* seq_lens, int max_seq_len,
+                                        float sm_scale, int causal,
+                                        void* o, int64_t o_sn, int64_t o_st, int64_t o_sh,
+                                        float* lse, int64_t l_sn, int64_t l_st, int64_t l_sh,
+                                        int lse_base, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dcp_attention_weights_paged -- adds the attention weights that the new tokens
+ * give to every cached token, the statistic an eviction goes by.  The weights
+ * are those of the whole softmax over all ranks: `lse` is the MERGED
+ * log-sum-exp (dcp_lse_combine's out_lse over the N partials).  The pages have
+ * no counterpart; the rank-local share and the causal rule are those of
+ * dcp_extend_attention_paged.
+ *
+ * For rank r, request b with Q_b > 0, KV head kh and local token i < L_r(seq_lens[b]):
+ *     acc[r, b, kh, i] = (i*N + r < seq_lens[b] - Q_b ? acc[r, b, kh, i] : 0)
+ *                        + sum over new tokens j that see i (i*N + r <= g) and the
+ *                          query heads h of kh of exp(s - lse[t, h])
+ * so the new tokens' own entries start from zero.  Rows whose lse is not
+ * finite add nothing.  Entries i >= L_r(seq_lens[b]) and requests without new
+ * tokens are left as they are.  Sums are fp32 in a fixed order: equal calls
+ * give equal bits.
+ *
+ *   lse [T, H] fp32 strides (l_st, l_sh), base lse_base
+ *   acc [N, B, Hkv, >= ceil(max_seq_len / N)] fp32 strides (a_sn, a_sb, a_sh), tokens contiguous
+ * Types, heads and pages as for dcp_extend_attention_paged; no workspace.
+ */
+dcp_status_t dcp_attention_weights_paged(int dtype, int N, int B, int T, int H, int Hkv, int D,
+                                         const void* q, int64_t q_st, int64_t q_sh,
+                                         const void* k_pages, int64_t k_sn, int64_t k_sp, int64_t k_st, int64_t k_sh,
+                                         int num_pages, int page_size,
+                                         const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                                         const int* query_start, const int* seq_lens, int max_seq_len,
+                                         float sm_scale,
+                                         const float* lse, int64_t l_st, int64_t l_sh, int lse_base,
+                                         float* acc, int64_t a_sn, int64_t a_sb, int64_t a_sh, void* stream);
+
+/*
+ * dcp_cache_evict_paged -- keeps the most attended tokens of every request and
+ * moves them to new pages.  (The pages have no counterpart.)
+ *
+ * Request b shrinks to min(seq_lens[b], keep_lens[b], max_keep) tokens, so rank r
+ * keeps K = L_r of that for every KV head on its own: first the tokens of
+ * global index >= seq_lens[b] - recent (the latest K of them if there are
+ * more), then the older ones by acc, larger first, equal values by the lower
+ * index, NaN after everything else.  The kept tokens stay in order: slot n of
+ * the result is the n-th kept token.  For n < K
+ *     kept[r, b, kh, n] = its local index,  acc_out[r, b, kh, n] = its acc,
+ * and its K and V head rows are copied to slot n % page_size of page
+ * dst_table[r][b][n / page_size] of the same pools.  Afterwards the caller uses
+ * dst_table with the new lengths min(seq_lens[b], keep_lens[b], max_keep).
+ * keep_lens[b] < 0 leaves request b alone (nothing is read or written).
+ * The pages of dst_table that are written must not be pages that the call reads.
+ * A source page outside [0, num_pages) reads as zero rows; a destination page
+ * outside it is not written.
+ *
+ *   acc     [N, B, Hkv, >= ceil(max_seq_len / N)] fp32 strides (a_sn, a_sb, a_sh)
+ *   keep_lens [B] int32 (device); kept int32 and acc_out fp32
+ *           [N, B, Hkv, >= ceil(max_keep / N)] strides (.._sn, .._sb, .._sh)
+ *   dst_table [N][B, dst_max_pages] int32, dst_max_pages covering ceil(max_keep / N) tokens
+ * dtype DCP_F16 or DCP_BF16, D a multiple of 8 up to 1024.
+ */
+dcp_status_t dcp_cache_evict_paged(int dtype, int N, int B, int Hkv, int D,
+                                   void* k_pages, int64_t k_sn, int64_t k_sp, int64_t k_st, int64_t k_sh,
+                                   void* v_pages, int64_t v_sn, int64_t v_sp, int64_t v_st, int64_t v_sh,
+                                   int num_pages, int page_size,
+                                   const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                                   const int* seq_lens, int max_seq_len,
+                                   const float* acc, int64_t a_sn, int64_t a_sb, int64_t a_sh,
+                                   const int* keep_lens, int max_keep, int recent,
+                                   const int* dst_table, int64_t dt_sn, int64_t dt_sb, int dst_max_pages,
+                                   int* kept, int64_t kp_sn, int64_t kp_sb, int64_t kp_sh,
+                                   float* acc_out, int64_t ao_sn, int64_t ao_sb, int64_t ao_sh, void* stream);
 
 /*
  * dcp_device_status -- DCP_OK, or DCP_ERR_TIMEOUT when a tensor-core kernel
