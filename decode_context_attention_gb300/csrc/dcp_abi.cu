@@ -611,7 +611,8 @@ dcp_status_t dcp_decode_attention_mla(int dtype, int N, int B, int H, int Dk, in
 dcp_status_t dcp_device_status(void) {
     const int s_mla = dcp::mla_device_status(true);
     const int s_gqa = dcp::attn_tc_device_status(true);
-    const int s = s_mla < 0 || s_gqa < 0 ? -1 : (s_mla ? s_mla : s_gqa);
+    const int s_chunk = dcp::chunk_attention_tc_status(true);
+    const int s = s_mla < 0 || s_gqa < 0 || s_chunk < 0 ? -1 : (s_mla ? s_mla : (s_gqa ? s_gqa : s_chunk));
     if (s < 0) return fail(DCP_ERR_CUDA, "dcp_device_status: the device status word could not be read");
     if (s) return fail((dcp_status_t)s, "dcp_device_status: a tensor-core kernel gave up on a bounded wait");
     return ok();

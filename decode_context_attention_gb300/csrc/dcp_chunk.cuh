@@ -92,6 +92,36 @@ __device__ __forceinline__ ChunkPos next_item(const ChunkParams& p, const ChunkP
     return y;
 }
 
+// A CTA's part of an item.
+struct ChunkSeg {
+    int b, r, hkv;
+    int row0, nrows;     // first token row, rows (token, head) of the item
+    int j0;              // first new token of the item within its request
+    int t0, t1;          // tiles [t0, t1) of its ntiles
+    int lim0, lim_last;  // tokens its first and its last row see: the tiles from lim0 / tt on are masked
+    int slot;            // where a partial result goes, -1 when the part is the whole item
+    Request q;
+};
+__device__ __forceinline__ ChunkSeg load_seg(const ChunkParams& p, const ChunkPos& x, const ChunkPos& first,
+                                             const ChunkPos& end, int tpi, int tt) {
+    ChunkSeg s;
+    s.b = x.b;
+    s.r = x.rh / p.Hkv;
+    s.hkv = x.rh - s.r * p.Hkv;
+    s.q = load_request(p, x.b);
+    s.j0 = x.qt * tpi;
+    const int tokens = min(tpi, s.q.n - s.j0);
+    s.row0 = s.q.start + s.j0;
+    s.nrows = tokens * p.gq;
+    s.lim0 = visible(p, s.q, s.j0, s.r);
+    s.lim_last = visible(p, s.q, s.j0 + tokens - 1, s.r);
+    const int ntiles = (s.lim_last + tt - 1) / tt;
+    s.t0 = x.tile;
+    s.t1 = same_item(x, end) ? end.tile : ntiles;
+    s.slot = s.t0 == 0 && s.t1 == ntiles ? -1 : 2 * (int)blockIdx.x + (same_item(x, first) ? 0 : 1);
+    return s;
+}
+
 // Where the partials of cut items and the ranges lie in the workspace.
 struct ChunkPartials {
     ChunkPos* pos;  // [ctas + 1]

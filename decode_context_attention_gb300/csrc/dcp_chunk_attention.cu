@@ -274,10 +274,13 @@ cudaError_t launch_mma_d(const ChunkParams& p, int dtype, cudaStream_t stream) {
 }  // namespace
 
 size_t chunk_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len) {
-    return chunk_partials_bytes(mma_ctas(D), kRows, D);
+    const size_t mma = chunk_partials_bytes(mma_ctas(D), kRows, D), tc = chunk_attention_tc_workspace(D);
+    return mma > tc ? mma : tc;
 }
 
 cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t stream) {
+    cudaError_t e;
+    if (launch_chunk_attention_tc(p, dtype, stream, &e)) return e;
     return dtype == DCP_F16 ? launch_mma_d<__half>(p, dtype, stream) : launch_mma_d<__nv_bfloat16>(p, dtype, stream);
 }
 

@@ -1,0 +1,764 @@
+// dcp_chunk_attention_tc.cu -- attention of a ragged batch's new tokens over every
+// rank's paged cache on the 5th-generation tensor cores: D = 64 or 128, pages
+// of at least 8 tokens.
+//
+// The mathematics is dcp_chunk_attention.cu's: rows (new token, query head of
+// the group) over the tiles of 128 tokens they see, one pass, an online softmax
+// in base 2.  Per tile and 128 rows two products of 128 x 128 x D:
+//     S = Q K^T into tensor memory;  P = 2^(S - m) back into S's columns as 16-bit
+//     pairs;  O += P V with P the A operand from tensor memory, V read MN-major.
+//
+// One persistent CTA per SM (the ranges of dcp_chunk.cuh), two stages of 128
+// rows, each with its own S / P (128 columns) and O (D columns), so that the
+// tensor core works on one stage while the other's exponentials run:
+//   * an item of more than 128 rows is a pair of row blocks that share every K and
+//     V tile (half the loads of one block alone);
+//   * an item of up to 128 rows (single new tokens, drafts) takes alternate tiles
+//     to the two stages, whose results are joined at the end: the loads of a
+//     long cache then stream without waiting for a tile's softmax.
+// Warps 0-3 and 4-7: the softmax of stage 0 and 1, a thread a row, so maxima and
+// sums need no exchange.  Warp 8: TMA (Q and the K / V tiles into a ring, a box
+// per page).  Warp 9: one thread issues the MMAs.  Warp 10: masked tiles: V rows
+// past the last visible token are zeroed, and values that are not finite (0
+// times infinity would reach rows that must not see them; they are added to
+// the rows that do see them at the end).
+// The reference maximum moves only when a row's maximum grows by more than 2^8,
+// so O is rarely rescaled; P then reaches 2^8, which a 16-bit type holds and
+// fp32 sums do too.  P is rounded to the payload type, half a step per term;
+// the row sums use it unrounded.
+// Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
+#include <cuda.h>
+#include <math.h>
+#include <stdlib.h>
+
+#include <type_traits>
+
+#include "dcp_chunk.cuh"
+#include "dcp_mma.cuh"
+#include "dcp_sm100.cuh"
+
+namespace dcp {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kTT = 128;        // tokens of a tile
+constexpr int kM = 128;         // rows of a stage
+constexpr int kThreadsTc = 384;
+constexpr int kChunkB = 128 * 128;  // 64 columns of 128 rows
+constexpr int kMisc = 2048;
+constexpr float kGrow = 8.f;
+// 2^(s qscale - m) takes one fused step, exact but for one rounding; m itself is
+// rounded, which moves a row's weights all alike and its log-sum-exp back, and
+// is harmless while m's rounding error (2^-24 |m|) is small.  Beyond this the
+// difference of the scores is taken first.
+constexpr float kFar = 65536.f;
+constexpr unsigned kAllLanes = 0xffffffffu;
+constexpr uint32_t kColO = 256;
+constexpr uint32_t kCols = 512;
+constexpr int kPoison = 8;      // per-item records of tokens with non-finite values
+
+__device__ int g_chunk_status;  // first bounded wait that ran out (0 if none)
+
+template <int D>
+struct TcShape {
+    static constexpr int kTileBytes = (D / 64) * kChunkB;
+    // a ring of 5 tiles of 32 KB or 8 of 16 KB beside two Q blocks
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr int kSmem = (2 + kSlots) * kTileBytes + kMisc + 1024;
+};
+
+struct TcBars {
+    uint64_t full[8], empty[8];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t v_clean[8];      // by ring slot: the masked tile in it is clean
+    uint64_t x_full, x_done;  // an item of one row block: stage 1's sums written, its O read
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+    int issued;               // ring positions whose loads are under way
+    unsigned poison[kPoison][16];  // 4 masked tiles of 128 tokens
+    float xm[kM], xl[kM];
+};
+static_assert(sizeof(TcBars) <= kMisc, "misc region too small");
+
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ void add2(unsigned long long& a, unsigned long long b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Columns from `seen` on are not visible.
+__device__ __forceinline__ void mask_cols(uint32_t (&v)[32], int seen) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (c >= seen) v[c] = 0xff800000u;
+}
+__device__ __forceinline__ void sub_cols(uint32_t (&v)[32], float x) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) - x);
+}
+__device__ __forceinline__ void row_max(const uint32_t (&v)[32], float& m0, float& m1) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        m0 = max3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+        m1 = max3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+    }
+}
+// P of 32 scores, 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
+template <typename T>
+__device__ __forceinline__ void exp_store(const uint32_t (&v)[32], uint32_t tP, unsigned long long qs2,
+                                          unsigned long long off2, unsigned long long& l2) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 f = unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), qs2, off2));
+        const float2 pr = make_float2(exp2_fast(f.x), exp2_fast(f.y));
+        add2(l2, pack2f(pr.x, pr.y));
+        w[e] = f32_to_pair(pr, T());
+    }
+    tmem_st16(tP, w);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    chunk_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                              const __grid_constant__ CUtensorMap vmap, const ChunkParams p, const ChunkPartials ws,
+                              const int tpi) {
+    using S = TcShape<D>;
+    constexpr int kSlots = S::kSlots, kTileBytes = S::kTileBytes;
+    constexpr int NCH = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = smem + 2 * kTileBytes;
+    TcBars* bar = reinterpret_cast<TcBars*>(ring + kSlots * kTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tj = tpi / 2;        // new tokens of a row block
+    const int rblk = tj * p.gq;    // its rows (at most 128)
+
+    if (tid == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+            mbar_init(&bar->v_clean[s], 1);
+        }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(&bar->q_full[u], 1);
+            mbar_init(&bar->q_empty[u], 1);
+            mbar_init(&bar->s_full[u], 1);
+            mbar_init(&bar->p_full[u], 4);
+            mbar_init(&bar->pv_done[u], 1);
+        }
+        mbar_init(&bar->x_full, 4);
+        mbar_init(&bar->x_done, 4);
+        mbar_init(&bar->mma_done, 1);
+        bar->abort = 0;
+        bar->issued = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&bar->tmem_base, kCols);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&qmap);
+        tma_prefetch_map(&kmap);
+        tma_prefetch_map(&vmap);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+    volatile int* abort = &bar->abort;
+    int* status = &g_chunk_status;
+    const ChunkPos first = ws.pos[blockIdx.x];
+    const ChunkPos end = ws.pos[blockIdx.x + 1];
+    ChunkPos x = first;
+    auto more = [&]() { return x.b < p.B && !(same_item(x, end) && x.tile == end.tile); };
+    auto advance = [&]() -> bool {  // false behind the last part
+        if (same_item(x, end)) return false;
+        x = next_item(p, x, tpi);
+        return true;
+    };
+    bool issued_any = false;
+
+    if (warp >= 8) {
+        regs_dec<88>();
+        if (warp == 8) {
+            // ------------------------------------------------------------ TMA
+            const int pb = min(1 << p.page_shift, kTT);  // rows of a box: a page, or a tile of one
+            int pos = 0, qn[2] = {0, 0};
+            bool ok = more() && !p.stall_loads;
+            while (ok) {
+                const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+                const int n = g.t1 - g.t0;
+                const bool pair = g.nrows > rblk;
+                auto load_q = [&](int u) -> bool {
+                    int go = 1;
+                    if (lane == 0) {
+                        if (qn[u] > 0)
+                            go = mbar_wait(&bar->q_empty[u], (qn[u] - 1) & 1, status, DCP_ERR_TIMEOUT, abort);
+                        if (go) {
+                            mbar_arrive_expect_tx(&bar->q_full[u], (uint32_t)(NCH * rblk * 128));
+                            for (int c = 0; c < NCH; ++c)
+                                tma_load_3d(smem + u * kTileBytes + c * kChunkB, &qmap, &bar->q_full[u], 64 * c,
+                                            g.hkv * p.gq, g.row0 + (pair ? u * tj : 0));
+                        }
+                    }
+                    ++qn[u];
+                    return __shfl_sync(kAllLanes, go, 0);
+                };
+                auto load_tile = [&](int i, const CUtensorMap* map) -> bool {
+                    const int s = pos % kSlots;
+                    const int tb = (g.t0 + i) * kTT;
+                    const int nseg = (min(kTT, g.lim_last - tb) + pb - 1) / pb;
+                    int pg = 0;
+                    if (lane < nseg) {  // entries of tokens that exist only
+                        pg = __ldg(p.bt + (int64_t)g.r * p.bt_sn + (int64_t)g.b * p.bt_sb +
+                                   ((tb + lane * pb) >> p.page_shift));
+                        if ((unsigned)pg >= (unsigned)p.num_pages) pg = p.num_pages;  // reads zeros
+                    }
+                    int go = 1;
+                    if (lane == 0) {
+                        if (pos >= kSlots)
+                            go = mbar_wait(&bar->empty[s], (pos / kSlots - 1) & 1, status, DCP_ERR_TIMEOUT, abort);
+                        if (go) {
+                            mbar_arrive_expect_tx(&bar->full[s], (uint32_t)(NCH * nseg * pb * 128));
+                            __threadfence_block();
+                            *(volatile int*)&bar->issued = pos + 1;
+                        }
+                    }
+                    if (!__shfl_sync(kAllLanes, go, 0)) return false;
+                    if (lane < nseg) {
+                        uint8_t* dst = ring + s * kTileBytes + lane * pb * 128;
+                        const int slot = (tb + lane * pb) & ((1 << p.page_shift) - 1);
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_5d(dst + c * kChunkB, map, &bar->full[s], 64 * c, g.hkv, slot, pg, g.r);
+                    }
+                    __syncwarp();
+                    ++pos;
+                    return true;
+                };
+                if (pair) {
+                    if (n > 0) ok = load_q(0) && load_tile(0, &kmap) && load_q(1) && load_tile(0, &vmap);
+                    for (int i = 1; ok && i < n; ++i) ok = load_tile(i, &kmap) && load_tile(i, &vmap);
+                } else {
+                    if (n > 0) ok = load_q(0) && load_tile(0, &kmap);
+                    if (ok && n > 1) ok = load_q(1) && load_tile(1, &kmap);
+                    for (int i = 0; ok && i < n; ++i) {
+                        ok = load_tile(i, &vmap);
+                        if (ok && i + 2 < n) ok = load_tile(i + 2, &kmap);
+                    }
+                }
+                if (!ok || !advance()) break;
+                ok = more();
+            }
+            // copies still in flight (only after an abort) land before the CTA ends
+            if (lane == 0) {
+                for (int j = max(0, pos - kSlots); j < pos; ++j) {
+                    const uint64_t t = global_timer_ns();
+                    while (!mbar_try_wait(&bar->full[j % kSlots], (j / kSlots) & 1) &&
+                           global_timer_ns() - t < kWaitLimitNs) {
+                    }
+                }
+                for (int u = 0; u < 2 && *abort; ++u) {
+                    const uint64_t t = global_timer_ns();
+                    while (qn[u] > 0 && !mbar_try_wait(&bar->q_full[u], (qn[u] - 1) & 1) &&
+                           global_timer_ns() - t < kWaitLimitNs / 100) {
+                    }
+                }
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMA
+            if (lane == 0) {
+                constexpr bool kBf16 = !std::is_same<T, __half>::value;
+                const uint32_t idesc_s = idesc_f16(kM, kTT, kBf16, 0, 0);
+                const uint32_t idesc_o = idesc_f16(kM, D, kBf16, 0, 1);
+                int base = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+                unsigned cleaned = 0u;  // phase of v_clean by slot
+                bool ok = more();
+                while (ok) {
+                    const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+                    const int n = g.t1 - g.t0;
+                    const bool pair = g.nrows > rblk;
+                    const int mtile = g.lim0 / kTT - g.t0;  // masked from here on, within the part
+                    // ring positions of a tile's K and V
+                    auto pos_k = [&](int i) { return base + (pair ? 2 * i : (i < 2 ? i : 2 * i - 1)); };
+                    auto pos_v = [&](int i) { return base + (pair ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1)); };
+                    auto issue_s = [&](int u, int i, bool release, bool last) -> bool {
+                        const int j = pos_k(i), s = j % kSlots;
+                        if (!mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort)) return false;
+                        tc_fence_after();
+                        const uint64_t da = smem_desc(smem_u32(smem + u * kTileBytes), 16, 1024, kSwizzle128B);
+                        const uint64_t db = smem_desc(smem_u32(ring + s * kTileBytes), 16, 1024, kSwizzle128B);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)(((kk >> 2) * kChunkB + (kk & 3) * 32) >> 4);
+                            mma_ss(tmem + kM * u, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(&bar->s_full[u]);
+                        if (release) mma_commit(&bar->empty[s]);
+                        if (last) mma_commit(&bar->q_empty[u]);
+                        issued_any = true;
+                        return true;
+                    };
+                    auto issue_o = [&](int u, int i, bool begin, bool clean, bool release) -> bool {
+                        if (!mbar_wait(&bar->p_full[u], pn[u] & 1, status, DCP_ERR_TIMEOUT, abort)) return false;
+                        ++pn[u];
+                        const int j = pos_v(i), s = j % kSlots;
+                        if (!mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort)) return false;
+                        if (clean && i >= mtile) {
+                            if (!mbar_wait(&bar->v_clean[s], (cleaned >> s) & 1, status, DCP_ERR_TIMEOUT, abort))
+                                return false;
+                            cleaned ^= 1u << s;
+                        }
+                        tc_fence_after();
+                        const uint64_t dv = smem_desc(smem_u32(ring + s * kTileBytes), kChunkB, 1024, kSwizzle128B);
+                        const uint32_t tP = tmem + kM * u;
+#pragma unroll
+                        for (int kk = 0; kk < kTT / 16; ++kk)
+                            mma_ts(tmem + kColO + D * u, tP + 8 * kk, dv + (uint64_t)((2048 * kk) >> 4), idesc_o,
+                                   (!begin || kk > 0) ? 1u : 0u);
+                        mma_commit(&bar->pv_done[u]);
+                        if (release) mma_commit(&bar->empty[s]);
+                        return true;
+                    };
+                    auto wait_q = [&](int u) -> bool {
+                        return mbar_wait(&bar->q_full[u], qn[u]++ & 1, status, DCP_ERR_TIMEOUT, abort);
+                    };
+                    if (pair) {
+                        if (n > 0)
+                            ok = wait_q(0) && issue_s(0, 0, false, n == 1) && wait_q(1) && issue_s(1, 0, true, n == 1);
+                        for (int i = 0; ok && i < n; ++i) {
+                            ok = issue_o(0, i, i == 0, true, false);
+                            if (ok && i + 1 < n) ok = issue_s(0, i + 1, false, i + 2 == n);
+                            if (ok) ok = issue_o(1, i, i == 0, false, true);
+                            if (ok && i + 1 < n) ok = issue_s(1, i + 1, true, i + 2 == n);
+                        }
+                    } else {
+                        if (n > 0) ok = wait_q(0) && issue_s(0, 0, true, n <= 2);
+                        if (ok && n > 1) ok = wait_q(1) && issue_s(1, 1, true, n <= 3);
+                        for (int i = 0; ok && i < n; ++i) {
+                            ok = issue_o(i & 1, i, i < 2, true, true);
+                            if (ok && i + 2 < n) ok = issue_s(i & 1, i + 2, true, i + 4 >= n);
+                        }
+                    }
+                    base += 2 * n;
+                    if (!ok || !advance()) break;
+                    ok = more();
+                }
+                if (issued_any) mma_commit(&bar->mma_done);
+            }
+        } else if (warp == 10) {
+            // -------------------------------------------- V of the masked tiles
+            int base = 0, seg = 0;
+            bool ok = more();
+            while (ok) {
+                const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+                const int n = g.t1 - g.t0;
+                const bool pair = g.nrows > rblk;
+                const int m0 = g.lim0 / kTT;
+                unsigned* poison = bar->poison[seg & (kPoison - 1)];
+                if (lane < 16) poison[lane] = 0u;
+                __syncwarp();
+                for (int t = max(m0, g.t0); ok && t < g.t1; ++t) {
+                    const int i = t - g.t0;
+                    const int j = base + (pair ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1)), s = j % kSlots;
+                    // this warp does not wait for every tile, so the slot's barrier may still
+                    // be phases behind: its parity means something once the load is under
+                    // way (and the slot cannot pass on before this tile is clean)
+                    const uint64_t t_start = global_timer_ns();
+                    while (*(volatile int*)&bar->issued <= j && !*abort) {
+                        if (global_timer_ns() - t_start > kWaitLimitNs) {
+                            atomicCAS(status, 0, DCP_ERR_TIMEOUT);
+                            *abort = 1;
+                        }
+                    }
+                    __threadfence_block();
+                    ok = !__any_sync(kAllLanes, *abort != 0) &&
+                         __all_sync(kAllLanes,
+                                    mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort));
+                    if (!ok) break;
+                    uint8_t* tile = ring + s * kTileBytes;
+                    const int live = g.lim_last - t * kTT;  // rows from here on are no one's
+                    for (int row = max(live, 0); row < kTT; ++row) {
+                        if (lane < 8 * NCH)
+                            *reinterpret_cast<uint4*>(tile + (lane >> 3) * kChunkB + row * 128 + (lane & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (g.lim0 < g.lim_last) {  // rows of the item differ in what they see
+                        // 16 bytes a lane, 4 rows of 128 bytes a step
+                        const int rows = min(live, kTT);
+                        for (int r4 = 0; r4 < rows; r4 += 4) {
+                            const int row = r4 + (lane >> 3);
+#pragma unroll
+                            for (int c = 0; c < NCH; ++c) {
+                                uint4* at = reinterpret_cast<uint4*>(tile + c * kChunkB + row * 128 + (lane & 7) * 16);
+                                uint4 v = *at;
+                                if (row < rows && (pair_nonfinite<T>(v.x) || pair_nonfinite<T>(v.y) ||
+                                                   pair_nonfinite<T>(v.z) || pair_nonfinite<T>(v.w))) {
+                                    v = make_uint4(pair_finite<T>(v.x), pair_finite<T>(v.y), pair_finite<T>(v.z),
+                                                   pair_finite<T>(v.w));
+                                    *at = v;
+                                    atomicOr(&poison[4 * (t - m0) + (row >> 5)], 1u << (row & 31));
+                                }
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->v_clean[s]);
+                }
+                base += 2 * n;
+                ++seg;
+                if (!ok || !advance()) break;
+                ok = more();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        regs_inc<208>();
+        const int u = warp >> 2;             // stage
+        const int m = tid & 127;             // row of the stage
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + kM * u + lanes, tO = tmem + kColO + D * u + lanes;
+        const float qscale = p.sm_scale * kLog2e;
+        const unsigned long long qs2 = pack2f(qscale, qscale);
+        int sn = 0, vn = 0, xn = 0, seg = 0;  // phases of s_full and pv_done, exchanges, parts
+        bool ok = more();
+        auto wait = [&](uint64_t* b, int parity) -> bool {
+            return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
+        };
+        while (ok) {
+            const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+            const int n = g.t1 - g.t0;
+            const bool pair = g.nrows > rblk;
+            const int mine = pair ? n : (n + 1 - u) / 2;   // tiles of this stage
+            const int step = pair ? 1 : 2, tile0 = g.t0 + (pair ? 0 : u);
+            const int row = (pair ? u * rblk : 0) + m;     // row of the item
+            const bool valid = m < rblk && row < g.nrows;
+            const int tok = row / p.gq, hh = row - tok * p.gq;
+            const int lim = valid ? visible(p, g.q, g.j0 + tok, g.r) : 0;
+            const bool live = __any_sync(kAllLanes, valid);
+            float mref = -INFINITY, vref = 0.f;  // the reference maximum, scaled and as a score
+            bool far = false;                    // a row of the warp has one beyond kFar
+            unsigned long long l2 = 0ull;
+            for (int i = 0; i < mine; ++i) {
+                if (!(ok = wait(&bar->s_full[u], sn))) break;
+                ++sn;
+                const int tb = (tile0 + i * step) * kTT;
+                if (live) {
+                    tc_fence_after();
+                    // the row's maximum, 32 columns at a time, the next ones in flight; the
+                    // last 32 stay, the others are read again (a row of 128 scores does
+                    // not fit in the registers beside the rest)
+                    const bool masked = tb + kTT > g.lim0;
+                    const int seen = lim - tb;
+                    float m0 = -INFINITY, m1 = -INFINITY;
+                    uint32_t va[32], vb[32], vc[32];
+                    tmem_ld32<0>(tS, va);
+                    tmem_wait_ld();
+                    pin(va);
+                    tmem_ld32<0>(tS + 32, vb);
+                    if (masked) mask_cols(va, seen);
+                    row_max(va, m0, m1);
+                    tmem_wait_ld();
+                    pin(vb);
+                    tmem_ld32<0>(tS + 64, va);
+                    if (masked) mask_cols(vb, seen - 32);
+                    row_max(vb, m0, m1);
+                    tmem_wait_ld();
+                    pin(va);
+                    tmem_ld32<0>(tS + 96, vb);
+                    if (masked) mask_cols(va, seen - 64);
+                    row_max(va, m0, m1);
+                    tmem_wait_ld();
+                    pin(vb);
+                    tmem_ld32<0>(tS, va);
+                    if (masked) mask_cols(vb, seen - 96);
+                    row_max(vb, m0, m1);
+                    const float vt = fmaxf(m0, m1);
+                    const bool grow = vt * qscale > mref + kGrow;
+                    if (__any_sync(kAllLanes, grow)) {
+                        float alpha = 1.f;
+                        if (grow) {
+                            alpha = mref == -INFINITY ? 0.f : exp2_fast((vref - vt) * qscale);
+                            vref = vt;
+                            mref = vt * qscale;
+                            const float2 l = unpack2(l2);
+                            l2 = pack2f(l.x * alpha, l.y * alpha);
+                        }
+                        far = __any_sync(kAllLanes, fabsf(mref) > kFar && mref != -INFINITY);
+                        if (i > 0) {  // O holds the tiles before: rescale it once the last of them has landed
+                            if (!(ok = wait(&bar->pv_done[u], vn + i - 1))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + 16 * c, o);
+                                tmem_wait_ld();
+                                pin(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(tO + 16 * c, o);
+                            }
+                        }
+                    }
+                    const float off = mref == -INFINITY || far ? 0.f : -mref;
+                    const float sub = mref == -INFINITY ? 0.f : vref;
+                    const unsigned long long off2 = pack2f(off, off);
+                    tmem_wait_ld();
+                    pin(va);
+                    tmem_ld32<0>(tS + 32, vc);
+                    if (masked) mask_cols(va, seen);
+                    if (far) sub_cols(va, sub);
+                    exp_store<T>(va, tS, qs2, off2, l2);
+                    tmem_wait_ld();
+                    pin(vc);
+                    tmem_ld32<0>(tS + 64, va);
+                    if (masked) mask_cols(vc, seen - 32);
+                    if (far) sub_cols(vc, sub);
+                    exp_store<T>(vc, tS + 16, qs2, off2, l2);
+                    tmem_wait_ld();
+                    pin(va);
+                    if (masked) mask_cols(va, seen - 64);
+                    if (far) sub_cols(va, sub);
+                    exp_store<T>(va, tS + 32, qs2, off2, l2);
+                    if (far) sub_cols(vb, sub);
+                    exp_store<T>(vb, tS + 48, qs2, off2, l2);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->p_full[u]);
+            }
+            if (ok && mine > 0) ok = wait(&bar->pv_done[u], vn + mine - 1);
+            vn += mine;
+            tc_fence_after();
+            const float2 lp = unpack2(l2);
+            float l = lp.x + lp.y;
+            // an item of one row block: stage 0 takes what stage 1 has
+            float w0 = 1.f, w1 = 0.f;
+            if (!pair && ok) {
+                if (u == 1) {
+                    bar->xm[m] = mref;
+                    bar->xl[m] = l;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->x_full);
+                    ok = wait(&bar->x_done, xn);
+                    tc_fence_after();
+                } else {
+                    ok = wait(&bar->x_full, xn);
+                    tc_fence_after();
+                    const float m1 = bar->xm[m], l1 = bar->xl[m];
+                    const float mx = fmaxf(mref, m1), z = mx == -INFINITY ? 0.f : mx;
+                    w0 = exp2_fast(mref - z);
+                    w1 = n > 1 ? exp2_fast(m1 - z) : 0.f;
+                    l = l * w0 + (n > 1 ? l1 * w1 : 0.f);
+                    mref = mx;
+                }
+                ++xn;
+            }
+            // l is 0 only where the row sees nothing (a visible row's largest term is at least 2^-8); NaN stays NaN
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float lse2 = l == 0.f ? -INFINITY : mref + log2f(l);
+            const bool writes = ok && live && (pair || u == 0);
+            const int h = g.hkv * p.gq + hh;
+            const int64_t t = g.row0 + tok;
+            if (writes) {
+                unsigned char* orow = p.o + (int64_t)g.r * p.o_sn + t * p.o_st + (int64_t)h * p.o_sh;
+                const int64_t prow = (int64_t)g.slot * (2 * kM) + row;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld32<0>(tO + 32 * c, o);
+                        tmem_wait_ld();
+                        pin(o);
+                        const float a = w0 * inv;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                        if (!pair && n > 1) {
+                            uint32_t o1[32];
+                            tmem_ld32<0>(tO + D + 32 * c, o1);
+                            tmem_wait_ld();
+                            pin(o1);
+                            const float b = w1 * inv;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), b, __uint_as_float(o[e])));
+                        }
+                    }
+                    if (valid) {
+                        // a row that sees nothing is zero, whatever the accumulator holds
+                        if (n == 0 || l == 0.f) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        }
+                        if (g.slot < 0) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = f32_to_pair(make_float2(__uint_as_float(o[8 * e + 2 * k]),
+                                                                   __uint_as_float(o[8 * e + 2 * k + 1])), T());
+                                *reinterpret_cast<uint4*>(orow + 64 * c + 16 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(ws.o + prow * D + 32 * c + 4 * e) =
+                                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (valid) {
+                    if (g.slot < 0)
+                        p.lse[(int64_t)g.r * p.l_sn + t * p.l_st + (int64_t)h * p.l_sh] = p.base2 ? lse2 : lse2 * kLn2;
+                    else
+                        ws.lse[prow] = lse2;
+                    // what the zeroed values of masked tiles give to the rows that do see them
+                    const int mt0 = g.lim0 / kTT;
+                    if (g.lim0 < g.lim_last && g.t1 > mt0) {
+                        volatile unsigned* mask = bar->poison[seg & (kPoison - 1)];
+                        unsigned any = 0u;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) any |= mask[e];
+                        if (any) {
+                            const T* qrow = reinterpret_cast<const T*>(p.q + t * p.q_st + (int64_t)h * p.q_sh);
+                            for (int e = 0; e < 4; ++e) {
+                                if (g.slot < 0)
+                                    add_nonfinite<T, T>(p, g.r, g.b, g.hkv, qrow, (mt0 + e) * kTT,
+                                                        (const unsigned*)mask + 4 * e, 4, lim, lse2,
+                                                        reinterpret_cast<T*>(orow));
+                                else
+                                    add_nonfinite<T, float>(p, g.r, g.b, g.hkv, qrow, (mt0 + e) * kTT,
+                                                            (const unsigned*)mask + 4 * e, 4, lim, lse2,
+                                                            ws.o + prow * D);
+                            }
+                        }
+                    }
+                }
+            }
+            if (!pair && u == 0) {  // stage 1 may go on
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->x_done);
+            }
+            ++seg;
+            if (!ok || !advance()) break;
+            ok = more();
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        if (lane == 0 && issued_any) {
+            // every MMA this CTA issued has completed before its tensor memory goes
+            const uint64_t t = global_timer_ns();
+            while (!mbar_try_wait(&bar->mma_done, 0) && global_timer_ns() - t < kWaitLimitNs) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_tc(const ChunkParams& p, const CUtensorMap (&maps)[3], int dtype, cudaStream_t stream) {
+    const int ctas = device_sm_count(), tpi = 2 * (kM / p.gq);
+    const ChunkPartials ws = chunk_partials_in(p.ws, ctas, 2 * kM, D);
+    cudaError_t e = launch_chunk_plan(p, ws, tpi, kTT, ctas, stream);
+    if (e != cudaSuccess) return e;
+    const void* k = (const void*)chunk_attention_tc_kernel<T, D>;
+    // the shared-memory opt-in is a per-device function attribute
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    chunk_attention_tc_kernel<T, D>
+        <<<ctas, kThreadsTc, TcShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, ws, tpi);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_chunk_merge(p, ws, tpi, 2 * kM, ctas, dtype, stream);
+}
+
+}  // namespace
+
+size_t chunk_attention_tc_workspace(int D) {
+    return D == 64 || D == 128 ? chunk_partials_bytes(device_sm_count(), 2 * kM, D) : 0;
+}
+
+bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
+    // the maximum of the scaled scores is that of the scores for a positive scale
+    // only; boxes hold whole 8-row swizzle atoms
+    if ((p.D != 64 && p.D != 128) || !(p.sm_scale > 0.f) || p.page_shift < 3) return false;
+    const EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const CUtensorMapDataType dt = dtype == DCP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    // a dimension of extent 1 is never stepped over: give it a nominal stride
+    auto stride = [](int64_t extent, int64_t bytes) -> cuuint64_t { return (cuuint64_t)(extent > 1 ? bytes : 256); };
+    CUtensorMap maps[3];
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.T};
+        const cuuint64_t strides[2] = {stride(p.H, p.q_sh), stride(p.T, p.q_st)};
+        const cuuint32_t box[3] = {64, (cuuint32_t)p.gq, (cuuint32_t)(kM / p.gq)};
+        if (enc(&maps[0], dt, 3, const_cast<unsigned char*>(p.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    for (int m = 0; m < 2; ++m) {
+        const int64_t rows = (int64_t)1 << p.page_shift;
+        const int64_t st = m ? p.v_st : p.k_st, sh = m ? p.v_sh : p.k_sh, sp = m ? p.v_sp : p.k_sp;
+        const cuuint64_t dims[5] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, (cuuint64_t)rows, (cuuint64_t)p.num_pages,
+                                    (cuuint64_t)p.N};
+        const cuuint64_t strides[4] = {stride(p.Hkv, sh), stride(rows, st), stride(p.num_pages, sp),
+                                       stride(p.N, m ? p.v_sn : p.k_sn)};
+        const cuuint32_t box[5] = {64, 1, (cuuint32_t)(rows < kTT ? rows : kTT), 1, 1};
+        if (enc(&maps[1 + m], dt, 5, m ? p.v : p.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;  // strides a tensor map cannot describe: the register-tiled kernel takes it
+    }
+    ChunkParams q = p;
+    // DCP_TEST_STALL_LOADS=1 (tests of the failure path only): no loads are
+    // issued, so the first wait on them runs out.  Unset in normal use.
+    const char* stall = getenv("DCP_TEST_STALL_LOADS");
+    q.stall_loads = stall && stall[0] == '1';
+    if (p.D == 128)
+        *err = dtype == DCP_F16 ? launch_tc<__half, 128>(q, maps, dtype, stream)
+                                : launch_tc<__nv_bfloat16, 128>(q, maps, dtype, stream);
+    else
+        *err = dtype == DCP_F16 ? launch_tc<__half, 64>(q, maps, dtype, stream)
+                                : launch_tc<__nv_bfloat16, 64>(q, maps, dtype, stream);
+    return true;
+}
+
+int chunk_attention_tc_status(bool clear) {
+    int s = 0;
+    if (cudaMemcpyFromSymbol(&s, g_chunk_status, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && s) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_chunk_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return s;
+}
+
+}  // namespace dcp

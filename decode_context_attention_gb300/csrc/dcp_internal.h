@@ -202,6 +202,12 @@ cudaError_t launch_append(const AppendParams& p, int dtype, cudaStream_t stream)
 // Attention of a chunk of new tokens: bytes of workspace the kernels want, and the launch.
 size_t chunk_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len);
 cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t stream);
+// The tcgen05 path of the same attention, for the shapes it takes (D = 64 or
+// 128, sm_scale > 0, pages of at least 8 tokens, strides a tensor map can
+// describe): false without launching anything otherwise.
+size_t chunk_attention_tc_workspace(int D);
+bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
+int chunk_attention_tc_status(bool clear);
 cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 
