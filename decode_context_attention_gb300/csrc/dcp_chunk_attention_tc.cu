@@ -98,33 +98,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Columns from `seen` on are not visible.
-__device__ __forceinline__ void mask_cols(uint32_t (&v)[32], int seen) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c)
-        if (c >= seen) v[c] = 0xff800000u;
+// A volatile read: the compiler keeps no copy of it.
+__device__ __forceinline__ ChunkPos load_pos(const ChunkPos* at) {
+    ChunkPos x;
+    asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.b), "=r"(x.rh), "=r"(x.qt), "=r"(x.tile)
+                 : "l"(at));
+    return x;
 }
-__device__ __forceinline__ void sub_cols(uint32_t (&v)[32], float x) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) - x);
-}
-__device__ __forceinline__ void row_max(const uint32_t (&v)[32], float& m0, float& m1) {
-#pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-        m0 = max3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-        m1 = max3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-    }
-}
-// P of 32 scores, 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
-template <typename T>
-__device__ __forceinline__ void exp_store(const uint32_t (&v)[32], uint32_t tP, unsigned long long qs2,
-                                          unsigned long long off2, unsigned long long& l2) {
+// P of the 32 scores v[OFF ..], 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
+template <typename T, int OFF>
+__device__ __forceinline__ void exp_store(const uint32_t (&v)[128], uint32_t tP, unsigned long long qs2,
+                                          unsigned long long off2, unsigned long long (&l2)[2]) {
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        const float2 f = unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), qs2, off2));
+        const float2 f = unpack2(fma2(pack2(v[OFF + 2 * e], v[OFF + 2 * e + 1]), qs2, off2));
         const float2 pr = make_float2(exp2_fast(f.x), exp2_fast(f.y));
-        add2(l2, pack2f(pr.x, pr.y));
+        add2(l2[e & 1], pack2f(pr.x, pr.y));
         w[e] = f32_to_pair(pr, T());
     }
     tmem_st16(tP, w);
@@ -181,15 +172,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
     int* status = &g_chunk_status;
-    const ChunkPos first = ws.pos[blockIdx.x];
-    const ChunkPos end = ws.pos[blockIdx.x + 1];
-    ChunkPos x = first;
-    auto more = [&]() { return x.b < p.B && !(same_item(x, end) && x.tile == end.tile); };
+    // the range, read again at every item rather than held in registers
+    const ChunkPos* range = ws.pos + blockIdx.x;
+    ChunkPos x = load_pos(range);
+    auto more = [&]() {
+        const ChunkPos end = load_pos(range + 1);
+        return x.b < p.B && !(same_item(x, end) && x.tile == end.tile);
+    };
     auto advance = [&]() -> bool {  // false behind the last part
-        if (same_item(x, end)) return false;
+        if (same_item(x, load_pos(range + 1))) return false;
         x = next_item(p, x, tpi);
         return true;
     };
+    auto this_seg = [&]() { return load_seg(p, x, load_pos(range), load_pos(range + 1), tpi, kTT); };
     bool issued_any = false;
 
     if (warp >= 8) {
@@ -200,7 +195,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             int pos = 0, qn[2] = {0, 0};
             bool ok = more() && !p.stall_loads;
             while (ok) {
-                const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+                const ChunkSeg g = this_seg();
                 const int n = g.t1 - g.t0;
                 const bool pair = g.nrows > rblk;
                 auto load_q = [&](int u) -> bool {
@@ -289,7 +284,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 unsigned cleaned = 0u;  // phase of v_clean by slot
                 bool ok = more();
                 while (ok) {
-                    const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+                    const ChunkSeg g = this_seg();
                     const int n = g.t1 - g.t0;
                     const bool pair = g.nrows > rblk;
                     const int mtile = g.lim0 / kTT - g.t0;  // masked from here on, within the part
@@ -365,7 +360,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             int base = 0, seg = 0;
             bool ok = more();
             while (ok) {
-                const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
+                const ChunkSeg g = this_seg();
                 const int n = g.t1 - g.t0;
                 const bool pair = g.nrows > rblk;
                 const int m0 = g.lim0 / kTT;
@@ -434,61 +429,58 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + kM * u + lanes, tO = tmem + kColO + D * u + lanes;
         const float qscale = p.sm_scale * kLog2e;
-        const unsigned long long qs2 = pack2f(qscale, qscale);
         int sn = 0, vn = 0, xn = 0, seg = 0;  // phases of s_full and pv_done, exchanges, parts
         bool ok = more();
         auto wait = [&](uint64_t* b, int parity) -> bool {
             return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
         };
         while (ok) {
-            const ChunkSeg g = load_seg(p, x, first, end, tpi, kTT);
-            const int n = g.t1 - g.t0;
-            const bool pair = g.nrows > rblk;
-            const int mine = pair ? n : (n + 1 - u) / 2;   // tiles of this stage
-            const int step = pair ? 1 : 2, tile0 = g.t0 + (pair ? 0 : u);
-            const int row = (pair ? u * rblk : 0) + m;     // row of the item
-            const bool valid = m < rblk && row < g.nrows;
-            const int tok = row / p.gq, hh = row - tok * p.gq;
-            const int lim = valid ? visible(p, g.q, g.j0 + tok, g.r) : 0;
-            const bool live = __any_sync(kAllLanes, valid);
+            int n, mine, step, tile0, lim, lim0;
+            bool pair, live;
+            {
+                const ChunkSeg g = this_seg();
+                n = g.t1 - g.t0;
+                pair = g.nrows > rblk;
+                mine = pair ? n : (n + 1 - u) / 2;  // tiles of this stage
+                step = pair ? 1 : 2;
+                tile0 = g.t0 + (pair ? 0 : u);
+                const int row = (pair ? u * rblk : 0) + m;
+                const bool valid = m < rblk && row < g.nrows;
+                lim = valid ? visible(p, g.q, g.j0 + row / p.gq, g.r) : 0;
+                lim0 = g.lim0;
+                live = __any_sync(kAllLanes, valid);
+            }
             float mref = -INFINITY, vref = 0.f;  // the reference maximum, scaled and as a score
             bool far = false;                    // a row of the warp has one beyond kFar
-            unsigned long long l2 = 0ull;
+            unsigned long long l2[2] = {0ull, 0ull};
             for (int i = 0; i < mine; ++i) {
                 if (!(ok = wait(&bar->s_full[u], sn))) break;
                 ++sn;
                 const int tb = (tile0 + i * step) * kTT;
                 if (live) {
                     tc_fence_after();
-                    // the row's maximum, 32 columns at a time, the next ones in flight; the
-                    // last 32 stay, the others are read again (a row of 128 scores does
-                    // not fit in the registers beside the rest)
-                    const bool masked = tb + kTT > g.lim0;
-                    const int seen = lim - tb;
-                    float m0 = -INFINITY, m1 = -INFINITY;
-                    uint32_t va[32], vb[32], vc[32];
-                    tmem_ld32<0>(tS, va);
+                    uint32_t v[128];
+                    tmem_ld32<0>(tS, v);
+                    tmem_ld32<32>(tS + 32, v);
+                    tmem_ld32<64>(tS + 64, v);
+                    tmem_ld32<96>(tS + 96, v);
                     tmem_wait_ld();
-                    pin(va);
-                    tmem_ld32<0>(tS + 32, vb);
-                    if (masked) mask_cols(va, seen);
-                    row_max(va, m0, m1);
-                    tmem_wait_ld();
-                    pin(vb);
-                    tmem_ld32<0>(tS + 64, va);
-                    if (masked) mask_cols(vb, seen - 32);
-                    row_max(vb, m0, m1);
-                    tmem_wait_ld();
-                    pin(va);
-                    tmem_ld32<0>(tS + 96, vb);
-                    if (masked) mask_cols(va, seen - 64);
-                    row_max(va, m0, m1);
-                    tmem_wait_ld();
-                    pin(vb);
-                    tmem_ld32<0>(tS, va);
-                    if (masked) mask_cols(vb, seen - 96);
-                    row_max(vb, m0, m1);
-                    const float vt = fmaxf(m0, m1);
+                    pin(v);
+                    if (tb + kTT > lim0) {
+                        const int seen = lim - tb;
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c >= seen) v[c] = 0xff800000u;
+                    }
+                    float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 8) {
+                        m0 = max3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                        m1 = max3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                        m2 = max3(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+                        m3 = max3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+                    }
+                    const float vt = fmaxf(max3(m0, m1, m2), m3);
                     const bool grow = vt * qscale > mref + kGrow;
                     if (__any_sync(kAllLanes, grow)) {
                         float alpha = 1.f;
@@ -496,8 +488,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             alpha = mref == -INFINITY ? 0.f : exp2_fast((vref - vt) * qscale);
                             vref = vt;
                             mref = vt * qscale;
-                            const float2 l = unpack2(l2);
-                            l2 = pack2f(l.x * alpha, l.y * alpha);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float2 l = unpack2(l2[e]);
+                                l2[e] = pack2f(l.x * alpha, l.y * alpha);
+                            }
                         }
                         far = __any_sync(kAllLanes, fabsf(mref) > kFar && mref != -INFINITY);
                         if (i > 0) {  // O holds the tiles before: rescale it once the last of them has landed
@@ -516,27 +511,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         }
                     }
                     const float off = mref == -INFINITY || far ? 0.f : -mref;
-                    const float sub = mref == -INFINITY ? 0.f : vref;
-                    const unsigned long long off2 = pack2f(off, off);
-                    tmem_wait_ld();
-                    pin(va);
-                    tmem_ld32<0>(tS + 32, vc);
-                    if (masked) mask_cols(va, seen);
-                    if (far) sub_cols(va, sub);
-                    exp_store<T>(va, tS, qs2, off2, l2);
-                    tmem_wait_ld();
-                    pin(vc);
-                    tmem_ld32<0>(tS + 64, va);
-                    if (masked) mask_cols(vc, seen - 32);
-                    if (far) sub_cols(vc, sub);
-                    exp_store<T>(vc, tS + 16, qs2, off2, l2);
-                    tmem_wait_ld();
-                    pin(va);
-                    if (masked) mask_cols(va, seen - 64);
-                    if (far) sub_cols(va, sub);
-                    exp_store<T>(va, tS + 32, qs2, off2, l2);
-                    if (far) sub_cols(vb, sub);
-                    exp_store<T>(vb, tS + 48, qs2, off2, l2);
+                    if (far) {
+                        const float sub = mref == -INFINITY ? 0.f : vref;
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) - sub);
+                    }
+                    const unsigned long long qs2 = pack2f(qscale, qscale), off2 = pack2f(off, off);
+                    exp_store<T, 0>(v, tS, qs2, off2, l2);
+                    exp_store<T, 32>(v, tS + 16, qs2, off2, l2);
+                    exp_store<T, 64>(v, tS + 32, qs2, off2, l2);
+                    exp_store<T, 96>(v, tS + 48, qs2, off2, l2);
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -546,7 +530,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (ok && mine > 0) ok = wait(&bar->pv_done[u], vn + mine - 1);
             vn += mine;
             tc_fence_after();
-            const float2 lp = unpack2(l2);
+            add2(l2[0], l2[1]);
+            const float2 lp = unpack2(l2[0]);
             float l = lp.x + lp.y;
             // an item of one row block: stage 0 takes what stage 1 has
             float w0 = 1.f, w1 = 0.f;
@@ -571,6 +556,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 ++xn;
             }
+            // the item again, for where its rows go: held through the tiles it would take
+            // the registers of their scores
+            asm volatile("" : "+r"(x.b), "+r"(x.rh), "+r"(x.qt), "+r"(x.tile));
+            const ChunkSeg g = this_seg();
+            const int row = (pair ? u * rblk : 0) + m;  // row of the item
+            const bool valid = m < rblk && row < g.nrows;
+            const int tok = row / p.gq, hh = row - tok * p.gq;
             // l is 0 only where the row sees nothing (a visible row's largest term is at least 2^-8); NaN stays NaN
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : mref + log2f(l);
@@ -580,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (writes) {
                 unsigned char* orow = p.o + (int64_t)g.r * p.o_sn + t * p.o_st + (int64_t)h * p.o_sh;
                 const int64_t prow = (int64_t)g.slot * (2 * kM) + row;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     if (n > 0) {
