@@ -276,85 +276,92 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
         } else if (warp == 9) {
             // ------------------------------------------------------------ MMA
-            if (lane == 0) {
-                constexpr bool kBf16 = !std::is_same<T, __half>::value;
-                const uint32_t idesc_s = idesc_f16(kM, kTT, kBf16, 0, 0);
-                const uint32_t idesc_o = idesc_f16(kM, D, kBf16, 0, 1);
-                int base = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
-                unsigned cleaned = 0u;  // phase of v_clean by slot
-                bool ok = more();
-                while (ok) {
+            // the whole warp runs along, its leader issues
+            constexpr bool kBf16 = !std::is_same<T, __half>::value;
+            const uint32_t idesc_s = idesc_f16(kM, kTT, kBf16, 0, 0);
+            const uint32_t idesc_o = idesc_f16(kM, D, kBf16, 0, 1);
+            const uint32_t tm = __shfl_sync(kAllLanes, tmem, 0);
+            const uint32_t qa = __shfl_sync(kAllLanes, smem_u32(smem), 0);
+            const uint32_t ra = qa + 2 * kTileBytes;
+            int base = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+            unsigned cleaned = 0u;  // phase of v_clean by slot
+            bool ok = more();
+            while (ok) {
+                int n, mtile;
+                bool pair;
+                {
                     const ChunkSeg g = this_seg();
-                    const int n = g.t1 - g.t0;
-                    const bool pair = g.nrows > rblk;
-                    const int mtile = g.lim0 / kTT - g.t0;  // masked from here on, within the part
-                    // ring positions of a tile's K and V
-                    auto pos_k = [&](int i) { return base + (pair ? 2 * i : (i < 2 ? i : 2 * i - 1)); };
-                    auto pos_v = [&](int i) { return base + (pair ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1)); };
-                    auto issue_s = [&](int u, int i, bool release, bool last) -> bool {
-                        const int j = pos_k(i), s = j % kSlots;
-                        if (!mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort)) return false;
-                        tc_fence_after();
-                        const uint64_t da = smem_desc(smem_u32(smem + u * kTileBytes), 16, 1024, kSwizzle128B);
-                        const uint64_t db = smem_desc(smem_u32(ring + s * kTileBytes), 16, 1024, kSwizzle128B);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (uint64_t)(((kk >> 2) * kChunkB + (kk & 3) * 32) >> 4);
-                            mma_ss(tmem + kM * u, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(&bar->s_full[u]);
-                        if (release) mma_commit(&bar->empty[s]);
-                        if (last) mma_commit(&bar->q_empty[u]);
-                        issued_any = true;
-                        return true;
-                    };
-                    auto issue_o = [&](int u, int i, bool begin, bool clean, bool release) -> bool {
-                        if (!mbar_wait(&bar->p_full[u], pn[u] & 1, status, DCP_ERR_TIMEOUT, abort)) return false;
-                        ++pn[u];
-                        const int j = pos_v(i), s = j % kSlots;
-                        if (!mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort)) return false;
-                        if (clean && i >= mtile) {
-                            if (!mbar_wait(&bar->v_clean[s], (cleaned >> s) & 1, status, DCP_ERR_TIMEOUT, abort))
-                                return false;
-                            cleaned ^= 1u << s;
-                        }
-                        tc_fence_after();
-                        const uint64_t dv = smem_desc(smem_u32(ring + s * kTileBytes), kChunkB, 1024, kSwizzle128B);
-                        const uint32_t tP = tmem + kM * u;
-#pragma unroll
-                        for (int kk = 0; kk < kTT / 16; ++kk)
-                            mma_ts(tmem + kColO + D * u, tP + 8 * kk, dv + (uint64_t)((2048 * kk) >> 4), idesc_o,
-                                   (!begin || kk > 0) ? 1u : 0u);
-                        mma_commit(&bar->pv_done[u]);
-                        if (release) mma_commit(&bar->empty[s]);
-                        return true;
-                    };
-                    auto wait_q = [&](int u) -> bool {
-                        return mbar_wait(&bar->q_full[u], qn[u]++ & 1, status, DCP_ERR_TIMEOUT, abort);
-                    };
-                    if (pair) {
-                        if (n > 0)
-                            ok = wait_q(0) && issue_s(0, 0, false, n == 1) && wait_q(1) && issue_s(1, 0, true, n == 1);
-                        for (int i = 0; ok && i < n; ++i) {
-                            ok = issue_o(0, i, i == 0, true, false);
-                            if (ok && i + 1 < n) ok = issue_s(0, i + 1, false, i + 2 == n);
-                            if (ok) ok = issue_o(1, i, i == 0, false, true);
-                            if (ok && i + 1 < n) ok = issue_s(1, i + 1, true, i + 2 == n);
-                        }
-                    } else {
-                        if (n > 0) ok = wait_q(0) && issue_s(0, 0, true, n <= 2);
-                        if (ok && n > 1) ok = wait_q(1) && issue_s(1, 1, true, n <= 3);
-                        for (int i = 0; ok && i < n; ++i) {
-                            ok = issue_o(i & 1, i, i < 2, true, true);
-                            if (ok && i + 2 < n) ok = issue_s(i & 1, i + 2, true, i + 4 >= n);
-                        }
-                    }
-                    base += 2 * n;
-                    if (!ok || !advance()) break;
-                    ok = more();
+                    n = __shfl_sync(kAllLanes, g.t1 - g.t0, 0);
+                    pair = __shfl_sync(kAllLanes, g.nrows > rblk ? 1 : 0, 0) != 0;
+                    mtile = __shfl_sync(kAllLanes, g.lim0 / kTT - g.t0, 0);  // masked from here on, within the part
                 }
-                if (issued_any) mma_commit(&bar->mma_done);
+                // ring positions of a tile's K and V
+                auto pos_k = [&](int i) { return base + (pair ? 2 * i : (i < 2 ? i : 2 * i - 1)); };
+                auto pos_v = [&](int i) { return base + (pair ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1)); };
+                auto wait = [&](uint64_t* b, int parity) -> bool {
+                    return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
+                };
+                auto issue_s = [&](int u, int i, bool release, bool last) -> bool {
+                    const int j = pos_k(i), s = j % kSlots;
+                    if (!wait(&bar->full[s], j / kSlots)) return false;
+                    tc_fence_after();
+                    const uint64_t da = smem_desc(qa + u * kTileBytes, 16, 1024, kSwizzle128B);
+                    const uint64_t db = smem_desc(ra + s * kTileBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kChunkB + (kk & 3) * 32) >> 4);
+                        mma_ss_warp(tm + kM * u, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_warp(&bar->s_full[u]);
+                    if (release) mma_commit_warp(&bar->empty[s]);
+                    if (last) mma_commit_warp(&bar->q_empty[u]);
+                    issued_any = true;
+                    return true;
+                };
+                auto issue_o = [&](int u, int i, bool begin, bool clean, bool release) -> bool {
+                    const int j = pos_v(i), s = j % kSlots;
+                    if (!wait(&bar->full[s], j / kSlots)) return false;
+                    if (clean && i >= mtile) {
+                        if (!wait(&bar->v_clean[s], (int)(cleaned >> s))) return false;
+                        cleaned ^= 1u << s;
+                    }
+                    if (!wait(&bar->p_full[u], pn[u])) return false;
+                    ++pn[u];
+                    tc_fence_after();
+                    const uint64_t dv = smem_desc(ra + s * kTileBytes, kChunkB, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int kk = 0; kk < kTT / 16; ++kk)
+                        mma_ts_warp(tm + kColO + D * u, tm + kM * u + 8 * kk, dv + (uint64_t)((2048 * kk) >> 4), idesc_o,
+                                    (!begin || kk > 0) ? 1u : 0u);
+                    mma_commit_warp(&bar->pv_done[u]);
+                    if (release) mma_commit_warp(&bar->empty[s]);
+                    return true;
+                };
+                if (pair) {
+                    if (n > 0)
+                        ok = wait(&bar->q_full[0], qn[0]++) && issue_s(0, 0, false, n == 1) &&
+                             wait(&bar->q_full[1], qn[1]++) && issue_s(1, 0, true, n == 1);
+                    for (int i = 0; ok && i < n; ++i) {
+                        ok = issue_o(0, i, i == 0, true, false);
+                        if (ok && i + 1 < n) ok = issue_s(0, i + 1, false, i + 2 == n);
+                        if (ok) ok = issue_o(1, i, i == 0, false, true);
+                        if (ok && i + 1 < n) ok = issue_s(1, i + 1, true, i + 2 == n);
+                    }
+                } else {
+                    if (n > 0) ok = wait(&bar->q_full[0], qn[0]++) && issue_s(0, 0, true, n <= 2);
+                    if (ok && n > 1) ok = wait(&bar->q_full[1], qn[1]++) && issue_s(1, 1, true, n <= 3);
+                    for (int i = 0; ok && i < n; i += 2) {
+                        ok = issue_o(0, i, i == 0, true, true);
+                        if (ok && i + 2 < n) ok = issue_s(0, i + 2, true, i + 4 >= n);
+                        if (ok && i + 1 < n) ok = issue_o(1, i + 1, i == 0, true, true);
+                        if (ok && i + 3 < n) ok = issue_s(1, i + 3, true, i + 5 >= n);
+                    }
+                }
+                base += 2 * n;
+                if (!ok || !advance()) break;
+                ok = more();
             }
+            if (issued_any) mma_commit_warp(&bar->mma_done);
         } else if (warp == 10) {
             // -------------------------------------------- V of the masked tiles
             int base = 0, seg = 0;
