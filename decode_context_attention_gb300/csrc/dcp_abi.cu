@@ -612,7 +612,9 @@ dcp_status_t dcp_device_status(void) {
     const int s_mla = dcp::mla_device_status(true);
     const int s_gqa = dcp::attn_tc_device_status(true);
     const int s_chunk = dcp::chunk_attention_tc_status(true);
-    const int s = s_mla < 0 || s_gqa < 0 || s_chunk < 0 ? -1 : (s_mla ? s_mla : (s_gqa ? s_gqa : s_chunk));
+    const int s_weights = dcp::chunk_weights_tc_status(true);
+    int s = 0;
+    for (int x : {s_mla, s_gqa, s_chunk, s_weights}) s = x < 0 || s < 0 ? -1 : (s ? s : x);
     if (s < 0) return fail(DCP_ERR_CUDA, "dcp_device_status: the device status word could not be read");
     if (s) return fail((dcp_status_t)s, "dcp_device_status: a tensor-core kernel gave up on a bounded wait");
     return ok();

@@ -57,6 +57,35 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// sum over i < n of floor((a i + b) / m), for b >= 0, m > 0, by Euclid's steps;
+// 32-bit divisions where the terms fit.
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    auto div = [](int64_t x, int64_t y) -> int64_t {
+        return ((x | y) >> 32) ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+    };
+    int64_t sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            const int64_t k = div(a, m);
+            sum += n * (n - 1) / 2 * k;
+            a -= k * m;
+        }
+        if (b >= m) {
+            const int64_t k = div(b, m);
+            sum += n * k;
+            b -= k * m;
+        }
+        const int64_t y = a * n + b;  // a and b below m <= 2^20, n below 2^31
+        if (y < m) break;
+        n = div(y, m);
+        b = y - n * m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
 // ---------------------------------------------------------------------------
 // The split of a ragged batch's attention.  An item is (request, rank, KV head,
 // block of `tpi` new tokens); its work is the tiles of `tt` cached tokens its

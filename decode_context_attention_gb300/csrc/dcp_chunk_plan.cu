@@ -21,29 +21,6 @@ constexpr int kMinPart = 4;   // a cut leaves at least this many tiles on both s
 constexpr int kPlanThreads = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 
-// sum over i < n of floor((a i + b) / m), for b >= 0, m > 0.
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-    int64_t sum = 0;
-    while (n > 0) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const int64_t y = a * n + b;  // below 2^19 * 2^31
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const int64_t t = m;
-        m = a;
-        a = t;
-    }
-    return sum;
-}
-
 // The work of one KV head of a (request, rank), by blocks of new tokens.
 struct HeadWork {
     int nq;       // blocks

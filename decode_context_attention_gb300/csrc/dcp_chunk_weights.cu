@@ -144,6 +144,8 @@ cudaError_t launch_weights_d(const ChunkParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t stream) {
+    cudaError_t e;
+    if (launch_chunk_weights_tc(p, dtype, stream, &e)) return e;
     return dtype == DCP_F16 ? launch_weights_d<__half>(p, stream) : launch_weights_d<__nv_bfloat16>(p, stream);
 }
 

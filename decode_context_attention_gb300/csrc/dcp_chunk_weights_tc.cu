@@ -1,0 +1,572 @@
+// dcp_chunk_weights_tc.cu -- the accumulated attention weights of
+// dcp_chunk_weights.cu on the 5th-generation tensor cores: D = 64 or 128, pages
+// of at least 8 tokens.
+//
+// With the merged log-sum-exp known a weight is one exponential and a token's sum
+// needs no other token, so the product runs transposed, tokens on M:
+//     S^T [128 tokens x up to 128 rows] = K_tile . Q_tile^T   (tcgen05, K-major both)
+//     acc[token] += sum over rows of 2^(S^T sm_scale log2e - lse2[row])
+// and a thread owns a token: its row of S^T comes from tensor memory, the rows'
+// log-sum-exps from shared memory (one address for the warp), the sum never
+// leaves its registers.  An item is a block of 256 tokens, two tiles of 128 that
+// share every tile of queries; it stays in shared memory while the queries pass
+// by, so the keys are read once (a decode step: they are all that is read) and a
+// chunk's queries are read from L2, 32 KB per 2 x 128 x 128 x D products.
+// The items, cut evenly by their number of query tiles, go to one persistent CTA
+// per SM; every CTA finds its range itself from the lengths (sums of floors, as
+// in the plan of the chunk attention).
+// Warps 0-3 and 4-7: the sums of the block's two tiles; warp 8: TMA (the next
+// block's keys while this one is worked on, a ring of query tiles); warp 9: MMAs
+// (two score buffers per tile); warp 10: the rows' log-sum-exps.
+// Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
+#include <cuda.h>
+#include <math.h>
+#include <stdlib.h>
+
+#include <type_traits>
+
+#include "dcp_chunk.cuh"
+#include "dcp_sm100.cuh"
+
+namespace dcp {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kM = 128;         // tokens of a tile, and the most query rows of one
+constexpr int kThreadsW = 384;
+constexpr int kChunkB = 128 * 128;  // 64 columns of 128 rows
+constexpr unsigned kAllLanes = 0xffffffffu;
+
+__device__ int g_weights_status;  // first bounded wait that ran out (0 if none)
+
+template <int D>
+struct WShape {
+    static constexpr int kTileBytes = (D / 64) * kChunkB;
+    static constexpr int kQSlots = D == 128 ? 3 : 6;
+    static constexpr int kMisc = kQSlots * kM * 4 + 512;
+    static constexpr int kSmem = (4 + kQSlots) * kTileBytes + kMisc + 1024;
+};
+
+struct WItem {
+    int b, rh, blk;  // request, rank * Hkv + KV head, block of 256 tokens; b = B at the end
+};
+
+struct WBars {
+    uint64_t k_full[2], k_empty[2];
+    uint64_t q_full[6], q_empty[6];  // query tiles loaded / read by the products
+    uint64_t i_full[6], i_empty[6];  // their log-sum-exps written / read
+    uint64_t s_full[2][2], s_empty[2][2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+    int plain[6];  // all the tile's rows have a finite log-sum-exp
+    WItem range[2];
+};
+static_assert(sizeof(WBars) <= 512, "barrier region too small");
+
+// An item as its tiles see it.
+struct WSeg {
+    Request q;
+    int r, hkv, tb, held;
+    int j0, nq;    // first new token that sees the block; query tiles from there on
+};
+__device__ __forceinline__ WSeg load_wseg(const ChunkParams& p, const WItem& x, int tj) {
+    WSeg s;
+    s.q = load_request(p, x.b);
+    s.r = x.rh / p.Hkv;
+    s.hkv = x.rh - s.r * p.Hkv;
+    s.tb = x.blk * 2 * kM;
+    s.held = rank_share(s.q.L, s.r, p.N);
+    s.j0 = max(0, s.tb * p.N + s.r - (s.q.L - s.q.n));
+    s.nq = (s.q.n - s.j0 + tj - 1) / tj;
+    return s;
+}
+__device__ __forceinline__ int blocks_of(const ChunkParams& p, const Request& q, int r) {
+    return q.n == 0 ? 0 : (rank_share(q.L, r, p.N) + 2 * kM - 1) / (2 * kM);
+}
+__device__ __forceinline__ WItem next_witem(const ChunkParams& p, WItem x) {
+    Request q = load_request(p, x.b);
+    if (++x.blk < blocks_of(p, q, x.rh / p.Hkv)) return x;
+    x.blk = 0;
+    for (;;) {
+        if (++x.rh >= p.N * p.Hkv) {
+            x.rh = 0;
+            do ++x.b;
+            while (x.b < p.B && load_request(p, x.b).n == 0);
+            if (x.b >= p.B) return x;
+            q = load_request(p, x.b);
+        }
+        if (blocks_of(p, q, x.rh / p.Hkv) > 0) return x;
+        if (q.L == 0 && x.rh + 1 < p.N * p.Hkv) x.rh = p.N * p.Hkv - 1;  // holds nothing anywhere
+    }
+}
+
+// The work of one KV head of a (request, rank): a block costs two (its keys and
+// its sums) and one per query tile.  Blocks before `full` meet all nq of them;
+// after that block k meets ceil((x - k m) / tj), m tokens of the request a block.
+struct WWork {
+    int nblk, full, nq;
+    int64_t x, m, tj;
+};
+__device__ WWork head_wwork(const ChunkParams& p, int64_t pair, int tj) {
+    WWork w;
+    const Request q = load_request(p, (int)(pair / p.N));
+    const int r = (int)(pair % p.N);
+    w.nblk = blocks_of(p, q, r);
+    w.nq = (q.n + tj - 1) / tj;
+    w.m = (int64_t)2 * kM * p.N;
+    w.tj = tj;
+    w.x = (int64_t)q.L - r;
+    // block k starts at the request's token k m + r: old, or the first new one, while that is <= L - n
+    const int64_t old = (int64_t)q.L - q.n - r;
+    w.full = old < 0 ? 0 : (int)min(old / w.m + 1, (int64_t)w.nblk);
+    return w;
+}
+__device__ int64_t wwork_before(const WWork& w, int k) {
+    const int f = min(k, w.full);
+    int64_t c = (int64_t)f * w.nq + 2 * (int64_t)k;
+    const int rest = k - f;  // blocks w.full .. k - 1, from the last one back: ceil((x - (k - 1) m) / tj) and up
+    if (rest > 0) c += floor_sum(rest, w.tj, w.m, w.x - (int64_t)(k - 1) * w.m + w.tj - 1);
+    return c;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsW, 1)
+    chunk_weights_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap_few,
+                            const __grid_constant__ CUtensorMap kmap, const ChunkParams p, const int few) {
+    using W = WShape<D>;
+    constexpr int kTileBytes = W::kTileBytes, kQSlots = W::kQSlots, NCH = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* qring = smem + 4 * kTileBytes;
+    float* lse_s = reinterpret_cast<float*>(qring + kQSlots * kTileBytes);
+    WBars* bar = reinterpret_cast<WBars*>(reinterpret_cast<uint8_t*>(lse_s) + kQSlots * kM * 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tj = kM / p.gq;  // new tokens of a query tile
+
+    // ------------------------------------------------ this CTA's range of items
+    {
+        int64_t* upto = reinterpret_cast<int64_t*>(smem);  // the key buffers are not in use yet
+        const int64_t npairs = (int64_t)p.B * p.N;
+        const int64_t per = (npairs + kThreadsW - 1) / kThreadsW;
+        int64_t sum = 0;
+        for (int64_t i = tid * per; i < min((tid + 1) * per, npairs); ++i) {
+            const WWork w = head_wwork(p, i, tj);
+            sum += wwork_before(w, w.nblk) * p.Hkv;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(kAllLanes, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) upto[kThreadsW + warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += upto[kThreadsW + w];
+        upto[tid] = sum;
+        __syncthreads();
+        const int64_t total = upto[kThreadsW - 1];
+        if (lane == 0 && warp < 2) {  // the first item that starts at or after this CTA's (the next one's) share
+            WItem x = {p.B, 0, 0};
+            const int c = blockIdx.x + warp;
+            const int64_t at = (int64_t)((double)total * c / gridDim.x);
+            if (c < (int)gridDim.x && at < total) {
+                int lo = 0, hi = kThreadsW - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (upto[mid] > at) hi = mid;
+                    else lo = mid + 1;
+                }
+                int64_t rem = at - (lo ? upto[lo - 1] : 0);
+                int64_t pair = lo * per;
+                WWork w = head_wwork(p, pair, tj);
+                int64_t head = wwork_before(w, w.nblk);
+                while (rem >= head * p.Hkv) {
+                    rem -= head * p.Hkv;
+                    w = head_wwork(p, ++pair, tj);
+                    head = wwork_before(w, w.nblk);
+                }
+                const int hkv = (int)(rem / head);
+                rem %= head;
+                int k0 = 0, k1 = w.nblk;
+                while (k0 < k1) {
+                    const int mid = (k0 + k1) >> 1;
+                    if (wwork_before(w, mid) >= rem) k1 = mid;
+                    else k0 = mid + 1;
+                }
+                x = {(int)(pair / p.N), (int)(pair % p.N) * p.Hkv + hkv, k0};
+                if (k0 >= w.nblk) {
+                    x.blk = w.nblk - 1;
+                    x = next_witem(p, x);
+                }
+            }
+            bar->range[warp] = x;
+        }
+    }
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar->k_full[s], 1);
+            mbar_init(&bar->k_empty[s], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&bar->s_full[u][s], 1);
+                mbar_init(&bar->s_empty[u][s], 4);
+            }
+        }
+        for (int s = 0; s < kQSlots; ++s) {
+            mbar_init(&bar->q_full[s], 1);
+            mbar_init(&bar->q_empty[s], 1);
+            mbar_init(&bar->i_full[s], 1);
+            mbar_init(&bar->i_empty[s], 8);
+        }
+        mbar_init(&bar->mma_done, 1);
+        bar->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&bar->tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&qmap);
+        tma_prefetch_map(&qmap_few);
+        tma_prefetch_map(&kmap);
+    }
+    fence_proxy_async_smem();  // the range's scratch is overwritten by copies
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+    volatile int* abort = &bar->abort;
+    int* status = &g_weights_status;
+    WItem x = bar->range[0];
+    const WItem end = bar->range[1];
+    auto more = [&]() { return x.b < p.B && !(x.b == end.b && x.rh == end.rh && x.blk == end.blk); };
+    bool issued_any = false;
+
+    if (warp == 8) {
+        // ---------------------------------------------------------------- TMA
+        const int pb = min(1 << p.page_shift, kM);
+        int it = 0, qc = 0;
+        bool ok = !p.stall_loads;
+        for (; ok && more(); x = next_witem(p, x), ++it) {
+            const WSeg g = load_wseg(p, x, tj);
+            const int kb = it & 1;
+            const int tokens = min(2 * kM, g.held - g.tb);
+            const int nseg = (tokens + pb - 1) / pb;  // at most 32: pages of 8 and up
+            int pg = 0;
+            if (lane < nseg) {  // entries of tokens that exist only
+                pg = __ldg(p.bt + (int64_t)g.r * p.bt_sn + (int64_t)x.b * p.bt_sb + ((g.tb + lane * pb) >> p.page_shift));
+                if ((unsigned)pg >= (unsigned)p.num_pages) pg = p.num_pages;  // reads zeros
+            }
+            int go = 1;
+            if (lane == 0) {
+                if (it >= 2) go = mbar_wait(&bar->k_empty[kb], ((it >> 1) - 1) & 1, status, DCP_ERR_TIMEOUT, abort);
+                if (go) mbar_arrive_expect_tx(&bar->k_full[kb], (uint32_t)(NCH * nseg * pb * 128));
+            }
+            if (!__shfl_sync(kAllLanes, go, 0)) break;
+            if (lane < nseg) {
+                const int row = lane * pb;  // token of the block: tile row / 128
+                uint8_t* dst = smem + (2 * kb + row / kM) * kTileBytes + (row % kM) * 128;
+                const int slot = (g.tb + row) & ((1 << p.page_shift) - 1);
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+                    tma_load_5d(dst + c * kChunkB, &kmap, &bar->k_full[kb], 64 * c, g.hkv, slot, pg, g.r);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                for (int k = 0; k < g.nq; ++k, ++qc) {
+                    const int s = qc % kQSlots;
+                    if (qc >= kQSlots &&
+                        !mbar_wait(&bar->q_empty[s], (qc / kQSlots - 1) & 1, status, DCP_ERR_TIMEOUT, abort)) {
+                        go = 0;
+                        break;
+                    }
+                    // a tile of few new tokens is loaded by a smaller box
+                    const int j = g.j0 + k * tj;
+                    const bool small = g.q.n - j <= few;
+                    mbar_arrive_expect_tx(&bar->q_full[s], (uint32_t)(NCH * (small ? few : tj) * p.gq * 128));
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(qring + s * kTileBytes + c * kChunkB, small ? &qmap_few : &qmap, &bar->q_full[s],
+                                    64 * c, g.hkv * p.gq, g.q.start + j);
+                }
+            }
+            qc = __shfl_sync(kAllLanes, qc, 0);
+            if (!__shfl_sync(kAllLanes, go, 0)) break;
+        }
+        // copies still in flight (only after an abort) land before the CTA ends
+        if (lane == 0 && *abort) {
+            const uint64_t t = global_timer_ns();
+            auto land = [&](uint64_t* b, int parity) {
+                while (!mbar_try_wait(b, parity & 1) && global_timer_ns() - t < kWaitLimitNs) {
+                }
+            };
+            for (int i = max(0, it - 1); i <= it; ++i) land(&bar->k_full[i & 1], i >> 1);
+            for (int i = max(0, qc - kQSlots); i < qc; ++i) land(&bar->q_full[i % kQSlots], i / kQSlots);
+        }
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------- MMA
+        // the whole warp runs along, its leader issues
+        constexpr bool kBf16 = !std::is_same<T, __half>::value;
+        const uint32_t tm = __shfl_sync(kAllLanes, tmem, 0);
+        const uint32_t ka = __shfl_sync(kAllLanes, smem_u32(smem), 0);
+        const uint32_t qa = ka + 4 * kTileBytes;
+        auto wait = [&](uint64_t* b, int parity) -> bool {
+            return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
+        };
+        int it = 0, qc = 0, sc[2] = {0, 0};
+        bool ok = true;
+        for (; ok && more(); x = next_witem(p, x), ++it) {
+            int nq, rows, two;
+            {
+                const WSeg g = load_wseg(p, x, tj);
+                nq = __shfl_sync(kAllLanes, g.nq, 0);
+                rows = __shfl_sync(kAllLanes, (g.q.n - g.j0) * p.gq, 0);
+                two = __shfl_sync(kAllLanes, g.held - g.tb > kM ? 1 : 0, 0);
+            }
+            const int kb = it & 1;
+            if (!(ok = wait(&bar->k_full[kb], it >> 1))) break;
+            for (int k = 0; k < nq; ++k, ++qc) {
+                const int s = qc % kQSlots;
+                const int cols = min(tj * p.gq, rows - k * tj * p.gq);
+                const uint32_t idesc = idesc_f16(kM, (cols + 15) & ~15, kBf16, 0, 0);
+                if (!(ok = wait(&bar->q_full[s], qc / kQSlots))) break;
+                for (int u = 0; u < 1 + two; ++u) {
+                    const int buf = sc[u] & 1;
+                    if (sc[u] >= 2 && !(ok = wait(&bar->s_empty[u][buf], (sc[u] >> 1) - 1))) break;
+                    tc_fence_after();
+                    const uint64_t da = smem_desc(ka + (2 * kb + u) * kTileBytes, 16, 1024, kSwizzle128B);
+                    const uint64_t db = smem_desc(qa + s * kTileBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kChunkB + (kk & 3) * 32) >> 4);
+                        mma_ss_warp(tm + 256 * u + kM * buf, da + off, db + off, idesc, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_warp(&bar->s_full[u][buf]);
+                    ++sc[u];
+                    issued_any = true;
+                }
+                if (!ok) break;
+                mma_commit_warp(&bar->q_empty[s]);
+            }
+            if (ok) mma_commit_warp(&bar->k_empty[kb]);
+        }
+        if (issued_any) mma_commit_warp(&bar->mma_done);
+    } else if (warp == 10) {
+        // --------------------------------------------- log-sum-exps of the rows
+        int qc = 0;
+        bool ok = true;
+        for (; ok && more(); x = next_witem(p, x)) {
+            const WSeg g = load_wseg(p, x, tj);
+            for (int k = 0; k < g.nq; ++k, ++qc) {
+                const int s = qc % kQSlots;
+                const int row0 = (g.j0 + k * tj) * p.gq, cols = min(tj * p.gq, g.q.n * p.gq - row0);
+                float l[4];
+                bool fin = true;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 4 * lane + e;
+                    l[e] = INFINITY;  // of no row, or of one that adds nothing
+                    if (c < cols) {
+                        const int row = row0 + c, j = row / p.gq;
+                        float v = p.lse[(int64_t)(g.q.start + j) * p.l_st + (int64_t)(g.hkv * p.gq + row - j * p.gq) * p.l_sh];
+                        if (!p.base2) v *= kLog2e;
+                        if (isfinite(v)) l[e] = v;
+                        else fin = false;
+                    }
+                }
+                if (qc >= kQSlots &&
+                    !(ok = __all_sync(kAllLanes, mbar_wait(&bar->i_empty[s], (qc / kQSlots - 1) & 1, status,
+                                                           DCP_ERR_TIMEOUT, abort))))
+                    break;
+                *reinterpret_cast<float4*>(lse_s + s * kM + 4 * lane) = make_float4(-l[0], -l[1], -l[2], -l[3]);
+                fin = __all_sync(kAllLanes, fin);
+                if (lane == 0) bar->plain[s] = fin;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->i_full[s]);
+            }
+        }
+    } else if (warp < 8) {
+        // --------------------------------------------------------------- sums
+        const int u = warp >> 2, m = tid & 127;
+        const uint32_t tS = tmem + 256 * u + ((uint32_t)(32 * (warp & 3)) << 16);
+        const float qscale = p.sm_scale * kLog2e;
+        const unsigned long long qs2 = pack2f(qscale, qscale);
+        auto wait = [&](uint64_t* b, int parity) -> bool {
+            return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
+        };
+        int qc = 0, sc = 0;
+        bool ok = true;
+        for (; ok && more(); x = next_witem(p, x)) {
+            const WSeg g = load_wseg(p, x, tj);
+            const int tok = g.tb + kM * u + m;
+            const bool active = g.tb + kM * u < g.held;
+            float total = 0.f;
+            for (int k = 0; k < g.nq; ++k, ++qc) {
+                const int s = qc % kQSlots;
+                if (!(ok = wait(&bar->i_full[s], qc / kQSlots))) break;
+                if (active) {
+                    const int buf = sc & 1;
+                    if (!(ok = wait(&bar->s_full[u][buf], sc >> 1))) break;
+                    ++sc;
+                    tc_fence_after();
+                    const int j = g.j0 + k * tj;
+                    const int cols = min(tj, g.q.n - j) * p.gq;
+                    // every row has a finite log-sum-exp and sees every token of the tile
+                    const bool plain = *(volatile int*)&bar->plain[s] != 0 &&
+                                       visible(p, g.q, j, g.r) >= min(g.held, g.tb + kM * (u + 1));
+                    const float* nl = lse_s + s * kM;  // negated
+                    unsigned long long acc[2] = {0ull, 0ull};
+                    float part = 0.f;
+                    uint32_t va[32], vb[32];
+                    tmem_ld32<0>(tS + kM * buf, va);
+                    auto columns = [&](uint32_t(&v)[32], int c0) {
+                        if (plain && c0 + 32 <= cols) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + c0 + e);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    unsigned long long f;
+                                    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+                                        : "=l"(f)
+                                        : "l"(pack2(v[e + 2 * h], v[e + 2 * h + 1])), "l"(qs2), "l"(h ? l.y : l.x));
+                                    const float2 y = unpack2(f);
+                                    asm("add.rn.f32x2 %0, %0, %1;"
+                                        : "+l"(acc[h])
+                                        : "l"(pack2f(exp2_fast(y.x), exp2_fast(y.y))));
+                                }
+                            }
+                        } else {
+                            int t = c0 / p.gq, h = c0 - t * p.gq;
+                            int lim = visible(p, g.q, j + t, g.r);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                if (c0 + e < cols) {
+                                    const float l = nl[c0 + e];
+                                    const float w = exp2_fast(fmaf(__uint_as_float(v[e]), qscale, l));
+                                    if (tok < lim && l != -INFINITY) part += w;
+                                    if (++h == p.gq) {
+                                        h = 0;
+                                        lim = visible(p, g.q, j + ++t, g.r);
+                                    }
+                                }
+                            }
+                        }
+                    };
+                    for (int c0 = 0; c0 < cols; c0 += 64) {
+                        tmem_wait_ld();
+                        pin(va);
+                        if (c0 + 32 < cols) tmem_ld32<0>(tS + kM * buf + c0 + 32, vb);
+                        columns(va, c0);
+                        if (c0 + 32 < cols) {
+                            tmem_wait_ld();
+                            pin(vb);
+                            if (c0 + 64 < cols) tmem_ld32<0>(tS + kM * buf + c0 + 64, va);
+                            columns(vb, c0 + 32);
+                        }
+                    }
+                    const float2 a0 = unpack2(acc[0]), a1 = unpack2(acc[1]);
+                    total += ((a0.x + a0.y) + (a1.x + a1.y)) + part;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->s_empty[u][buf]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->i_empty[s]);
+            }
+            if (ok && tok < g.held) {
+                float* a = p.acc + (int64_t)g.r * p.a_sn + (int64_t)x.b * p.a_sb + (int64_t)g.hkv * p.a_sh + tok;
+                *a = (tok * p.N + g.r < g.q.L - g.q.n ? *a : 0.f) + total;
+            }
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        if (lane == 0 && issued_any) {
+            // every MMA this CTA issued has completed before its tensor memory goes
+            const uint64_t t = global_timer_ns();
+            while (!mbar_try_wait(&bar->mma_done, 0) && global_timer_ns() - t < kWaitLimitNs) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_weights_tc(const ChunkParams& p, const CUtensorMap (&maps)[3], int few, cudaStream_t stream) {
+    const void* k = (const void*)chunk_weights_tc_kernel<T, D>;
+    // the shared-memory opt-in is a per-device function attribute
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, WShape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    chunk_weights_tc_kernel<T, D>
+        <<<device_sm_count(), kThreadsW, WShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, few);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
+    if ((p.D != 64 && p.D != 128) || p.page_shift < 3) return false;  // boxes hold whole 8-row swizzle atoms
+    const EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const CUtensorMapDataType dt = dtype == DCP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    // a dimension of extent 1 is never stepped over: give it a nominal stride
+    auto stride = [](int64_t extent, int64_t bytes) -> cuuint64_t { return (cuuint64_t)(extent > 1 ? bytes : 256); };
+    CUtensorMap maps[3];
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    // query tiles of up to 128 / gq new tokens, and of as few as a request has on average
+    const int tj = kM / p.gq;
+    const int few = (int)(((int64_t)p.T + p.B - 1) / p.B < tj ? ((int64_t)p.T + p.B - 1) / p.B : tj);
+    for (int m = 0; m < 2; ++m) {
+        const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.T};
+        const cuuint64_t strides[2] = {stride(p.H, p.q_sh), stride(p.T, p.q_st)};
+        const cuuint32_t box[3] = {64, (cuuint32_t)p.gq, (cuuint32_t)(m ? few : tj)};
+        if (enc(&maps[m], dt, 3, const_cast<unsigned char*>(p.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    {
+        const int64_t rows = (int64_t)1 << p.page_shift;
+        const cuuint64_t dims[5] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, (cuuint64_t)rows, (cuuint64_t)p.num_pages,
+                                    (cuuint64_t)p.N};
+        const cuuint64_t strides[4] = {stride(p.Hkv, p.k_sh), stride(rows, p.k_st), stride(p.num_pages, p.k_sp),
+                                       stride(p.N, p.k_sn)};
+        const cuuint32_t box[5] = {64, 1, (cuuint32_t)(rows < kM ? rows : kM), 1, 1};
+        if (enc(&maps[2], dt, 5, p.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;  // strides a tensor map cannot describe: the register-tiled kernel takes it
+    }
+    ChunkParams q = p;
+    // DCP_TEST_STALL_LOADS=1 (tests of the failure path only): no loads are
+    // issued, so the first wait on them runs out.  Unset in normal use.
+    const char* stall = getenv("DCP_TEST_STALL_LOADS");
+    q.stall_loads = stall && stall[0] == '1';
+    if (p.D == 128)
+        *err = dtype == DCP_F16 ? launch_weights_tc<__half, 128>(q, maps, few, stream)
+                                : launch_weights_tc<__nv_bfloat16, 128>(q, maps, few, stream);
+    else
+        *err = dtype == DCP_F16 ? launch_weights_tc<__half, 64>(q, maps, few, stream)
+                                : launch_weights_tc<__nv_bfloat16, 64>(q, maps, few, stream);
+    return true;
+}
+
+int chunk_weights_tc_status(bool clear) {
+    int s = 0;
+    if (cudaMemcpyFromSymbol(&s, g_weights_status, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && s) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_weights_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return s;
+}
+
+}  // namespace dcp

@@ -209,6 +209,8 @@ size_t chunk_attention_tc_workspace(int D);
 bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
 int chunk_attention_tc_status(bool clear);
 cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t stream);
+bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
+int chunk_weights_tc_status(bool clear);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).
