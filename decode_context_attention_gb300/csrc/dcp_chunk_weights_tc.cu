@@ -66,42 +66,63 @@ struct WBars {
 };
 static_assert(sizeof(WBars) <= 512, "barrier region too small");
 
-// An item as its tiles see it.
-struct WSeg {
-    Request q;
-    int r, hkv, tb, held;
-    int j0, nq;    // first new token that sees the block; query tiles from there on
-};
-__device__ __forceinline__ WSeg load_wseg(const ChunkParams& p, const WItem& x, int tj) {
-    WSeg s;
-    s.q = load_request(p, x.b);
-    s.r = x.rh / p.Hkv;
-    s.hkv = x.rh - s.r * p.Hkv;
-    s.tb = x.blk * 2 * kM;
-    s.held = rank_share(s.q.L, s.r, p.N);
-    s.j0 = max(0, s.tb * p.N + s.r - (s.q.L - s.q.n));
-    s.nq = (s.q.n - s.j0 + tj - 1) / tj;
-    return s;
-}
 __device__ __forceinline__ int blocks_of(const ChunkParams& p, const Request& q, int r) {
     return q.n == 0 ? 0 : (rank_share(q.L, r, p.N) + 2 * kM - 1) / (2 * kM);
 }
-__device__ __forceinline__ WItem next_witem(const ChunkParams& p, WItem x) {
-    Request q = load_request(p, x.b);
-    if (++x.blk < blocks_of(p, q, x.rh / p.Hkv)) return x;
-    x.blk = 0;
-    for (;;) {
-        if (++x.rh >= p.N * p.Hkv) {
-            x.rh = 0;
-            do ++x.b;
-            while (x.b < p.B && load_request(p, x.b).n == 0);
-            if (x.b >= p.B) return x;
-            q = load_request(p, x.b);
-        }
-        if (blocks_of(p, q, x.rh / p.Hkv) > 0) return x;
-        if (q.L == 0 && x.rh + 1 < p.N * p.Hkv) x.rh = p.N * p.Hkv - 1;  // holds nothing anywhere
+// The items in order, and what their tiles need to know; divisions only where
+// the rank or the request changes.
+struct WCursor {
+    Request q;
+    int b, r, hkv, blk;  // b = B at the end
+    int nblk, held, nq_all;
+    // the current item
+    int tb, j0, nq;      // first token; first new token that sees the block; query tiles from there on
+
+    __device__ __forceinline__ void rank(const ChunkParams& p) {  // the pair (b, r) has changed
+        held = q.n == 0 ? 0 : rank_share(q.L, r, p.N);
+        nblk = (held + 2 * kM - 1) / (2 * kM);
     }
-}
+    __device__ __forceinline__ void item(const ChunkParams& p, int tj) {
+        tb = blk * 2 * kM;
+        j0 = max(0, tb * p.N + r - (q.L - q.n));
+        nq = j0 == 0 ? nq_all : (q.n - j0 + tj - 1) / tj;
+    }
+    __device__ __forceinline__ void start(const ChunkParams& p, const WItem& x, int tj) {
+        b = x.b;
+        if (b >= p.B) return;
+        r = x.rh / p.Hkv;
+        hkv = x.rh - r * p.Hkv;
+        blk = x.blk;
+        q = load_request(p, b);
+        nq_all = (q.n + tj - 1) / tj;
+        rank(p);
+        item(p, tj);
+    }
+    // the next item that has tokens
+    __device__ __forceinline__ void next(const ChunkParams& p, int tj) {
+        if (++blk >= nblk) {
+            blk = 0;
+            if (++hkv >= p.Hkv) {
+                hkv = 0;
+                do {
+                    if (++r >= p.N || held == 0) {  // a rank that holds nothing: nor do the later ones
+                        r = 0;
+                        do {
+                            if (++b >= p.B) return;
+                            q = load_request(p, b);
+                        } while (q.n == 0 || q.L == 0);
+                        nq_all = (q.n + tj - 1) / tj;
+                    }
+                    rank(p);
+                } while (nblk == 0);
+            }
+        }
+        item(p, tj);
+    }
+    __device__ __forceinline__ bool before(const ChunkParams& p, const WItem& end) const {
+        return b < p.B && !(b == end.b && r * p.Hkv + hkv == end.rh && blk == end.blk);
+    }
+};
 
 // The work of one KV head of a (request, rank): a block costs two (its keys and
 // its sums) and one per query tile.  Blocks before `full` meet all nq of them;
@@ -197,8 +218,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 }
                 x = {(int)(pair / p.N), (int)(pair % p.N) * p.Hkv + hkv, k0};
                 if (k0 >= w.nblk) {
+                    WCursor z;
                     x.blk = w.nblk - 1;
-                    x = next_witem(p, x);
+                    z.start(p, x, tj);
+                    z.next(p, tj);
+                    x = {z.b, z.r * p.Hkv + z.hkv, z.blk};
+                    if (z.b >= p.B) x = {p.B, 0, 0};
                 }
             }
             bar->range[warp] = x;
@@ -239,9 +264,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
     int* status = &g_weights_status;
-    WItem x = bar->range[0];
     const WItem end = bar->range[1];
-    auto more = [&]() { return x.b < p.B && !(x.b == end.b && x.rh == end.rh && x.blk == end.blk); };
+    WCursor g;
+    g.start(p, bar->range[0], tj);
+    auto more = [&]() { return g.before(p, end); };
     bool issued_any = false;
 
     if (warp == 8) {
@@ -249,14 +275,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         const int pb = min(1 << p.page_shift, kM);
         int it = 0, qc = 0;
         bool ok = !p.stall_loads;
-        for (; ok && more(); x = next_witem(p, x), ++it) {
-            const WSeg g = load_wseg(p, x, tj);
+        for (; ok && more(); g.next(p, tj), ++it) {
             const int kb = it & 1;
             const int tokens = min(2 * kM, g.held - g.tb);
             const int nseg = (tokens + pb - 1) / pb;  // at most 32: pages of 8 and up
             int pg = 0;
             if (lane < nseg) {  // entries of tokens that exist only
-                pg = __ldg(p.bt + (int64_t)g.r * p.bt_sn + (int64_t)x.b * p.bt_sb + ((g.tb + lane * pb) >> p.page_shift));
+                pg = __ldg(p.bt + (int64_t)g.r * p.bt_sn + (int64_t)g.b * p.bt_sb + ((g.tb + lane * pb) >> p.page_shift));
                 if ((unsigned)pg >= (unsigned)p.num_pages) pg = p.num_pages;  // reads zeros
             }
             int go = 1;
@@ -315,13 +340,12 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         auto wait = [&](uint64_t* b, int parity) -> bool {
             return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
         };
-        int it = 0, qc = 0, sc[2] = {0, 0};
+        int it = 0, qc = 0, sc0 = 0, sc1 = 0;
         bool ok = true;
-        for (; ok && more(); x = next_witem(p, x), ++it) {
+        for (; ok && more(); g.next(p, tj), ++it) {
             int nq, rows, two;
             {
-                const WSeg g = load_wseg(p, x, tj);
-                nq = __shfl_sync(kAllLanes, g.nq, 0);
+                    nq = __shfl_sync(kAllLanes, g.nq, 0);
                 rows = __shfl_sync(kAllLanes, (g.q.n - g.j0) * p.gq, 0);
                 two = __shfl_sync(kAllLanes, g.held - g.tb > kM ? 1 : 0, 0);
             }
@@ -332,9 +356,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 const int cols = min(tj * p.gq, rows - k * tj * p.gq);
                 const uint32_t idesc = idesc_f16(kM, (cols + 15) & ~15, kBf16, 0, 0);
                 if (!(ok = wait(&bar->q_full[s], qc / kQSlots))) break;
-                for (int u = 0; u < 1 + two; ++u) {
-                    const int buf = sc[u] & 1;
-                    if (sc[u] >= 2 && !(ok = wait(&bar->s_empty[u][buf], (sc[u] >> 1) - 1))) break;
+                auto issue = [&](int u, int& sc) -> bool {
+                    const int buf = sc & 1;
+                    if (sc >= 2 && !wait(&bar->s_empty[u][buf], (sc >> 1) - 1)) return false;
                     tc_fence_after();
                     const uint64_t da = smem_desc(ka + (2 * kb + u) * kTileBytes, 16, 1024, kSwizzle128B);
                     const uint64_t db = smem_desc(qa + s * kTileBytes, 16, 1024, kSwizzle128B);
@@ -344,9 +368,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                         mma_ss_warp(tm + 256 * u + kM * buf, da + off, db + off, idesc, kk > 0 ? 1u : 0u);
                     }
                     mma_commit_warp(&bar->s_full[u][buf]);
-                    ++sc[u];
+                    ++sc;
                     issued_any = true;
-                }
+                    return true;
+                };
+                ok = issue(0, sc0) && (!two || issue(1, sc1));
                 if (!ok) break;
                 mma_commit_warp(&bar->q_empty[s]);
             }
@@ -357,8 +383,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         // --------------------------------------------- log-sum-exps of the rows
         int qc = 0;
         bool ok = true;
-        for (; ok && more(); x = next_witem(p, x)) {
-            const WSeg g = load_wseg(p, x, tj);
+        for (; ok && more(); g.next(p, tj)) {
             for (int k = 0; k < g.nq; ++k, ++qc) {
                 const int s = qc % kQSlots;
                 const int row0 = (g.j0 + k * tj) * p.gq, cols = min(tj * p.gq, g.q.n * p.gq - row0);
@@ -398,10 +423,14 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         };
         int qc = 0, sc = 0;
         bool ok = true;
-        for (; ok && more(); x = next_witem(p, x)) {
-            const WSeg g = load_wseg(p, x, tj);
+        for (; ok && more(); g.next(p, tj)) {
             const int tok = g.tb + kM * u + m;
             const bool active = g.tb + kM * u < g.held;
+            float* a = p.acc + (int64_t)g.r * p.a_sn + (int64_t)g.b * p.a_sb + (int64_t)g.hkv * p.a_sh + tok;
+            const float before = tok < g.held && tok * p.N + g.r < g.q.L - g.q.n ? *a : 0.f;
+            // new token j sees this thread's token when L - n + j >= tok N + r
+            const int from = tok * p.N + g.r - (g.q.L - g.q.n);
+            const int all = (min(g.held, g.tb + kM * (u + 1)) - 1) * p.N + g.r - (g.q.L - g.q.n);  // and the whole tile
             float total = 0.f;
             for (int k = 0; k < g.nq; ++k, ++qc) {
                 const int s = qc % kQSlots;
@@ -414,11 +443,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                     const int j = g.j0 + k * tj;
                     const int cols = min(tj, g.q.n - j) * p.gq;
                     // every row has a finite log-sum-exp and sees every token of the tile
-                    const bool plain = *(volatile int*)&bar->plain[s] != 0 &&
-                                       visible(p, g.q, j, g.r) >= min(g.held, g.tb + kM * (u + 1));
+                    const bool plain = *(volatile int*)&bar->plain[s] != 0 && j >= all;
+                    const int first = (from - j) * p.gq;  // the first column that sees this token
                     const float* nl = lse_s + s * kM;  // negated
                     unsigned long long acc[2] = {0ull, 0ull};
-                    float part = 0.f;
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
                     uint32_t va[32], vb[32];
                     tmem_ld32<0>(tS + kM * buf, va);
                     auto columns = [&](uint32_t(&v)[32], int c0) {
@@ -439,18 +468,16 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                                 }
                             }
                         } else {
-                            int t = c0 / p.gq, h = c0 - t * p.gq;
-                            int lim = visible(p, g.q, j + t, g.r);
+                            // columns of no row, and of rows that add nothing, hold -infinity
+                            // here; their scores may be anything
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (c0 + e < cols) {
-                                    const float l = nl[c0 + e];
-                                    const float w = exp2_fast(fmaf(__uint_as_float(v[e]), qscale, l));
-                                    if (tok < lim && l != -INFINITY) part += w;
-                                    if (++h == p.gq) {
-                                        h = 0;
-                                        lim = visible(p, g.q, j + ++t, g.r);
-                                    }
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 l4 = *reinterpret_cast<const float4*>(nl + c0 + e);
+                                const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    const float w = exp2_fast(fmaf(__uint_as_float(v[e + h]), qscale, l[h]));
+                                    part[h] += c0 + e + h >= first && l[h] != -INFINITY ? w : 0.f;
                                 }
                             }
                         }
@@ -468,7 +495,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                         }
                     }
                     const float2 a0 = unpack2(acc[0]), a1 = unpack2(acc[1]);
-                    total += ((a0.x + a0.y) + (a1.x + a1.y)) + part;
+                    total += ((a0.x + a0.y) + (a1.x + a1.y)) + ((part[0] + part[1]) + (part[2] + part[3]));
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar->s_empty[u][buf]);
@@ -476,10 +503,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->i_empty[s]);
             }
-            if (ok && tok < g.held) {
-                float* a = p.acc + (int64_t)g.r * p.a_sn + (int64_t)x.b * p.a_sb + (int64_t)g.hkv * p.a_sh + tok;
-                *a = (tok * p.N + g.r < g.q.L - g.q.n ? *a : 0.f) + total;
-            }
+            if (ok && tok < g.held) *a = before + total;
         }
     }
 
