@@ -15,9 +15,12 @@
 // The items, cut evenly by their number of query tiles, go to one persistent CTA
 // per SM; every CTA finds its range itself from the lengths (sums of floors, as
 // in the plan of the chunk attention).
-// Warps 0-3 and 4-7: the sums of the block's two tiles; warp 8: TMA (the next
-// block's keys while this one is worked on, a ring of query tiles); warp 9: MMAs
-// (two score buffers per tile); warp 10: the rows' log-sum-exps.
+// Warps 0-15: the sums, four warps for each of the block's two tiles and of the
+// two score buffers (query tiles alternate; at the end of an item one of the two
+// adds its sum to what the other has written): with eight warps the waits of a
+// tile were half its time.  Warp 16: TMA (the next block's keys while this one is
+// worked on, a ring of query tiles); warp 17: MMAs; warps 18 and 19: the
+// log-sum-exps of the even and the odd query tiles' rows.
 // Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
 #include <cuda.h>
 #include <math.h>
@@ -35,7 +38,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kM = 128;         // tokens of a tile, and the most query rows of one
-constexpr int kThreadsW = 384;
+constexpr int kThreadsW = 640;
 constexpr int kChunkB = 128 * 128;  // 64 columns of 128 rows
 constexpr unsigned kAllLanes = 0xffffffffu;
 
@@ -45,7 +48,7 @@ template <int D>
 struct WShape {
     static constexpr int kTileBytes = (D / 64) * kChunkB;
     static constexpr int kQSlots = D == 128 ? 3 : 6;
-    static constexpr int kMisc = kQSlots * kM * 4 + 512;
+    static constexpr int kMisc = 2 * kM * 4 + 512;
     static constexpr int kSmem = (4 + kQSlots) * kTileBytes + kMisc + 1024;
 };
 
@@ -56,12 +59,13 @@ struct WItem {
 struct WBars {
     uint64_t k_full[2], k_empty[2];
     uint64_t q_full[6], q_empty[6];  // query tiles loaded / read by the products
-    uint64_t i_full[6], i_empty[6];  // their log-sum-exps written / read
+    uint64_t i_full[2], i_empty[2];  // the even and odd ones' log-sum-exps written / read
     uint64_t s_full[2][2], s_empty[2][2];
+    uint64_t x_full[2][4];           // an item's first sum written, by tile and item
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
-    int plain[6];  // all the tile's rows have a finite log-sum-exp
+    int plain[2];  // all the tile's rows have a finite log-sum-exp
     WItem range[2];
 };
 static_assert(sizeof(WBars) <= 512, "barrier region too small");
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* qring = smem + 4 * kTileBytes;
     float* lse_s = reinterpret_cast<float*>(qring + kQSlots * kTileBytes);
-    WBars* bar = reinterpret_cast<WBars*>(reinterpret_cast<uint8_t*>(lse_s) + kQSlots * kM * 4);
+    WBars* bar = reinterpret_cast<WBars*>(lse_s + 2 * kM);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tj = kM / p.gq;  // new tokens of a query tile
 
@@ -233,6 +237,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar->k_full[s], 1);
             mbar_init(&bar->k_empty[s], 1);
+            mbar_init(&bar->i_full[s], 1);
+            mbar_init(&bar->i_empty[s], 8);
+            for (int i = 0; i < 4; ++i) mbar_init(&bar->x_full[s][i], 4);
             for (int u = 0; u < 2; ++u) {
                 mbar_init(&bar->s_full[u][s], 1);
                 mbar_init(&bar->s_empty[u][s], 4);
@@ -241,18 +248,16 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         for (int s = 0; s < kQSlots; ++s) {
             mbar_init(&bar->q_full[s], 1);
             mbar_init(&bar->q_empty[s], 1);
-            mbar_init(&bar->i_full[s], 1);
-            mbar_init(&bar->i_empty[s], 8);
         }
         mbar_init(&bar->mma_done, 1);
         bar->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(&bar->tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 16 && lane == 0) {
         tma_prefetch_map(&qmap);
         tma_prefetch_map(&qmap_few);
         tma_prefetch_map(&kmap);
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     auto more = [&]() { return g.before(p, end); };
     bool issued_any = false;
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---------------------------------------------------------------- TMA
         const int pb = min(1 << p.page_shift, kM);
         int it = 0, qc = 0;
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
             for (int i = max(0, it - 1); i <= it; ++i) land(&bar->k_full[i & 1], i >> 1);
             for (int i = max(0, qc - kQSlots); i < qc; ++i) land(&bar->q_full[i % kQSlots], i / kQSlots);
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ---------------------------------------------------------------- MMA
         // the whole warp runs along, its leader issues
         constexpr bool kBf16 = !std::is_same<T, __half>::value;
@@ -340,7 +345,8 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         auto wait = [&](uint64_t* b, int parity) -> bool {
             return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
         };
-        int it = 0, qc = 0, sc0 = 0, sc1 = 0;
+        int it = 0, qc = 0;
+        unsigned used = 0u;  // phase of s_empty by tile and buffer (a barrier's phase before its first counts as done)
         bool ok = true;
         for (; ok && more(); g.next(p, tj), ++it) {
             int nq, rows, two;
@@ -356,9 +362,11 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 const int cols = min(tj * p.gq, rows - k * tj * p.gq);
                 const uint32_t idesc = idesc_f16(kM, (cols + 15) & ~15, kBf16, 0, 0);
                 if (!(ok = wait(&bar->q_full[s], qc / kQSlots))) break;
-                auto issue = [&](int u, int& sc) -> bool {
-                    const int buf = sc & 1;
-                    if (sc >= 2 && !wait(&bar->s_empty[u][buf], (sc >> 1) - 1)) return false;
+                const int buf = qc & 1;
+                for (int u = 0; u < 1 + two; ++u) {
+                    const unsigned bit = 1u << (2 * u + buf);
+                    if (!(ok = wait(&bar->s_empty[u][buf], used & bit ? 0 : 1))) break;
+                    used ^= bit;
                     tc_fence_after();
                     const uint64_t da = smem_desc(ka + (2 * kb + u) * kTileBytes, 16, 1024, kSwizzle128B);
                     const uint64_t db = smem_desc(qa + s * kTileBytes, 16, 1024, kSwizzle128B);
@@ -368,24 +376,22 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                         mma_ss_warp(tm + 256 * u + kM * buf, da + off, db + off, idesc, kk > 0 ? 1u : 0u);
                     }
                     mma_commit_warp(&bar->s_full[u][buf]);
-                    ++sc;
                     issued_any = true;
-                    return true;
-                };
-                ok = issue(0, sc0) && (!two || issue(1, sc1));
+                }
                 if (!ok) break;
                 mma_commit_warp(&bar->q_empty[s]);
             }
             if (ok) mma_commit_warp(&bar->k_empty[kb]);
         }
         if (issued_any) mma_commit_warp(&bar->mma_done);
-    } else if (warp == 10) {
-        // --------------------------------------------- log-sum-exps of the rows
+    } else if (warp >= 18) {
+        // ------------------------- log-sum-exps of the even (warp 18) and odd tiles' rows
+        const int h = warp - 18;
         int qc = 0;
         bool ok = true;
         for (; ok && more(); g.next(p, tj)) {
             for (int k = 0; k < g.nq; ++k, ++qc) {
-                const int s = qc % kQSlots;
+                if ((qc & 1) != h) continue;
                 const int row0 = (g.j0 + k * tj) * p.gq, cols = min(tj * p.gq, g.q.n * p.gq - row0);
                 float l[4];
                 bool fin = true;
@@ -394,63 +400,68 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                     const int c = 4 * lane + e;
                     l[e] = INFINITY;  // of no row, or of one that adds nothing
                     if (c < cols) {
-                        const int row = row0 + c, j = row / p.gq;
-                        float v = p.lse[(int64_t)(g.q.start + j) * p.l_st + (int64_t)(g.hkv * p.gq + row - j * p.gq) * p.l_sh];
+                        const int t = c / p.gq;
+                        float v = p.lse[(int64_t)(g.q.start + g.j0 + k * tj + t) * p.l_st +
+                                        (int64_t)(g.hkv * p.gq + c - t * p.gq) * p.l_sh];
                         if (!p.base2) v *= kLog2e;
                         if (isfinite(v)) l[e] = v;
                         else fin = false;
                     }
                 }
-                if (qc >= kQSlots &&
-                    !(ok = __all_sync(kAllLanes, mbar_wait(&bar->i_empty[s], (qc / kQSlots - 1) & 1, status,
+                if (qc >= 2 &&
+                    !(ok = __all_sync(kAllLanes, mbar_wait(&bar->i_empty[h], ((qc >> 1) - 1) & 1, status,
                                                            DCP_ERR_TIMEOUT, abort))))
                     break;
-                *reinterpret_cast<float4*>(lse_s + s * kM + 4 * lane) = make_float4(-l[0], -l[1], -l[2], -l[3]);
+                *reinterpret_cast<float4*>(lse_s + h * kM + 4 * lane) = make_float4(-l[0], -l[1], -l[2], -l[3]);
                 fin = __all_sync(kAllLanes, fin);
-                if (lane == 0) bar->plain[s] = fin;
+                if (lane == 0) bar->plain[h] = fin;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->i_full[s]);
+                if (lane == 0) mbar_arrive(&bar->i_full[h]);
             }
         }
-    } else if (warp < 8) {
+    } else {
         // --------------------------------------------------------------- sums
-        const int u = warp >> 2, m = tid & 127;
-        const uint32_t tS = tmem + 256 * u + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int u = (warp >> 2) & 1, buf = warp >> 3, m = tid & 127;
+        const uint32_t tS = tmem + 256 * u + kM * buf + ((uint32_t)(32 * (warp & 3)) << 16);
         const float qscale = p.sm_scale * kLog2e;
         const unsigned long long qs2 = pack2f(qscale, qscale);
+        const float* nl = lse_s + buf * kM;  // negated log-sum-exps
         auto wait = [&](uint64_t* b, int parity) -> bool {
             return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
         };
-        int qc = 0, sc = 0;
+        int qc = 0, sn = 0, xn = 0;
         bool ok = true;
         for (; ok && more(); g.next(p, tj)) {
             const int tok = g.tb + kM * u + m;
             const bool active = g.tb + kM * u < g.held;
+            const int skip = (buf - qc) & 1;         // the item's first tile of this buffer
+            const bool lead = skip == 0;             // whose warps write first
+            qc += g.nq;
+            if (skip >= g.nq) continue;              // an item of one tile: the other warps'
             float* a = p.acc + (int64_t)g.r * p.a_sn + (int64_t)g.b * p.a_sb + (int64_t)g.hkv * p.a_sh + tok;
-            const float before = tok < g.held && tok * p.N + g.r < g.q.L - g.q.n ? *a : 0.f;
+            const float before = lead && tok < g.held && tok * p.N + g.r < g.q.L - g.q.n ? *a : 0.f;
             // new token j sees this thread's token when L - n + j >= tok N + r
             const int from = tok * p.N + g.r - (g.q.L - g.q.n);
             const int all = (min(g.held, g.tb + kM * (u + 1)) - 1) * p.N + g.r - (g.q.L - g.q.n);  // and the whole tile
             float total = 0.f;
-            for (int k = 0; k < g.nq; ++k, ++qc) {
-                const int s = qc % kQSlots;
-                if (!(ok = wait(&bar->i_full[s], qc / kQSlots))) break;
+            for (int k = skip; k < g.nq; k += 2) {
+                if (!(ok = wait(&bar->i_full[buf], (qc - g.nq + k) >> 1))) break;
                 if (active) {
-                    const int buf = sc & 1;
-                    if (!(ok = wait(&bar->s_full[u][buf], sc >> 1))) break;
-                    ++sc;
+                    if (!(ok = wait(&bar->s_full[u][buf], sn))) break;
+                    ++sn;
                     tc_fence_after();
                     const int j = g.j0 + k * tj;
                     const int cols = min(tj, g.q.n - j) * p.gq;
                     // every row has a finite log-sum-exp and sees every token of the tile
-                    const bool plain = *(volatile int*)&bar->plain[s] != 0 && j >= all;
+                    const bool plain = *(volatile int*)&bar->plain[buf] != 0 && j >= all;
                     const int first = (from - j) * p.gq;  // the first column that sees this token
-                    const float* nl = lse_s + s * kM;  // negated
                     unsigned long long acc[2] = {0ull, 0ull};
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t va[32], vb[32];
-                    tmem_ld32<0>(tS + kM * buf, va);
-                    auto columns = [&](uint32_t(&v)[32], int c0) {
+                    float part[2] = {0.f, 0.f};
+                    for (int c0 = 0; c0 < cols; c0 += 32) {
+                        uint32_t v[32];
+                        tmem_ld32<0>(tS + c0, v);
+                        tmem_wait_ld();
+                        pin(v);
                         if (plain && c0 + 32 <= cols) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
@@ -477,40 +488,45 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 #pragma unroll
                                 for (int h = 0; h < 4; ++h) {
                                     const float w = exp2_fast(fmaf(__uint_as_float(v[e + h]), qscale, l[h]));
-                                    part[h] += c0 + e + h >= first && l[h] != -INFINITY ? w : 0.f;
+                                    part[h & 1] += c0 + e + h >= first && l[h] != -INFINITY ? w : 0.f;
                                 }
                             }
                         }
-                    };
-                    for (int c0 = 0; c0 < cols; c0 += 64) {
-                        tmem_wait_ld();
-                        pin(va);
-                        if (c0 + 32 < cols) tmem_ld32<0>(tS + kM * buf + c0 + 32, vb);
-                        columns(va, c0);
-                        if (c0 + 32 < cols) {
-                            tmem_wait_ld();
-                            pin(vb);
-                            if (c0 + 64 < cols) tmem_ld32<0>(tS + kM * buf + c0 + 64, va);
-                            columns(vb, c0 + 32);
-                        }
                     }
                     const float2 a0 = unpack2(acc[0]), a1 = unpack2(acc[1]);
-                    total += ((a0.x + a0.y) + (a1.x + a1.y)) + ((part[0] + part[1]) + (part[2] + part[3]));
+                    total += ((a0.x + a0.y) + (a1.x + a1.y)) + (part[0] + part[1]);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar->s_empty[u][buf]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->i_empty[s]);
+                if (lane == 0) mbar_arrive(&bar->i_empty[buf]);
             }
-            if (ok && tok < g.held) *a = before + total;
+            // the sums of an item's even and odd tiles, in a fixed order.  The writer is
+            // at most three items ahead of the other warps: the score buffers hold it
+            // back there.
+            if (g.nq > 1) {
+                if (lead) {
+                    if (ok && tok < g.held) __stcg(a, before + total);
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->x_full[u][xn & 3]);
+                } else {
+                    ok = ok && wait(&bar->x_full[u][xn & 3], xn >> 2);
+                    __threadfence();
+                    if (ok && tok < g.held) __stcg(a, __ldcg(a) + total);
+                }
+                ++xn;
+            } else if (ok && tok < g.held) {
+                *a = before + total;
+            }
         }
     }
 
     // --------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         if (lane == 0 && issued_any) {
             // every MMA this CTA issued has completed before its tensor memory goes
             const uint64_t t = global_timer_ns();
