@@ -335,7 +335,8 @@ dcp_status_t dcp_cache_evict_paged(int dtype, int N, int B, int Hkv, int D,
         return fail(DCP_ERR_INVALID_ARG, "%s: destination table rows of %d entries; %lld needed for %lld local tokens",
                     who, dst_max_pages, (long long)need, (long long)kcap);
     const int64_t rb = (int64_t)D * 2;
-    if (kcap * (rb / 16) >= (1ll << 30) || ((kcap * (rb / 16) + 255) / 256) * N * B * Hkv >= (1ll << 31))
+    // 8 CTAs a problem, and a few rows a CTA, stay below 2^31 CTAs
+    if (8 * (int64_t)N * B * Hkv >= (1ll << 31) || (kcap / 8 + 1) * N * B * Hkv >= (1ll << 31))
         return fail(DCP_ERR_INVALID_ARG, "%s: too many rows to move", who);
     if (B == 0 || cap == 0 || kcap == 0) return ok();
     if (!k_pages || !v_pages || !block_table || !seq_lens || !acc || !keep_lens || !dst_table || !kept || !acc_out)
