@@ -18,7 +18,8 @@
 namespace dcp {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendCtas = 8;  // per SM: 64 registers a thread, 1024 threads with 64 bytes in flight each
 
 template <typename T>
 __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
@@ -59,7 +60,7 @@ __device__ __forceinline__ int owner_of(const ChunkParams& p, int t, int u, unsi
 }
 
 template <typename T, int LPR>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams a) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams a) {
     const ChunkParams& p = a.c;
     const int lane = threadIdx.x & 31, u = lane % LPR;
     const int gshift = lane - u;
@@ -197,9 +198,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 template <typename T, int LPR>
 cudaError_t launch_append_t(AppendParams a, cudaStream_t stream) {
     const int rows = a.c.H + 2 * a.c.Hkv;
-    // one row a group while that does not yet fill the SMs four times over; then as
-    // many rows of a token per group as still do (at least four groups a token)
-    const int64_t full = (int64_t)device_sm_count() * 2048 * 4 / LPR;
+    // one row a group while that does not yet fill the SMs; then as many rows of a
+    // token per group as still do (at least four groups a token).  Measured at
+    // 16384 tokens of 32 + 2 x 4 heads of 128: 8 rows 70 us, 4 rows 81 us (the
+    // lookups of a token are repeated more often); 64 tokens: 1 row 4.1 us.
+    const int64_t full = (int64_t)device_sm_count() * 2048 / LPR;
     int gpt = rows;
     while (gpt > 4 && (int64_t)a.c.T * (gpt / 2) >= full) gpt = (gpt + 1) / 2;
     a.groups_per_token = gpt;
