@@ -121,6 +121,125 @@ __device__ __forceinline__ ChunkPos next_item(const ChunkParams& p, const ChunkP
     return y;
 }
 
+constexpr int kItemCost = 2;  // fixed part of an item's work, in tiles
+constexpr int kMinPart = 4;   // a cut leaves at least this many tiles on both sides
+
+// The work of one KV head of a (request, rank), by blocks of new tokens.
+struct HeadWork {
+    int nq;       // blocks
+    int last;     // tiles of the last one
+    int q0;       // blocks that see nothing because the request has more new tokens than tokens
+    int64_t a, b, m;
+};
+__device__ inline HeadWork head_work(const ChunkParams& p, int pair, int tpi, int tt) {
+    HeadWork w;
+    const int r = pair % p.N;
+    const Request q = load_request(p, pair / p.N);
+    w.nq = (q.n + tpi - 1) / tpi;
+    w.last = (rank_share(q.L, r, p.N) + tt - 1) / tt;  // its last row is the request's last token
+    w.q0 = 0;
+    w.m = (int64_t)p.N * tt;
+    if (p.causal) {
+        // block qt's last row has x = L - n + (qt + 1) tpi tokens before or at it: rank_share(x) =
+        // floor((x + N - 1 - r) / N), tiles = floor((x + m - 1 - r) / m), 0 below zero
+        w.a = tpi;
+        w.b = (int64_t)q.L - q.n + tpi + w.m - 1 - r;
+        if (w.b < 0) {
+            w.q0 = (int)((-w.b + tpi - 1) / tpi);
+            w.b += (int64_t)w.q0 * tpi;
+        }
+    } else {
+        w.a = 0;
+        w.b = w.last * w.m;
+    }
+    return w;
+}
+// Work of the blocks before q.
+__device__ inline int64_t work_before(const HeadWork& w, int q) {
+    const int k = min(q, w.nq - 1) - w.q0;
+    int64_t c = (int64_t)q * kItemCost;
+    if (k > 0) c += floor_sum(k, w.m, w.a, w.b);
+    if (q >= w.nq && w.nq > 0) c += w.last;
+    return c;
+}
+
+// The start of range c of `ctas`.  upto[t] is the work up to and with the pairs of
+// slot t (`per` (request, rank) pairs each, `slots` slots).  One thread.
+__device__ __forceinline__ ChunkPos range_start(const ChunkParams& p, int tpi, int tt, int ctas, int c,
+                                                const int64_t* upto, int slots, int64_t per) {
+    ChunkPos x = {p.B, 0, 0, 0};
+    const int64_t total = upto[slots - 1];
+    const int64_t at = (int64_t)((double)total * c / ctas);  // exact below 2^53 / ctas, monotone above
+    if (c >= ctas || at >= total) return x;
+    int lo = 0, hi = slots - 1;  // the first slot whose pairs pass `at`
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (upto[mid] > at) hi = mid;
+        else lo = mid + 1;
+    }
+    int64_t rem = at - (lo ? upto[lo - 1] : 0);
+    int64_t pair = lo * per;
+    HeadWork w = head_work(p, (int)pair, tpi, tt);
+    int64_t head = work_before(w, w.nq);
+    while (rem >= head * p.Hkv) {  // `at` lies in one of this slot's pairs
+        rem -= head * p.Hkv;
+        w = head_work(p, (int)++pair, tpi, tt);
+        head = work_before(w, w.nq);
+    }
+    const int b = (int)(pair / p.N), r = (int)(pair - (int64_t)b * p.N);
+    const int hkv = (int)(rem / head);
+    rem -= hkv * head;
+    int q0 = 0, q1 = w.nq - 1;  // the last block whose work starts at or before rem
+    while (q0 < q1) {
+        const int mid = (q0 + q1 + 1) >> 1;
+        if (work_before(w, mid) <= rem) q0 = mid;
+        else q1 = mid - 1;
+    }
+    const int64_t begin = work_before(w, q0);
+    const int n = (int)(work_before(w, q0 + 1) - begin) - kItemCost, off = (int)(rem - begin);
+    x = {b, r * p.Hkv + hkv, q0, max(off - kItemCost, 0)};
+    // a cut near an end of its item, or into a short one, moves to the nearer end
+    if (2 * off < n + kItemCost) {
+        if (x.tile < kMinPart || n < 2 * kMinPart) x.tile = 0;
+    } else if (n - x.tile < kMinPart || n < 2 * kMinPart) {
+        x = next_item(p, x, tpi);
+    }
+    return x;
+}
+
+// Every CTA finds its own range: range[0] and range[1], with the starts of all
+// ranges left in pos for the merge.  `scratch` holds THREADS + 32 numbers.  All
+// threads of the CTA; ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ void find_range(const ChunkParams& p, int tpi, int tt, ChunkPos* pos, int64_t* scratch,
+                                           ChunkPos* range) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t npairs = (int64_t)p.B * p.N;
+    const int64_t per = (npairs + THREADS - 1) / THREADS;
+    int64_t sum = 0;
+    for (int64_t i = tid * per; i < min((tid + 1) * per, npairs); ++i) {
+        const HeadWork w = head_work(p, (int)i, tpi, tt);
+        sum += work_before(w, w.nq) * p.Hkv;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 31) scratch[THREADS + warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += scratch[THREADS + w];
+    scratch[tid] = sum;
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+        const int c = (int)blockIdx.x + warp;
+        const ChunkPos x = range_start(p, tpi, tt, (int)gridDim.x, c, scratch, THREADS, per);
+        range[warp] = x;
+        if (warp == 0 || c == (int)gridDim.x) pos[c] = x;
+    }
+    __syncthreads();
+}
+
 // A CTA's part of an item.
 struct ChunkSeg {
     int b, r, hkv;
@@ -159,11 +278,10 @@ struct ChunkPartials {
 };
 size_t chunk_partials_bytes(int ctas, int rows, int D);
 ChunkPartials chunk_partials_in(unsigned char* ws, int ctas, int rows, int D);
-// Fills pos; joins the cut items (rows of an item: tpi tokens x gq heads, at most `rows`).
-cudaError_t launch_chunk_plan(const ChunkParams& p, const ChunkPartials& ws, int tpi, int tt, int ctas,
-                              cudaStream_t stream);
-cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
-                               cudaStream_t stream);
+// Joins the cut items (rows of an item: tpi tokens x gq heads, at most `rows`); nothing
+// to do, and no launch, when no item is long enough to be cut.
+cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int tt, int rows, int ctas,
+                               int dtype, cudaStream_t stream);
 
 // Adds what the tokens set in `mask` (local tokens tile0 + bit, tokens whose V row
 // holds NaN or infinities and was zeroed for the product) give to a row that

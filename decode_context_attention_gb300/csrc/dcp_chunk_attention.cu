@@ -41,8 +41,10 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
     unsigned char* vs = ks + kTile * P;
     __shared__ unsigned poison[4][2];  // tokens of the item's masked tiles whose V row is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    ChunkPos x = ws.pos[blockIdx.x];
-    const ChunkPos end = ws.pos[blockIdx.x + 1];
+    __shared__ ChunkPos range[2];
+    find_range<kThreadsMma>(p, tpi, kTile, ws.pos, reinterpret_cast<int64_t*>(smem), range);
+    ChunkPos x = range[0];
+    const ChunkPos end = range[1];
     const ChunkPos first = x;
     const float qscale = p.sm_scale * kLog2e;
 
@@ -250,15 +252,13 @@ template <typename T, int D>
 cudaError_t launch_mma(const ChunkParams& p, int dtype, cudaStream_t stream) {
     const int ctas = mma_ctas(D), tpi = kRows / p.gq;
     const ChunkPartials ws = chunk_partials_in(p.ws, ctas, kRows, D);
-    cudaError_t e = launch_chunk_plan(p, ws, tpi, kTile, ctas, stream);
-    if (e != cudaSuccess) return e;
     constexpr int smem = MmaShape<D>::kSmem;
-    e = cudaFuncSetAttribute(chunk_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     chunk_attention_kernel<T, D><<<ctas, kThreadsMma, smem, stream>>>(p, ws, tpi);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge(p, ws, tpi, kRows, ctas, dtype, stream);
+    return launch_chunk_merge(p, ws, tpi, kTile, kRows, ctas, dtype, stream);
 }
 
 template <typename T>

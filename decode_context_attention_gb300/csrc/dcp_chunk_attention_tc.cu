@@ -81,6 +81,7 @@ struct TcBars {
     int issued;               // ring positions whose loads are under way
     unsigned poison[kPoison][16];  // 4 masked tiles of 128 tokens
     float xm[kM], xl[kM];
+    alignas(16) ChunkPos range[2];
 };
 static_assert(sizeof(TcBars) <= kMisc, "misc region too small");
 
@@ -98,12 +99,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// A volatile read: the compiler keeps no copy of it.
+// A volatile read from shared memory: the compiler keeps no copy of it.
 __device__ __forceinline__ ChunkPos load_pos(const ChunkPos* at) {
     ChunkPos x;
-    asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(x.b), "=r"(x.rh), "=r"(x.qt), "=r"(x.tile)
-                 : "l"(at));
+                 : "r"(smem_u32(at)));
     return x;
 }
 // P of the 32 scores v[OFF ..], 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
@@ -137,6 +138,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int tj = tpi / 2;        // new tokens of a row block
     const int rblk = tj * p.gq;    // its rows (at most 128)
 
+    // the Q blocks are not in use yet
+    find_range<kThreadsTc>(p, tpi, kTT, ws.pos, reinterpret_cast<int64_t*>(smem), bar->range);
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&bar->full[s], 1);
@@ -166,6 +169,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tma_prefetch_map(&kmap);
         tma_prefetch_map(&vmap);
     }
+    fence_proxy_async_smem();  // the range's scratch is overwritten by copies
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     volatile int* abort = &bar->abort;
     int* status = &g_chunk_status;
     // the range, read again at every item rather than held in registers
-    const ChunkPos* range = ws.pos + blockIdx.x;
+    const ChunkPos* range = bar->range;
     ChunkPos x = load_pos(range);
     auto more = [&]() {
         const ChunkPos end = load_pos(range + 1);
@@ -434,6 +438,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int u = warp >> 2;             // stage
         const int m = tid & 127;             // row of the stage
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int mtok = m / p.gq, hh = m - mtok * p.gq;  // new token of the row block, head of the group
         const uint32_t tS = tmem + kM * u + lanes, tO = tmem + kColO + D * u + lanes;
         const float qscale = p.sm_scale * kLog2e;
         int sn = 0, vn = 0, xn = 0, seg = 0;  // phases of s_full and pv_done, exchanges, parts
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 tile0 = g.t0 + (pair ? 0 : u);
                 const int row = (pair ? u * rblk : 0) + m;
                 const bool valid = m < rblk && row < g.nrows;
-                lim = valid ? visible(p, g.q, g.j0 + row / p.gq, g.r) : 0;
+                lim = valid ? visible(p, g.q, g.j0 + (pair ? u * tj : 0) + mtok, g.r) : 0;
                 lim0 = g.lim0;
                 live = __any_sync(kAllLanes, valid);
             }
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const ChunkSeg g = this_seg();
             const int row = (pair ? u * rblk : 0) + m;  // row of the item
             const bool valid = m < rblk && row < g.nrows;
-            const int tok = row / p.gq, hh = row - tok * p.gq;
+            const int tok = (pair ? u * tj : 0) + mtok;
             // l is 0 only where the row sees nothing (a visible row's largest term is at least 2^-8); NaN stays NaN
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : mref + log2f(l);
@@ -684,17 +689,15 @@ template <typename T, int D>
 cudaError_t launch_tc(const ChunkParams& p, const CUtensorMap (&maps)[3], int dtype, cudaStream_t stream) {
     const int ctas = device_sm_count(), tpi = 2 * (kM / p.gq);
     const ChunkPartials ws = chunk_partials_in(p.ws, ctas, 2 * kM, D);
-    cudaError_t e = launch_chunk_plan(p, ws, tpi, kTT, ctas, stream);
-    if (e != cudaSuccess) return e;
     const void* k = (const void*)chunk_attention_tc_kernel<T, D>;
     // the shared-memory opt-in is a per-device function attribute
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
     if (e != cudaSuccess) return e;
     chunk_attention_tc_kernel<T, D>
         <<<ctas, kThreadsTc, TcShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, ws, tpi);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge(p, ws, tpi, 2 * kM, ctas, dtype, stream);
+    return launch_chunk_merge(p, ws, tpi, kTT, 2 * kM, ctas, dtype, stream);
 }
 
 }  // namespace

@@ -14,7 +14,7 @@
 // chunk's queries are read from L2, 32 KB per 2 x 128 x 128 x D products.
 // The items, cut evenly by their number of query tiles, go to one persistent CTA
 // per SM; every CTA finds its range itself from the lengths (sums of floors, as
-// in the plan of the chunk attention).
+// in the chunk attention).
 // Warps 0-15: the sums, four warps for each of the block's two tiles and of the
 // two score buffers (query tiles alternate; at the end of an item one of the two
 // adds its sum to what the other has written): with eight warps the waits of a
