@@ -397,26 +397,30 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                                     mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort));
                     if (!ok) break;
                     uint8_t* tile = ring + s * kTileBytes;
-                    const int live = g.lim_last - t * kTT;  // rows from here on are no one's
-                    for (int row = max(live, 0); row < kTT; ++row) {
-                        if (lane < 8 * NCH)
-                            *reinterpret_cast<uint4*>(tile + (lane >> 3) * kChunkB + row * 128 + (lane & 7) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                    // 16 bytes a lane, 4 rows of 128 bytes a step
+                    const int live = min(max(g.lim_last - t * kTT, 0), kTT);  // rows from here on are no one's
+                    uint8_t* mine = tile + (lane >> 3) * 128 + (lane & 7) * 16;
+                    for (int r4 = live & ~3; r4 < kTT; r4 += 4) {
+                        if (r4 + (lane >> 3) < live) continue;
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            *reinterpret_cast<uint4*>(mine + c * kChunkB + r4 * 128) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     if (g.lim0 < g.lim_last) {  // rows of the item differ in what they see
-                        // 16 bytes a lane, 4 rows of 128 bytes a step
-                        const int rows = min(live, kTT);
-                        for (int r4 = 0; r4 < rows; r4 += 4) {
-                            const int row = r4 + (lane >> 3);
+                        for (int r4 = 0; r4 < live; r4 += 16) {
+                            uint4 v[4 * NCH];
 #pragma unroll
-                            for (int c = 0; c < NCH; ++c) {
-                                uint4* at = reinterpret_cast<uint4*>(tile + c * kChunkB + row * 128 + (lane & 7) * 16);
-                                uint4 v = *at;
-                                if (row < rows && (pair_nonfinite<T>(v.x) || pair_nonfinite<T>(v.y) ||
-                                                   pair_nonfinite<T>(v.z) || pair_nonfinite<T>(v.w))) {
-                                    v = make_uint4(pair_finite<T>(v.x), pair_finite<T>(v.y), pair_finite<T>(v.z),
-                                                   pair_finite<T>(v.w));
-                                    *at = v;
+                            for (int e = 0; e < 4 * NCH; ++e)
+                                v[e] = *reinterpret_cast<const uint4*>(mine + (e >> 2) * kChunkB +
+                                                                       min(r4 + 4 * (e & 3), kTT - 4) * 128);
+#pragma unroll
+                            for (int e = 0; e < 4 * NCH; ++e) {
+                                const int row = r4 + 4 * (e & 3) + (lane >> 3);
+                                if (row < live && (pair_nonfinite<T>(v[e].x) || pair_nonfinite<T>(v[e].y) ||
+                                                   pair_nonfinite<T>(v[e].z) || pair_nonfinite<T>(v[e].w))) {
+                                    *reinterpret_cast<uint4*>(mine + (e >> 2) * kChunkB + (row & ~3) * 128) =
+                                        make_uint4(pair_finite<T>(v[e].x), pair_finite<T>(v[e].y),
+                                                   pair_finite<T>(v[e].z), pair_finite<T>(v[e].w));
                                     atomicOr(&poison[4 * (t - m0) + (row >> 5)], 1u << (row & 31));
                                 }
                             }
