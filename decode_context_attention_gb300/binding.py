@@ -57,6 +57,8 @@ _lib = None
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the library (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -457,78 +459,135 @@ class _PreparedOn(_Prepared):
     """A prepared call whose tensors live on a given device: the call runs with
     that device current, whichever one is current where it is made."""
 
-    def __init__(self, fn_name: str, device, args: tuple, keep: tuple):
-        super().__init__(fn_name, args, keep)
+    def __init__(self, fn, name: str, device, args: tuple, keep: tuple):
+        self._fn, self._name, self._args, self._keep = fn, name, args, keep
         self._device = device.index if device.type == "cuda" else None
 
     def __call__(self) -> None:
         if self._device is None or self._device == torch.cuda.current_device():
-            super().__call__()
+            st = self._fn(*self._args)
         else:
             with torch.cuda.device(self._device):
-                super().__call__()
+                st = self._fn(*self._args)
+        if st != DCP_OK:
+            check(st, self._name)
+
+
+def _run_on(device, fn, name: str, args: tuple) -> None:
+    """One call with `device` current."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != DCP_OK:
+        check(st, name)
 
 
 def _chunk_device(q: torch.Tensor, *ts) -> torch.device:
     """The device of the operands: `q`'s, which the other CUDA tensors share."""
-    _need_cuda(q, *ts)
     d = q.device
     for t in ts:
-        if t is not None and t.device != d and t.is_cuda and q.is_cuda:
-            raise ValueError(f"operands on {d} and {t.device}")
+        if t is not None and t.device != d:
+            _need_cuda(t)
+            if t.is_cuda and q.is_cuda:
+                raise ValueError(f"operands on {d} and {t.device}")
+    if not q.is_cuda:
+        _need_cuda(q, *ts)
     return d
+
+
+# the raw handle of the current stream without building a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_on(device, stream) -> int:
     if stream is None:
+        if _raw_stream is not None and device.type == "cuda":
+            return _raw_stream(device.index)
         return torch.cuda.current_stream(device if device.type == "cuda" else None).cuda_stream
     return _stream_handle(stream)
 
 
-def _int32(**ts) -> None:
-    for name, t in ts.items():
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != 1:
-            raise ValueError(f"{name} must be a contiguous 1-dim int32 tensor")
+def _int32(name: str, t: torch.Tensor, n: int) -> int:
+    if t.dtype != torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+def _same_dtype(t: torch.Tensor, *ts) -> int:
+    d = t.dtype
+    for x in ts:
+        if x is not None and x.dtype != d:
+            raise ValueError(f"payload tensors of types {d} and {x.dtype}")
+    return _dtype_code(t)
 
 
-def _same_dtype(*ts) -> int:
-    for t in ts:
-        if t is not None and t.dtype != ts[0].dtype:
-            raise ValueError(f"payload tensors of types {ts[0].dtype} and {t.dtype}")
-    return _dtype_code(ts[0])
-
-
-def _pool_args(pages: torch.Tensor, N: int, Hkv: int, D: int, like: torch.Tensor | None = None):
-    if pages.dim() != 5 or pages.shape[0] != N or pages.shape[3] != Hkv or pages.shape[4] != D or (
-            like is not None and pages.shape != like.shape):
-        raise ValueError(f"pages are [N, num_pages, page_size, Hkv, D], here {(N, '..', '..', Hkv, D)}; got "
-                         f"{tuple(pages.shape)}")
-    _inner_ok(pages)
+def _pool_args(pages: torch.Tensor, shape):
+    """Pointer and strides of a pool [N, num_pages, page_size, Hkv, D]."""
     s = pages.stride()
+    if pages.shape != shape or (shape[4] > 1 and s[4] != 1):
+        raise ValueError(f"pages are [N, num_pages, page_size, Hkv, D] = {tuple(shape)} with unit stride along D; got "
+                         f"{tuple(pages.shape)}, strides {s}")
     return (pages.data_ptr(), s[0], s[1], s[2], s[3])
 
 
 def _table_args(table: torch.Tensor, N: int, B: int, name: str = "block_table"):
-    if table.dtype != torch.int32 or table.dim() != 3 or table.shape[0] != N or table.shape[1] != B or (
-            table.shape[2] > 1 and table.stride(2) != 1):
+    n, b, m = table.shape
+    s = table.stride()
+    if table.dtype != torch.int32 or n != N or b != B or (m > 1 and s[2] != 1):
         raise ValueError(f"{name} is int32 [N, B, max_pages] = [{N}, {B}, ..] with unit stride along the pages")
-    return (table.data_ptr(), table.stride(0), table.stride(1), table.shape[2])
+    return (table.data_ptr(), s[0], s[1], m)
 
 
-def _rows_args(t: torch.Tensor, shape: tuple, name: str, inner: bool = True):
-    """Pointer and the strides of a tensor's leading dimensions."""
-    _shape(t, shape, name)
+def _rows_args(t: torch.Tensor, shape: tuple, name: str):
+    """Pointer of a tensor of head rows and the strides of all but its last dimension."""
     s = t.stride()
-    if inner:
-        if shape[-1] > 1 and s[-1] != 1:
-            raise ValueError("the innermost (D) dimension must have stride 1")
-        s = s[:-1]
-    return (t.data_ptr(), *s)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if shape[-1] > 1 and s[-1] != 1:
+        raise ValueError(f"{name}: the innermost dimension must have stride 1")
+    return (t.data_ptr(), *s[:-1])
+
+
+def _word_args(t: torch.Tensor, shape: tuple, name: str):
+    """Pointer and strides of an fp32 tensor of single words."""
+    if t.dtype != torch.float32 or t.shape != shape:
+        raise ValueError(f"{name}: expected fp32 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return (t.data_ptr(), *t.stride())
+
+
+def _append_args(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table, query_start,
+                 seq_lens, max_seq_len, q_out, interleaved, stream):
+    dev = _chunk_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
+                        seq_lens, q_out)
+    T, H, D = q.shape
+    pool = k_pages.shape
+    N, num_pages, page_size, Hkv, _ = pool
+    B = seq_lens.shape[0]
+    code = _same_dtype(q, k, v, q_weight, k_weight, k_pages, v_pages, q_out)
+    rows, kv = (T, H, D), (T, Hkv, D)
+    if pool[4] != D:
+        raise ValueError(f"pages of head dimension {pool[4]}, heads of {D}")
+    qw = kw = cs = ps = None
+    rot = npos = 0
+    if q_weight is not None:
+        qw = _rows_args(q_weight, (D,), "q_weight")[0]
+    if k_weight is not None:
+        kw = _rows_args(k_weight, (D,), "k_weight")[0]
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("cos_sin and positions are given together")
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin is a contiguous fp32 [num_positions, rot_dim] tensor")
+        npos, rot = cos_sin.shape
+        cs = cos_sin.data_ptr()
+        ps = _int32("positions", positions, T)
+    return dev, (code, N, B, T, H, Hkv, D, *_rows_args(q, rows, "q"), *_rows_args(k, kv, "k"),
+                 *_rows_args(v, kv, "v"), qw, kw, float(eps), cs, npos, rot, 1 if interleaved else 0, ps,
+                 *_rows_args(q_out, rows, "q_out"), *_pool_args(k_pages, pool), *_pool_args(v_pages, pool), num_pages,
+                 page_size, *_table_args(block_table, N, B), _int32("query_start", query_start, B + 1),
+                 _int32("seq_lens", seq_lens, B), int(max_seq_len), _stream_on(dev, stream))
 
 
 def prepare_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
@@ -545,48 +604,23 @@ def prepare_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     or both None; k_pages, v_pages [N,num_pages,page_size,Hkv,D]; block_table
     [N,B,max_pages] int32; query_start [B+1], seq_lens [B] int32 (lengths with
     the new tokens)."""
-    dev = _chunk_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
-                        seq_lens, q_out)
-    T, H, D = q.shape
-    Hkv, N, B = k.shape[1], k_pages.shape[0], seq_lens.shape[0]
-    code = _same_dtype(q, k, v, q_weight, k_weight, k_pages, v_pages, q_out)
-    _int32(query_start=query_start, seq_lens=seq_lens)
-    _shape(query_start, (B + 1,), "query_start")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _shape(w, (D,), name)
-            _inner_ok(w)
-    rot = npos = 0
-    if (cos_sin is None) != (positions is None):
-        raise ValueError("cos_sin and positions are given together")
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin is a contiguous fp32 [num_positions, rot_dim] tensor")
-        npos, rot = cos_sin.shape
-        _int32(positions=positions)
-        _shape(positions, (T,), "positions")
-    args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_rows_args(k, (T, Hkv, D), "k"),
-            *_rows_args(v, (T, Hkv, D), "v"),
-            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            float(eps), None if cos_sin is None else cos_sin.data_ptr(), npos, rot, 1 if interleaved else 0,
-            None if positions is None else positions.data_ptr(), *_rows_args(q_out, (T, H, D), "q_out"),
-            *_pool_args(k_pages, N, Hkv, D), *_pool_args(v_pages, N, Hkv, D, k_pages), k_pages.shape[1],
-            k_pages.shape[2], *_table_args(block_table, N, B), query_start.data_ptr(), seq_lens.data_ptr(),
-            int(max_seq_len), _stream_on(dev, stream))
-    return _PreparedOn("dcp_qk_norm_rope_append", dev, args,
+    dev, args = _append_args(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table,
+                             query_start, seq_lens, max_seq_len, q_out, interleaved, stream)
+    return _PreparedOn(load().dcp_qk_norm_rope_append, "dcp_qk_norm_rope_append", dev, args,
                        (q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
                         seq_lens, q_out))
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table,
                         query_start, seq_lens, max_seq_len, q_out, interleaved=False, stream=None) -> None:
-    prepare_qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table,
-                                query_start, seq_lens, max_seq_len, q_out, interleaved, stream)()
+    dev, args = _append_args(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table,
+                             query_start, seq_lens, max_seq_len, q_out, interleaved, stream)
+    _run_on(dev, load().dcp_qk_norm_rope_append, "dcp_qk_norm_rope_append", args)
 
 
 def extend_workspace_bytes(N: int, B: int, T: int, H: int, Hkv: int, D: int, max_seq_len: int) -> int:
     """Bytes of workspace extend_attention_paged needs on the current device."""
-    return dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, max_seq_len)
+    return dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, int(max_seq_len))
 
 
 def _scratch(nbytes: int, device, stream):
@@ -603,6 +637,34 @@ def _scratch(nbytes: int, device, stream):
     return ws
 
 
+def _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse, sm_scale, base, causal,
+                 workspace, stream):
+    dev = _chunk_device(q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace)
+    T, H, D = q.shape
+    pool = k_pages.shape
+    N, num_pages, page_size, Hkv, _ = pool
+    B = seq_lens.shape[0]
+    if pool[4] != D:
+        raise ValueError(f"pages of head dimension {pool[4]}, heads of {D}")
+    code = _same_dtype(q, k_pages, v_pages, o)
+    args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, pool),
+            *_pool_args(v_pages, pool), num_pages, page_size, *_table_args(block_table, N, B),
+            _int32("query_start", query_start, B + 1), _int32("seq_lens", seq_lens, B), int(max_seq_len), float(sm_scale),
+            1 if causal else 0, *_rows_args(o, (N, T, H, D), "o"), *_word_args(lse, (N, T, H), "lse"),
+            _base_code(base))
+    if workspace is None:
+        on = dev if dev.type == "cuda" else torch.device("cuda", torch.cuda.current_device())
+        size = load().dcp_extend_attention_workspace_size
+        if on.index == torch.cuda.current_device():
+            nbytes = size(N, B, T, H, Hkv, D, int(max_seq_len))
+        else:
+            with torch.cuda.device(on):
+                nbytes = size(N, B, T, H, Hkv, D, int(max_seq_len))
+        workspace = _scratch(nbytes, on, stream)
+    return dev, workspace, (*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            _stream_on(dev, stream))
+
+
 def prepare_extend_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                                    block_table: torch.Tensor, query_start: torch.Tensor, seq_lens: torch.Tensor,
                                    max_seq_len: int, o: torch.Tensor, lse: torch.Tensor, sm_scale: float,
@@ -614,36 +676,35 @@ def prepare_extend_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pag
     [N,B,max_pages] int32; query_start [B+1], seq_lens [B] int32; o [N,T,H,D],
     lse [N,T,H] fp32: the partials that lse_combine merges.  `workspace` (uint8,
     device, extend_workspace_bytes() long) is allocated here when not given."""
-    dev = _chunk_device(q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace)
-    T, H, D = q.shape
-    N, B, Hkv = k_pages.shape[0], seq_lens.shape[0], k_pages.shape[3]
-    code = _same_dtype(q, k_pages, v_pages, o)
-    _int32(query_start=query_start, seq_lens=seq_lens)
-    _shape(query_start, (B + 1,), "query_start")
-    if lse.dtype != torch.float32:
-        raise ValueError("LSE tensors are fp32")
-    rows = (*_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, N, Hkv, D),
-            *_pool_args(v_pages, N, Hkv, D, k_pages), k_pages.shape[1], k_pages.shape[2],
-            *_table_args(block_table, N, B), query_start.data_ptr(), seq_lens.data_ptr(), int(max_seq_len),
-            float(sm_scale), 1 if causal else 0, *_rows_args(o, (N, T, H, D), "o"),
-            *_rows_args(lse, (N, T, H), "lse", inner=False), _base_code(base))
-    if workspace is None:
-        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                nbytes = extend_workspace_bytes(N, B, T, H, Hkv, D, int(max_seq_len))
-        else:
-            nbytes = extend_workspace_bytes(N, B, T, H, Hkv, D, int(max_seq_len))
-        workspace = _scratch(nbytes, dev if dev.type == "cuda" else torch.device("cuda"), stream)
-    args = (code, N, B, T, H, Hkv, D, *rows, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream_on(dev, stream))
-    return _PreparedOn("dcp_extend_attention_paged", dev, args,
+    dev, workspace, args = _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse,
+                                        sm_scale, base, causal, workspace, stream)
+    return _PreparedOn(load().dcp_extend_attention_paged, "dcp_extend_attention_paged", dev, args,
                        (q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace))
 
 
 def extend_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse, sm_scale,
                            base="e", causal=True, workspace=None, stream=None) -> None:
-    prepare_extend_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse,
-                                   sm_scale, base, causal, workspace, stream)()
+    dev, _, args = _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse,
+                                sm_scale, base, causal, workspace, stream)
+    _run_on(dev, load().dcp_extend_attention_paged, "dcp_extend_attention_paged", args)
+
+
+def _weights_args(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale, base, stream):
+    dev = _chunk_device(q, k_pages, block_table, query_start, seq_lens, lse, acc)
+    T, H, D = q.shape
+    pool = k_pages.shape
+    N, num_pages, page_size, Hkv, _ = pool
+    B = seq_lens.shape[0]
+    if pool[4] != D:
+        raise ValueError(f"pages of head dimension {pool[4]}, heads of {D}")
+    code = _same_dtype(q, k_pages)
+    cap = acc.shape[-1]
+    if cap * N < max_seq_len or acc.dtype != torch.float32:
+        raise ValueError("acc is fp32 [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
+    return dev, (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, pool), num_pages,
+                 page_size, *_table_args(block_table, N, B), _int32("query_start", query_start, B + 1),
+                 _int32("seq_lens", seq_lens, B), int(max_seq_len), float(sm_scale), *_word_args(lse, (T, H), "lse"),
+                 _base_code(base), *_rows_args(acc, (N, B, Hkv, cap), "acc"), _stream_on(dev, stream))
 
 
 def prepare_attention_weights_paged(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor,
@@ -655,28 +716,38 @@ def prepare_attention_weights_paged(q: torch.Tensor, k_pages: torch.Tensor, bloc
     q [T,H,D]; k_pages [N,num_pages,page_size,Hkv,D]; lse [T,H] fp32, the MERGED
     log-sum-exp (lse_combine's out_lse); acc [N,B,Hkv,cap] fp32, cap >=
     ceil(max_seq_len / N), updated in place (new tokens' entries start from 0)."""
-    dev = _chunk_device(q, k_pages, block_table, query_start, seq_lens, lse, acc)
-    T, H, D = q.shape
-    N, B, Hkv = k_pages.shape[0], seq_lens.shape[0], k_pages.shape[3]
-    code = _same_dtype(q, k_pages)
-    _int32(query_start=query_start, seq_lens=seq_lens)
-    _shape(query_start, (B + 1,), "query_start")
-    if lse.dtype != torch.float32 or acc.dtype != torch.float32:
-        raise ValueError("LSE and weight tensors are fp32")
-    if acc.dim() != 4 or acc.shape[3] * N < int(max_seq_len):
-        raise ValueError("acc is [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
-    args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, N, Hkv, D),
-            k_pages.shape[1], k_pages.shape[2], *_table_args(block_table, N, B), query_start.data_ptr(),
-            seq_lens.data_ptr(), int(max_seq_len), float(sm_scale), *_rows_args(lse, (T, H), "lse", inner=False),
-            _base_code(base), *_rows_args(acc, (N, B, Hkv, acc.shape[3]), "acc"), _stream_on(dev, stream))
-    return _PreparedOn("dcp_attention_weights_paged", dev, args,
+    dev, args = _weights_args(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale, base,
+                              stream)
+    return _PreparedOn(load().dcp_attention_weights_paged, "dcp_attention_weights_paged", dev, args,
                        (q, k_pages, block_table, query_start, seq_lens, lse, acc))
 
 
 def attention_weights_paged(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale,
                             base="e", stream=None) -> None:
-    prepare_attention_weights_paged(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale,
-                                    base, stream)()
+    dev, args = _weights_args(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale, base,
+                              stream)
+    _run_on(dev, load().dcp_attention_weights_paged, "dcp_attention_weights_paged", args)
+
+
+def _evict_args(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent, dst_table,
+                kept, acc_out, stream):
+    dev = _chunk_device(k_pages, v_pages, block_table, seq_lens, acc, keep_lens, dst_table, kept, acc_out)
+    pool = k_pages.shape
+    N, num_pages, page_size, Hkv, D = pool
+    B = seq_lens.shape[0]
+    code = _same_dtype(k_pages, v_pages)
+    cap, kcap = acc.shape[-1], kept.shape[-1]
+    if acc.dtype != torch.float32 or acc_out.dtype != torch.float32 or kept.dtype != torch.int32:
+        raise ValueError("acc and acc_out are fp32, kept is int32")
+    if cap * N < max_seq_len:
+        raise ValueError("acc is [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
+    if kcap * N < min(max_keep, max_seq_len):
+        raise ValueError("kept and acc_out are [N, B, Hkv, kcap] with kcap >= ceil(max_keep / N)")
+    return dev, (code, N, B, Hkv, D, *_pool_args(k_pages, pool), *_pool_args(v_pages, pool), num_pages, page_size,
+                 *_table_args(block_table, N, B), _int32("seq_lens", seq_lens, B), int(max_seq_len),
+                 *_rows_args(acc, (N, B, Hkv, cap), "acc"), _int32("keep_lens", keep_lens, B), int(max_keep), int(recent),
+                 *_table_args(dst_table, N, B, "dst_table"), *_rows_args(kept, (N, B, Hkv, kcap), "kept"),
+                 *_rows_args(acc_out, (N, B, Hkv, kcap), "acc_out"), _stream_on(dev, stream))
 
 
 def prepare_cache_evict_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
@@ -690,32 +761,17 @@ def prepare_cache_evict_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, bloc
     leave the request alone), at most max_keep; dst_table [N,B,pages] int32;
     kept int32 and acc_out fp32 [N,B,Hkv,kcap], kcap >= ceil(max_keep / N): the
     kept tokens' old local indices and their weights."""
-    dev = _chunk_device(k_pages, v_pages, block_table, seq_lens, acc, keep_lens, dst_table, kept, acc_out)
-    N, _, _, Hkv, D = k_pages.shape
-    B = seq_lens.shape[0]
-    code = _same_dtype(k_pages, v_pages)
-    _int32(seq_lens=seq_lens, keep_lens=keep_lens)
-    _shape(keep_lens, (B,), "keep_lens")
-    if acc.dtype != torch.float32 or acc_out.dtype != torch.float32 or kept.dtype != torch.int32:
-        raise ValueError("acc and acc_out are fp32, kept is int32")
-    if acc.dim() != 4 or acc.shape[3] * N < int(max_seq_len):
-        raise ValueError("acc is [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
-    if kept.dim() != 4 or kept.shape[3] * N < min(int(max_keep), int(max_seq_len)):
-        raise ValueError("kept and acc_out are [N, B, Hkv, kcap] with kcap >= ceil(max_keep / N)")
-    args = (code, N, B, Hkv, D, *_pool_args(k_pages, N, Hkv, D), *_pool_args(v_pages, N, Hkv, D, k_pages),
-            k_pages.shape[1], k_pages.shape[2], *_table_args(block_table, N, B), seq_lens.data_ptr(),
-            int(max_seq_len), *_rows_args(acc, (N, B, Hkv, acc.shape[3]), "acc"), keep_lens.data_ptr(),
-            int(max_keep), int(recent), *_table_args(dst_table, N, B, "dst_table"),
-            *_rows_args(kept, (N, B, Hkv, kept.shape[3]), "kept"),
-            *_rows_args(acc_out, (N, B, Hkv, kept.shape[3]), "acc_out"), _stream_on(dev, stream))
-    return _PreparedOn("dcp_cache_evict_paged", dev, args,
+    dev, args = _evict_args(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
+                            dst_table, kept, acc_out, stream)
+    return _PreparedOn(load().dcp_cache_evict_paged, "dcp_cache_evict_paged", dev, args,
                        (k_pages, v_pages, block_table, seq_lens, acc, keep_lens, dst_table, kept, acc_out))
 
 
 def cache_evict_paged(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
                       dst_table, kept, acc_out, stream=None) -> None:
-    prepare_cache_evict_paged(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
-                              dst_table, kept, acc_out, stream)()
+    dev, args = _evict_args(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
+                            dst_table, kept, acc_out, stream)
+    _run_on(dev, load().dcp_cache_evict_paged, "dcp_cache_evict_paged", args)
 
 
 def device_status() -> int:
