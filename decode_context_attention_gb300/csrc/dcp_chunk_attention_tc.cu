@@ -57,6 +57,7 @@ constexpr float kFar = 65536.f;
 constexpr unsigned kAllLanes = 0xffffffffu;
 constexpr uint32_t kColO = 256;
 constexpr uint32_t kCols = 512;
+constexpr int kSegs = 3;
 constexpr int kPoison = 8;      // per-item records of tokens with non-finite values
 
 __device__ int g_chunk_status;  // first bounded wait that ran out (0 if none)
@@ -79,9 +80,11 @@ struct TcBars {
     uint32_t tmem_base;
     int abort;
     int issued;               // ring positions whose loads are under way
-    unsigned poison[kPoison][16];  // 4 masked tiles of 128 tokens
+    unsigned poison[kPoison][12];  // 3 masked tiles of 128 tokens
     float xm[kM], xl[kM];
     alignas(16) ChunkPos range[2];
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
+    alignas(16) int4 seg[kSegs][4];  // the CTA's parts, as warp 11 hands them out
 };
 static_assert(sizeof(TcBars) <= kMisc, "misc region too small");
 
@@ -100,12 +103,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // A volatile read from shared memory: the compiler keeps no copy of it.
-__device__ __forceinline__ ChunkPos load_pos(const ChunkPos* at) {
-    ChunkPos x;
+__device__ __forceinline__ int4 ld_shared4(const int4* at) {
+    int4 x;
     asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.b), "=r"(x.rh), "=r"(x.qt), "=r"(x.tile)
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                  : "r"(smem_u32(at)));
     return x;
+}
+__device__ __forceinline__ ChunkSeg read_seg(const int4* at) {
+    const int4 a = ld_shared4(at), b = ld_shared4(at + 1), c = ld_shared4(at + 2), d = ld_shared4(at + 3);
+    ChunkSeg s;
+    s.b = a.x; s.r = a.y; s.hkv = a.z; s.row0 = a.w;
+    s.nrows = b.x; s.j0 = b.y; s.t0 = b.z; s.t1 = b.w;
+    s.lim0 = c.x; s.lim_last = c.y; s.slot = c.z; s.q.n = c.w;
+    s.q.L = d.x; s.q.start = d.y;
+    return s;
 }
 // P of the 32 scores v[OFF ..], 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
 template <typename T, int OFF>
@@ -146,6 +158,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&bar->empty[s], 1);
             mbar_init(&bar->v_clean[s], 1);
         }
+        for (int s = 0; s < kSegs; ++s) {
+            mbar_init(&bar->seg_full[s], 1);
+            mbar_init(&bar->seg_empty[s], 11);  // warps 0 to 10
+        }
         for (int u = 0; u < 2; ++u) {
             mbar_init(&bar->q_full[u], 1);
             mbar_init(&bar->q_empty[u], 1);
@@ -176,30 +192,29 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
     int* status = &g_chunk_status;
-    // the range, read again at every item rather than held in registers
-    const ChunkPos* range = bar->range;
-    ChunkPos x = load_pos(range);
-    auto more = [&]() {
-        const ChunkPos end = load_pos(range + 1);
-        return x.b < p.B && !(same_item(x, end) && x.tile == end.tile);
+    // the k-th part of this CTA's range, from warp 11; false behind the last one
+    auto get_seg = [&](int k, ChunkSeg* g) -> bool {
+        if (!__all_sync(kAllLanes, mbar_wait(&bar->seg_full[k % kSegs], (k / kSegs) & 1, status, DCP_ERR_TIMEOUT, abort)))
+            return false;
+        *g = read_seg(bar->seg[k % kSegs]);
+        return g->b >= 0;
     };
-    auto advance = [&]() -> bool {  // false behind the last part
-        if (same_item(x, load_pos(range + 1))) return false;
-        x = next_item(p, x, tpi);
-        return true;
+    auto release_seg = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->seg_empty[k % kSegs]);
     };
-    auto this_seg = [&]() { return load_seg(p, x, load_pos(range), load_pos(range + 1), tpi, kTT); };
     bool issued_any = false;
 
     if (warp >= 8) {
-        regs_dec<88>();
+        regs_dec<56>();
         if (warp == 8) {
             // ------------------------------------------------------------ TMA
             const int pb = min(1 << p.page_shift, kTT);  // rows of a box: a page, or a tile of one
             int pos = 0, qn[2] = {0, 0};
-            bool ok = more() && !p.stall_loads;
-            while (ok) {
-                const ChunkSeg g = this_seg();
+            bool ok = !p.stall_loads;
+            ChunkSeg g;
+            for (int seg = 0; ok && get_seg(seg, &g); ++seg) {
+                release_seg(seg);
                 const int n = g.t1 - g.t0;
                 const bool pair = g.nrows > rblk;
                 auto load_q = [&](int u) -> bool {
@@ -260,8 +275,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (ok && i + 2 < n) ok = load_tile(i + 2, &kmap);
                     }
                 }
-                if (!ok || !advance()) break;
-                ok = more();
             }
             // copies still in flight (only after an abort) land before the CTA ends
             if (lane == 0) {
@@ -289,12 +302,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const uint32_t ra = qa + 2 * kTileBytes;
             int base = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
             unsigned cleaned = 0u;  // phase of v_clean by slot
-            bool ok = more();
-            while (ok) {
+            bool ok = true;
+            ChunkSeg g;
+            for (int seg = 0; ok && get_seg(seg, &g); ++seg) {
+                release_seg(seg);
                 int n, mtile;
                 bool pair;
                 {
-                    const ChunkSeg g = this_seg();
                     n = __shfl_sync(kAllLanes, g.t1 - g.t0, 0);
                     pair = __shfl_sync(kAllLanes, g.nrows > rblk ? 1 : 0, 0) != 0;
                     mtile = __shfl_sync(kAllLanes, g.lim0 / kTT - g.t0, 0);  // masked from here on, within the part
@@ -362,21 +376,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     }
                 }
                 base += 2 * n;
-                if (!ok || !advance()) break;
-                ok = more();
             }
             if (issued_any) mma_commit_warp(&bar->mma_done);
         } else if (warp == 10) {
             // -------------------------------------------- V of the masked tiles
-            int base = 0, seg = 0;
-            bool ok = more();
-            while (ok) {
-                const ChunkSeg g = this_seg();
+            int base = 0;
+            bool ok = true;
+            ChunkSeg g;
+            for (int seg = 0; ok && get_seg(seg, &g); ++seg) {
+                release_seg(seg);
                 const int n = g.t1 - g.t0;
                 const bool pair = g.nrows > rblk;
                 const int m0 = g.lim0 / kTT;
                 unsigned* poison = bar->poison[seg & (kPoison - 1)];
-                if (lane < 16) poison[lane] = 0u;
+                if (lane < 12) poison[lane] = 0u;
                 __syncwarp();
                 for (int t = max(m0, g.t0); ok && t < g.t1; ++t) {
                     const int i = t - g.t0;
@@ -431,30 +444,55 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (lane == 0) mbar_arrive(&bar->v_clean[s]);
                 }
                 base += 2 * n;
-                ++seg;
-                if (!ok || !advance()) break;
-                ok = more();
+            }
+        } else {
+            // ------------------------------------------------ the parts, ahead of everyone
+            ChunkPos x = bar->range[0];
+            const ChunkPos first = x, end = bar->range[1];
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const bool more = x.b < p.B && !(same_item(x, end) && x.tile == end.tile);
+                ChunkSeg g;
+                g.b = -1;
+                if (more) g = load_seg(p, x, first, end, tpi, kTT);
+                if (k >= kSegs)
+                    ok = __all_sync(kAllLanes, mbar_wait(&bar->seg_empty[k % kSegs], (k / kSegs - 1) & 1, status,
+                                                         DCP_ERR_TIMEOUT, abort));
+                if (!ok) break;
+                if (lane == 0) {
+                    int4* at = bar->seg[k % kSegs];
+                    at[0] = make_int4(g.b, g.r, g.hkv, g.row0);
+                    at[1] = make_int4(g.nrows, g.j0, g.t0, g.t1);
+                    at[2] = make_int4(g.lim0, g.lim_last, g.slot, g.q.n);
+                    at[3] = make_int4(g.q.L, g.q.start, 0, 0);
+                    mbar_arrive(&bar->seg_full[k % kSegs]);
+                }
+                __syncwarp();
+                if (!more) break;
+                if (same_item(x, end)) x = end;  // its first tiles were the last part
+                else x = next_item(p, x, tpi);
             }
         }
     } else {
         // ------------------------------------------------------------ softmax
-        regs_inc<208>();
+        regs_inc<224>();
         const int u = warp >> 2;             // stage
         const int m = tid & 127;             // row of the stage
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int mtok = m / p.gq, hh = m - mtok * p.gq;  // new token of the row block, head of the group
         const uint32_t tS = tmem + kM * u + lanes, tO = tmem + kColO + D * u + lanes;
         const float qscale = p.sm_scale * kLog2e;
-        int sn = 0, vn = 0, xn = 0, seg = 0;  // phases of s_full and pv_done, exchanges, parts
-        bool ok = more();
+        int sn = 0, vn = 0, xn = 0;  // phases of s_full and pv_done, exchanges
+        bool ok = true;
         auto wait = [&](uint64_t* b, int parity) -> bool {
             return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
         };
-        while (ok) {
+        for (int seg = 0; ok; ++seg) {
             int n, mine, step, tile0, lim, lim0;
             bool pair, live;
             {
-                const ChunkSeg g = this_seg();
+                ChunkSeg g;
+                if (!get_seg(seg, &g)) break;
                 n = g.t1 - g.t0;
                 pair = g.nrows > rblk;
                 mine = pair ? n : (n + 1 - u) / 2;  // tiles of this stage
@@ -574,8 +612,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             // the item again, for where its rows go: held through the tiles it would take
             // the registers of their scores
-            asm volatile("" : "+r"(x.b), "+r"(x.rh), "+r"(x.qt), "+r"(x.tile));
-            const ChunkSeg g = this_seg();
+            const ChunkSeg g = read_seg(bar->seg[seg % kSegs]);
             const int row = (pair ? u * rblk : 0) + m;  // row of the item
             const bool valid = m < rblk && row < g.nrows;
             const int tok = (pair ? u * tj : 0) + mtok;
@@ -645,10 +682,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         volatile unsigned* mask = bar->poison[seg & (kPoison - 1)];
                         unsigned any = 0u;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) any |= mask[e];
+                        for (int e = 0; e < 12; ++e) any |= mask[e];
                         if (any) {
                             const T* qrow = reinterpret_cast<const T*>(p.q + t * p.q_st + (int64_t)h * p.q_sh);
-                            for (int e = 0; e < 4; ++e) {
+                            for (int e = 0; e < 3; ++e) {
                                 if (g.slot < 0)
                                     add_nonfinite<T, T>(p, g.r, g.b, g.hkv, qrow, (mt0 + e) * kTT,
                                                         (const unsigned*)mask + 4 * e, 4, lim, lse2,
@@ -667,9 +704,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->x_done);
             }
-            ++seg;
-            if (!ok || !advance()) break;
-            ok = more();
+            release_seg(seg);
         }
     }
 
