@@ -21,24 +21,30 @@ namespace {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendCtas = 8;  // per SM: 64 registers a thread, 1024 threads with 64 bytes in flight each
 
+// Eight 16-bit elements as four fp32 pairs (two fp32 operations an instruction:
+// with one at a time this kernel was bound by its instructions).
+using Pair = unsigned long long;
 template <typename T>
-__device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
-    const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2(word_to_pair<T>(w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ void widen(const uint4& v, Pair (&x)[4]) {
+    x[0] = word_to_pair<T>(v.x);
+    x[1] = word_to_pair<T>(v.y);
+    x[2] = word_to_pair<T>(v.z);
+    x[3] = word_to_pair<T>(v.w);
 }
 template <typename T>
-__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
-    uint4 v;
-    v.x = f32_to_pair(make_float2(x[0], x[1]), T());
-    v.y = f32_to_pair(make_float2(x[2], x[3]), T());
-    v.z = f32_to_pair(make_float2(x[4], x[5]), T());
-    v.w = f32_to_pair(make_float2(x[6], x[7]), T());
-    return v;
+__device__ __forceinline__ uint4 narrow(const Pair (&x)[4]) {
+    return make_uint4(f32_to_pair(unpack2(x[0]), T()), f32_to_pair(unpack2(x[1]), T()),
+                      f32_to_pair(unpack2(x[2]), T()), f32_to_pair(unpack2(x[3]), T()));
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 // The request that owns row t: the largest b with query_start[b] <= t, -1 when
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
     }
     // cosines and sines of this lane's pairs: the same angle for both vectors'
     // elements (halves), or four angles a vector (neighbours)
-    float cs[8], sn[8];
+    Pair cs[4], sn[4];
     if (turned) {
         const float* c = a.cos_sin + (int64_t)pos * a.rot;
         const int i0 = a.interleaved ? 4 * u : 8 * u;
@@ -120,10 +126,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
         const float4 c1 = __ldg(reinterpret_cast<const float4*>(c + i1));
         const float4 s0 = __ldg(reinterpret_cast<const float4*>(c + a.rot / 2 + i0));
         const float4 s1 = __ldg(reinterpret_cast<const float4*>(c + a.rot / 2 + i1));
-        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
-        cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-        sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+        cs[0] = pack2f(c0.x, c0.y); cs[1] = pack2f(c0.z, c0.w);
+        cs[2] = pack2f(c1.x, c1.y); cs[3] = pack2f(c1.z, c1.w);
+        sn[0] = pack2f(s0.x, s0.y); sn[1] = pack2f(s0.z, s0.w);
+        sn[2] = pack2f(s1.x, s1.y); sn[3] = pack2f(s1.z, s1.w);
     }
     const float inv_d = 1.f / (float)p.D;
     while (row < rows) {
@@ -143,42 +149,52 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
             dst = v_at < 0 ? nullptr : p.v + v_at + (int64_t)(row - p.H - p.Hkv) * p.v_sh;
         }
         if (row < p.H + p.Hkv) {
-            float x0[8], x1[8];
+            Pair x0[4], x1[4];
             widen<T>(v0, x0);
             widen<T>(v1, x1);
             const unsigned char* w = row < p.H ? a.qw : a.kw;
             if (w) {
-                float ss = 0.f;
+                Pair sq = mul2(x0[0], x0[0]), sr = mul2(x1[0], x1[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], ss));
+                for (int i = 1; i < 4; ++i) {
+                    sq = fma2(x0[i], x0[i], sq);
+                    sr = fma2(x1[i], x1[i], sr);
+                }
+                const float2 f = unpack2(sq), g = unpack2(sr);
+                float ss = (f.x + f.y) + (g.x + g.y);
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o);
                 const float rs = rsqrtf(ss * inv_d + a.eps);
-                float w0[8], w1[8];
+                const Pair rs2 = pack2f(rs, rs);
+                Pair w0[4], w1[4];
                 widen<T>(mine ? __ldg(reinterpret_cast<const uint4*>(w + 2 * e0)) : zero, w0);
                 widen<T>(mine ? __ldg(reinterpret_cast<const uint4*>(w + 2 * e1)) : zero, w1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x0[i] = x0[i] * rs * w0[i];
-                    x1[i] = x1[i] * rs * w1[i];
+                for (int i = 0; i < 4; ++i) {
+                    x0[i] = mul2(mul2(x0[i], rs2), w0[i]);
+                    x1[i] = mul2(mul2(x1[i], rs2), w1[i]);
                 }
             }
             if (turned) {
                 if (a.interleaved) {
+                    // pair i of a vector turns by one angle: (a c - b s, b c + a s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float a0 = x0[2 * i], b0 = x0[2 * i + 1], a1 = x1[2 * i], b1 = x1[2 * i + 1];
-                        x0[2 * i] = a0 * cs[i] - b0 * sn[i];
-                        x0[2 * i + 1] = b0 * cs[i] + a0 * sn[i];
-                        x1[2 * i] = a1 * cs[4 + i] - b1 * sn[4 + i];
-                        x1[2 * i + 1] = b1 * cs[4 + i] + a1 * sn[4 + i];
+                        const float2 p0 = unpack2(x0[i]), p1 = unpack2(x1[i]);
+                        const float2 ca = unpack2(cs[i >> 1]), sa = unpack2(sn[i >> 1]);
+                        const float2 cb = unpack2(cs[2 + (i >> 1)]), sb = unpack2(sn[2 + (i >> 1)]);
+                        const float c0 = i & 1 ? ca.y : ca.x, s0 = i & 1 ? sa.y : sa.x;
+                        const float c1 = i & 1 ? cb.y : cb.x, s1 = i & 1 ? sb.y : sb.x;
+                        x0[i] = fma2(x0[i], pack2f(c0, c0), pack2f(-p0.y * s0, p0.x * s0));
+                        x1[i] = fma2(x1[i], pack2f(c1, c1), pack2f(-p1.y * s1, p1.x * s1));
                     }
                 } else {
+                    const Pair minus = pack2f(-1.f, -1.f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float f = x0[i], s = x1[i];
-                        x0[i] = f * cs[i] - s * sn[i];
-                        x1[i] = s * cs[i] + f * sn[i];
+                    for (int i = 0; i < 4; ++i) {
+                        const Pair f = x0[i], g = x1[i];
+                        x0[i] = fma2(f, cs[i], mul2(mul2(g, minus), sn[i]));
+                        x1[i] = fma2(g, cs[i], mul2(f, sn[i]));
                     }
                 }
             }
