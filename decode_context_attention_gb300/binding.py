@@ -461,10 +461,10 @@ class _PreparedOn(_Prepared):
 
     def __init__(self, fn, name: str, device, args: tuple, keep: tuple):
         self._fn, self._name, self._args, self._keep = fn, name, args, keep
-        self._device = device.index if device.type == "cuda" else None
+        self._device = device.index
 
     def __call__(self) -> None:
-        if self._device is None or self._device == torch.cuda.current_device():
+        if self._device == torch.cuda.current_device():
             st = self._fn(*self._args)
         else:
             with torch.cuda.device(self._device):
@@ -475,7 +475,7 @@ class _PreparedOn(_Prepared):
 
 def _run_on(device, fn, name: str, args: tuple) -> None:
     """One call with `device` current."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
+    if device.index == torch.cuda.current_device():
         st = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -485,16 +485,23 @@ def _run_on(device, fn, name: str, args: tuple) -> None:
 
 
 def _chunk_device(q: torch.Tensor, *ts) -> torch.device:
-    """The device of the operands: `q`'s, which the other CUDA tensors share."""
+    """The device of the operands, which share it.  Host tensors are refused,
+    pinned ones too: pages and queries are read by the TMA unit."""
     d = q.device
+    if d.type != "cuda":
+        raise ValueError("the chunk-serving kernels take CUDA tensors only (no CPU fallback, no pinned host memory)")
     for t in ts:
         if t is not None and t.device != d:
-            _need_cuda(t)
-            if t.is_cuda and q.is_cuda:
-                raise ValueError(f"operands on {d} and {t.device}")
-    if not q.is_cuda:
-        _need_cuda(q, *ts)
+            raise ValueError(f"operands on {d} and {t.device}")
     return d
+
+
+def _length(name: str, n: int) -> int:
+    """A token count for a C int: ctypes would drop the high bits of a larger one."""
+    n = int(n)
+    if n > 0x7FFFFFFF or n < -0x80000000:
+        raise ValueError(f"{name}={n} does not fit 32 bits")
+    return n
 
 
 # the raw handle of the current stream without building a Stream object, where torch has it
@@ -503,9 +510,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream_on(device, stream) -> int:
     if stream is None:
-        if _raw_stream is not None and device.type == "cuda":
+        if _raw_stream is not None:
             return _raw_stream(device.index)
-        return torch.cuda.current_stream(device if device.type == "cuda" else None).cuda_stream
+        return torch.cuda.current_stream(device).cuda_stream
     return _stream_handle(stream)
 
 
@@ -562,6 +569,7 @@ def _append_args(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, 
     dev = _chunk_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
                         seq_lens, q_out)
     T, H, D = q.shape
+    max_seq_len = _length("max_seq_len", max_seq_len)
     pool = k_pages.shape
     N, num_pages, page_size, Hkv, _ = pool
     B = seq_lens.shape[0]
@@ -587,7 +595,7 @@ def _append_args(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, 
                  *_rows_args(v, kv, "v"), qw, kw, float(eps), cs, npos, rot, 1 if interleaved else 0, ps,
                  *_rows_args(q_out, rows, "q_out"), *_pool_args(k_pages, pool), *_pool_args(v_pages, pool), num_pages,
                  page_size, *_table_args(block_table, N, B), _int32("query_start", query_start, B + 1),
-                 _int32("seq_lens", seq_lens, B), int(max_seq_len), _stream_on(dev, stream))
+                 _int32("seq_lens", seq_lens, B), max_seq_len, _stream_on(dev, stream))
 
 
 def prepare_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
@@ -620,7 +628,7 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_
 
 def extend_workspace_bytes(N: int, B: int, T: int, H: int, Hkv: int, D: int, max_seq_len: int) -> int:
     """Bytes of workspace extend_attention_paged needs on the current device."""
-    return dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, int(max_seq_len))
+    return dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, _length("max_seq_len", max_seq_len))
 
 
 def _scratch(nbytes: int, device, stream):
@@ -641,6 +649,7 @@ def _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_se
                  workspace, stream):
     dev = _chunk_device(q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace)
     T, H, D = q.shape
+    max_seq_len = _length("max_seq_len", max_seq_len)
     pool = k_pages.shape
     N, num_pages, page_size, Hkv, _ = pool
     B = seq_lens.shape[0]
@@ -649,18 +658,17 @@ def _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_se
     code = _same_dtype(q, k_pages, v_pages, o)
     args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, pool),
             *_pool_args(v_pages, pool), num_pages, page_size, *_table_args(block_table, N, B),
-            _int32("query_start", query_start, B + 1), _int32("seq_lens", seq_lens, B), int(max_seq_len), float(sm_scale),
+            _int32("query_start", query_start, B + 1), _int32("seq_lens", seq_lens, B), max_seq_len, float(sm_scale),
             1 if causal else 0, *_rows_args(o, (N, T, H, D), "o"), *_word_args(lse, (N, T, H), "lse"),
             _base_code(base))
     if workspace is None:
-        on = dev if dev.type == "cuda" else torch.device("cuda", torch.cuda.current_device())
         size = load().dcp_extend_attention_workspace_size
-        if on.index == torch.cuda.current_device():
-            nbytes = size(N, B, T, H, Hkv, D, int(max_seq_len))
+        if dev.index == torch.cuda.current_device():
+            nbytes = size(N, B, T, H, Hkv, D, max_seq_len)
         else:
-            with torch.cuda.device(on):
-                nbytes = size(N, B, T, H, Hkv, D, int(max_seq_len))
-        workspace = _scratch(nbytes, on, stream)
+            with torch.cuda.device(dev):
+                nbytes = size(N, B, T, H, Hkv, D, max_seq_len)
+        workspace = _scratch(nbytes, dev, stream)
     return dev, workspace, (*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                             _stream_on(dev, stream))
 
@@ -692,6 +700,7 @@ def extend_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_le
 def _weights_args(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale, base, stream):
     dev = _chunk_device(q, k_pages, block_table, query_start, seq_lens, lse, acc)
     T, H, D = q.shape
+    max_seq_len = _length("max_seq_len", max_seq_len)
     pool = k_pages.shape
     N, num_pages, page_size, Hkv, _ = pool
     B = seq_lens.shape[0]
@@ -703,7 +712,7 @@ def _weights_args(q, k_pages, block_table, query_start, seq_lens, max_seq_len, l
         raise ValueError("acc is fp32 [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
     return dev, (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, pool), num_pages,
                  page_size, *_table_args(block_table, N, B), _int32("query_start", query_start, B + 1),
-                 _int32("seq_lens", seq_lens, B), int(max_seq_len), float(sm_scale), *_word_args(lse, (T, H), "lse"),
+                 _int32("seq_lens", seq_lens, B), max_seq_len, float(sm_scale), *_word_args(lse, (T, H), "lse"),
                  _base_code(base), *_rows_args(acc, (N, B, Hkv, cap), "acc"), _stream_on(dev, stream))
 
 
@@ -732,6 +741,9 @@ def attention_weights_paged(q, k_pages, block_table, query_start, seq_lens, max_
 def _evict_args(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent, dst_table,
                 kept, acc_out, stream):
     dev = _chunk_device(k_pages, v_pages, block_table, seq_lens, acc, keep_lens, dst_table, kept, acc_out)
+    max_seq_len = _length("max_seq_len", max_seq_len)
+    # more than a request can hold means all of it
+    max_keep, recent = (_length(k, min(x, max(max_seq_len, 0))) for k, x in (("max_keep", max_keep), ("recent", recent)))
     pool = k_pages.shape
     N, num_pages, page_size, Hkv, D = pool
     B = seq_lens.shape[0]
@@ -741,11 +753,11 @@ def _evict_args(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_
         raise ValueError("acc and acc_out are fp32, kept is int32")
     if cap * N < max_seq_len:
         raise ValueError("acc is [N, B, Hkv, cap] with cap >= ceil(max_seq_len / N)")
-    if kcap * N < min(max_keep, max_seq_len):
+    if kcap * N < max_keep:
         raise ValueError("kept and acc_out are [N, B, Hkv, kcap] with kcap >= ceil(max_keep / N)")
     return dev, (code, N, B, Hkv, D, *_pool_args(k_pages, pool), *_pool_args(v_pages, pool), num_pages, page_size,
-                 *_table_args(block_table, N, B), _int32("seq_lens", seq_lens, B), int(max_seq_len),
-                 *_rows_args(acc, (N, B, Hkv, cap), "acc"), _int32("keep_lens", keep_lens, B), int(max_keep), int(recent),
+                 *_table_args(block_table, N, B), _int32("seq_lens", seq_lens, B), max_seq_len,
+                 *_rows_args(acc, (N, B, Hkv, cap), "acc"), _int32("keep_lens", keep_lens, B), max_keep, recent,
                  *_table_args(dst_table, N, B, "dst_table"), *_rows_args(kept, (N, B, Hkv, kcap), "kept"),
                  *_rows_args(acc_out, (N, B, Hkv, kcap), "acc_out"), _stream_on(dev, stream))
 

@@ -22,6 +22,12 @@
 // worked on, a ring of query tiles); warp 17: MMAs; warps 18 and 19: the
 // log-sum-exps of the even and the odd query tiles' rows.
 // Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
+// Measured (D = 128, bf16, 32 query heads over 4): one new token of 64 requests of
+// 8192 tokens, 4 ranks: 98 us, 5.7 TB/s, bound by the keys' bytes (83 us at the copy
+// rate); 2048 new tokens over 16384, 2 ranks: 275 us, 0.94 PFLOP/s: the two tiles'
+// 2 x 128 exponentials a row of threads take the multi-function unit as long as
+// their products take the tensor core, each is busy half the time, and 256 blocks
+// over 152 CTAs leave a sixth of it idle.
 #include <cuda.h>
 #include <math.h>
 #include <stdlib.h>
@@ -159,8 +165,8 @@ __device__ int64_t wwork_before(const WWork& w, int k) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsW, 1)
-    chunk_weights_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap_few,
-                            const __grid_constant__ CUtensorMap kmap, const ChunkParams p, const int few) {
+    chunk_weights_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                            const ChunkParams p) {
     using W = WShape<D>;
     constexpr int kTileBytes = W::kTileBytes, kQSlots = W::kQSlots, NCH = D / 64;
     extern __shared__ uint8_t smem_raw[];
@@ -259,7 +265,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     }
     if (warp == 16 && lane == 0) {
         tma_prefetch_map(&qmap);
-        tma_prefetch_map(&qmap_few);
         tma_prefetch_map(&kmap);
     }
     fence_proxy_async_smem();  // the range's scratch is overwritten by copies
@@ -312,14 +317,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                         go = 0;
                         break;
                     }
-                    // a tile of few new tokens is loaded by a smaller box
-                    const int j = g.j0 + k * tj;
-                    const bool small = g.q.n - j <= few;
-                    mbar_arrive_expect_tx(&bar->q_full[s], (uint32_t)(NCH * (small ? few : tj) * p.gq * 128));
+                    // whole boxes, also past the request's last row (a smaller box for
+                    // few new tokens gained nothing: 98 us either way at 64 single ones)
+                    mbar_arrive_expect_tx(&bar->q_full[s], (uint32_t)(NCH * tj * p.gq * 128));
 #pragma unroll
                     for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(qring + s * kTileBytes + c * kChunkB, small ? &qmap_few : &qmap, &bar->q_full[s],
-                                    64 * c, g.hkv * p.gq, g.q.start + j);
+                        tma_load_3d(qring + s * kTileBytes + c * kChunkB, &qmap, &bar->q_full[s], 64 * c, g.hkv * p.gq,
+                                    g.q.start + g.j0 + k * tj);
                 }
             }
             qc = __shfl_sync(kAllLanes, qc, 0);
@@ -540,35 +544,35 @@ __global__ void __launch_bounds__(kThreadsW, 1)
 }
 
 template <typename T, int D>
-cudaError_t launch_weights_tc(const ChunkParams& p, const CUtensorMap (&maps)[3], int few, cudaStream_t stream) {
+cudaError_t launch_weights_tc(const ChunkParams& p, const CUtensorMap (&maps)[2], cudaStream_t stream) {
     const void* k = (const void*)chunk_weights_tc_kernel<T, D>;
     // the shared-memory opt-in is a per-device function attribute
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, WShape<D>::kSmem);
     if (e != cudaSuccess) return e;
     chunk_weights_tc_kernel<T, D>
-        <<<device_sm_count(), kThreadsW, WShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, few);
+        <<<device_sm_count(), kThreadsW, WShape<D>::kSmem, stream>>>(maps[0], maps[1], p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
-    if ((p.D != 64 && p.D != 128) || p.page_shift < 3) return false;  // boxes hold whole 8-row swizzle atoms
+    // boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one is
+    // faster at every size measured: 98 against 147 us (64 single tokens, 8192),
+    // 74 against 178 us (ragged, 12 heads a group), 275 against 1412 us (2048 new)
+    if ((p.D != 64 && p.D != 128) || p.page_shift < 3) return false;
     const EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
     const CUtensorMapDataType dt = dtype == DCP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     // a dimension of extent 1 is never stepped over: give it a nominal stride
     auto stride = [](int64_t extent, int64_t bytes) -> cuuint64_t { return (cuuint64_t)(extent > 1 ? bytes : 256); };
-    CUtensorMap maps[3];
+    CUtensorMap maps[2];
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-    // query tiles of up to 128 / gq new tokens, and of as few as a request has on average
-    const int tj = kM / p.gq;
-    const int few = (int)(((int64_t)p.T + p.B - 1) / p.B < tj ? ((int64_t)p.T + p.B - 1) / p.B : tj);
-    for (int m = 0; m < 2; ++m) {
+    {
         const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.T};
         const cuuint64_t strides[2] = {stride(p.H, p.q_sh), stride(p.T, p.q_st)};
-        const cuuint32_t box[3] = {64, (cuuint32_t)p.gq, (cuuint32_t)(m ? few : tj)};
-        if (enc(&maps[m], dt, 3, const_cast<unsigned char*>(p.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        const cuuint32_t box[3] = {64, (cuuint32_t)p.gq, (cuuint32_t)(kM / p.gq)};
+        if (enc(&maps[0], dt, 3, const_cast<unsigned char*>(p.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;
@@ -580,7 +584,7 @@ bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t strea
         const cuuint64_t strides[4] = {stride(p.Hkv, p.k_sh), stride(rows, p.k_st), stride(p.num_pages, p.k_sp),
                                        stride(p.N, p.k_sn)};
         const cuuint32_t box[5] = {64, 1, (cuuint32_t)(rows < kM ? rows : kM), 1, 1};
-        if (enc(&maps[2], dt, 5, p.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        if (enc(&maps[1], dt, 5, p.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;  // strides a tensor map cannot describe: the register-tiled kernel takes it
@@ -591,11 +595,11 @@ bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t strea
     const char* stall = getenv("DCP_TEST_STALL_LOADS");
     q.stall_loads = stall && stall[0] == '1';
     if (p.D == 128)
-        *err = dtype == DCP_F16 ? launch_weights_tc<__half, 128>(q, maps, few, stream)
-                                : launch_weights_tc<__nv_bfloat16, 128>(q, maps, few, stream);
+        *err = dtype == DCP_F16 ? launch_weights_tc<__half, 128>(q, maps, stream)
+                                : launch_weights_tc<__nv_bfloat16, 128>(q, maps, stream);
     else
-        *err = dtype == DCP_F16 ? launch_weights_tc<__half, 64>(q, maps, few, stream)
-                                : launch_weights_tc<__nv_bfloat16, 64>(q, maps, few, stream);
+        *err = dtype == DCP_F16 ? launch_weights_tc<__half, 64>(q, maps, stream)
+                                : launch_weights_tc<__nv_bfloat16, 64>(q, maps, stream);
     return true;
 }
 

@@ -13,6 +13,9 @@
 // bytes.
 // The rows then move by a second kernel, whose bytes are the cost: two reads and
 // two writes of every kept head row, four rows a thread in flight.
+// Measured (bf16, D = 128): 32 requests of 8192 tokens on 4 ranks cut to half, 4 KV
+// heads: 106 us, of which 84 move 537 MB (6.4 TB/s) and the rest selects;
+// 131072 tokens to 8192 on 2 ranks, 8 KV heads: 43 us, 30 of them the selection.
 #include <cooperative_groups.h>
 
 #include "dcp_chunk.cuh"
@@ -270,7 +273,9 @@ cudaError_t launch_evict(const EvictParams& e, cudaStream_t stream) {
     const ChunkParams& p = e.c;
     const int64_t problems = (int64_t)p.N * p.B * p.Hkv;
     const int64_t cap = ((int64_t)p.max_seq_len + p.N - 1) / p.N;
-    // CTAs of a problem: as many as the SMs have room for, a step of keys each at least
+    // CTAs of a problem: as many as the SMs have room for, a step of keys each at
+    // least (131072 tokens, 16 problems: 43 us with 8, 151 us with one; 512 problems
+    // fill the SMs with one each: 106 us)
     int cs = 1;
     while (cs < 8 && problems * cs * 2 <= 2 * device_sm_count() && cap > (int64_t)cs * 4 * kSelThreads) cs *= 2;
     const int64_t slice = (((cap + 4 * kSelThreads - 1) / (4 * kSelThreads) + cs - 1) / cs) * 4 * kSelThreads;

@@ -412,6 +412,8 @@ dcp_status_t dcp_decode_attention_mla(int dtype, int N, int B, int H, int Dk, in
  *               ceil(ceil(max_seq_len / N) / page_size) entries; only entries of
  *               tokens that exist are read.  Rows start on 16-byte
  *               boundaries; page_size a power of two up to 65536.
+ * Every operand is device memory of the current device: pinned host memory is
+ * not taken here (queries and pages are read by the TMA unit).
  * With L_r(n) = n / N + (r < n % N) the rank-local share of n tokens.
  */
 

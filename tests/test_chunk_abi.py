@@ -175,6 +175,12 @@ def test_torch_layer_checks_shapes_and_types():
         binding.attention_weights_paged(q, kp, bt, qs, sl, 100, lse, acc, 0.1)
 
 
+def test_lengths_beyond_32_bits_are_refused():
+    for n in (1 << 31, (1 << 32) + 5, -(1 << 40)):
+        with pytest.raises(ValueError):
+            binding.extend_workspace_bytes(2, 3, 8, 4, 2, 128, n)
+
+
 def test_symbols_are_exported(lib):
     for name in ("dcp_qk_norm_rope_append", "dcp_extend_attention_workspace_size", "dcp_extend_attention_paged",
                  "dcp_attention_weights_paged", "dcp_cache_evict_paged"):

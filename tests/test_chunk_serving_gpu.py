@@ -255,6 +255,41 @@ def test_two_threads_on_their_own_streams():
         xs[t][0].check(xs[t][1][0])
 
 
+def test_host_tensors_and_long_lengths_are_refused():
+    sv = Server(N=2, B=2, H=4, Hkv=2, max_len=100)
+    x = sv.batch([20, 30])
+    sv.append(x)
+    args = [x["qn"], sv.k_pages, sv.v_pages, sv.table, x["qs"], x["sl"], sv.max_len, x["o"], x["lse"], sv.scale]
+    for i in (0, 1, 2, 3, 4, 5, 7, 8):
+        for host in (args[i].cpu(), args[i].cpu().pin_memory()):
+            with pytest.raises(ValueError):
+                binding.extend_attention_paged(*args[:i], host, *args[i + 1:])
+    with pytest.raises(ValueError):
+        binding.extend_attention_paged(*args[:6], (1 << 32) + sv.max_len, *args[7:])
+    binding.extend_attention_paged(*args)
+
+
+def test_a_recent_window_beyond_every_length_keeps_the_latest():
+    sv = Server(N=2, B=2, H=4, Hkv=2, max_len=100)
+    x = sv.batch([60, 90])
+    sv.append(x)
+    sv.acc.uniform_(0, 1, generator=sv.g)
+    keep = torch.tensor([20, 31], dtype=torch.int32, device=DEV)
+    outs = []
+    for recent in (100, 1 << 40):
+        kept = torch.full((2, 2, 2, 50), -1, dtype=torch.int32, device=DEV)
+        out = torch.full((2, 2, 2, 50), math.nan, device=DEV)
+        binding.cache_evict_paged(sv.k_pages, sv.v_pages, sv.table, x["sl"], 100, sv.acc, keep, 1 << 40, recent, sv.spare,
+                                  kept, out)
+        outs.append(kept)
+    assert torch.equal(*outs)
+    for b, (n, k) in enumerate(((60, 20), (90, 31))):
+        for r in range(2):
+            held, some = share(n, r, 2), share(k, r, 2)
+            want = torch.arange(held - some, held, dtype=torch.int32, device=DEV)
+            assert (outs[0][r, b, :, :some] == want).all() and (outs[0][r, b, :, some:] == -1).all()
+
+
 STALL = r"""
 import os, sys
 sys.path[:0] = [sys.argv[1], os.path.join(sys.argv[1], "tests")]
