@@ -89,7 +89,8 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 // ---------------------------------------------------------------------------
 // The split of a ragged batch's attention.  An item is (request, rank, KV head,
 // block of `tpi` new tokens); its work is the tiles of `tt` cached tokens its
-// rows see, plus a fixed part.  The items' total is cut into `ctas` equal
+// rows see, dearer when the item has more new tokens than `half` (it then fills
+// both row blocks of a CTA), plus a fixed part.  The items' total is cut into `ctas` equal
 // ranges: a range starts and ends inside items, so every CTA has the same work
 // whatever the mix of long and short requests, and a single request with a
 // long cache is split over all of them.  Items that are cut leave partial
@@ -121,7 +122,9 @@ __device__ __forceinline__ ChunkPos next_item(const ChunkParams& p, const ChunkP
     return y;
 }
 
-constexpr int kItemCost = 4;  // fixed part of an item's work, in tiles (2, 4, 6 for a mixed batch: 205, 187, 197 us)
+constexpr int kPairTile = 4, kBlockTile = 3;  // work of a tile of two row blocks, and of one
+constexpr int kItemCost = 13;                 // fixed part of an item's work (about 4.8 us against 1.5 us a pair's tile)
+// A mixed batch of 17 requests: 144 us; with 4, 3, 9: 146, with 4, 3, 18: 165, with 2, 1, 5: 161
 constexpr int kMinPart = 4;   // a cut leaves at least this many tiles on both sides
 
 // The work of one KV head of a (request, rank), by blocks of new tokens.
@@ -129,15 +132,19 @@ struct HeadWork {
     int nq;       // blocks
     int last;     // tiles of the last one
     int q0;       // blocks that see nothing because the request has more new tokens than tokens
+    int wf, wl;   // weight of a tile: of a full block, of the last one
     int64_t a, b, m;
+    __device__ int weight(int q) const { return q < nq - 1 ? wf : wl; }
 };
-__device__ inline HeadWork head_work(const ChunkParams& p, int pair, int tpi, int tt) {
+__device__ inline HeadWork head_work(const ChunkParams& p, int pair, int tpi, int half, int tt) {
     HeadWork w;
     const int r = pair % p.N;
     const Request q = load_request(p, pair / p.N);
     w.nq = (q.n + tpi - 1) / tpi;
     w.last = (rank_share(q.L, r, p.N) + tt - 1) / tt;  // its last row is the request's last token
     w.q0 = 0;
+    w.wf = tpi > half ? kPairTile : kBlockTile;
+    w.wl = q.n - (w.nq - 1) * tpi > half ? kPairTile : kBlockTile;
     w.m = (int64_t)p.N * tt;
     if (p.causal) {
         // block qt's last row has x = L - n + (qt + 1) tpi tokens before or at it: rank_share(x) =
@@ -158,48 +165,57 @@ __device__ inline HeadWork head_work(const ChunkParams& p, int pair, int tpi, in
 __device__ inline int64_t work_before(const HeadWork& w, int q) {
     const int k = min(q, w.nq - 1) - w.q0;
     int64_t c = (int64_t)q * kItemCost;
-    if (k > 0) c += floor_sum(k, w.m, w.a, w.b);
-    if (q >= w.nq && w.nq > 0) c += w.last;
+    if (k > 0) c += w.wf * floor_sum(k, w.m, w.a, w.b);
+    if (q >= w.nq && w.nq > 0) c += (int64_t)w.wl * w.last;
     return c;
 }
 
 // The start of range c of `ctas`.  upto[t] is the work up to and with the pairs of
-// slot t (`per` (request, rank) pairs each, `slots` slots).  One thread.
-__device__ __forceinline__ ChunkPos range_start(const ChunkParams& p, int tpi, int tt, int ctas, int c,
+// slot t (`per` (request, rank) pairs each, `slots` slots).  One warp, whose lanes
+// try as many places of a search at once.
+__device__ __forceinline__ ChunkPos range_start(const ChunkParams& p, int tpi, int half, int tt, int ctas, int c,
                                                 const int64_t* upto, int slots, int64_t per) {
+    const unsigned all = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
     ChunkPos x = {p.B, 0, 0, 0};
     const int64_t total = upto[slots - 1];
     const int64_t at = (int64_t)((double)total * c / ctas);  // exact below 2^53 / ctas, monotone above
     if (c >= ctas || at >= total) return x;
-    int lo = 0, hi = slots - 1;  // the first slot whose pairs pass `at`
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (upto[mid] > at) hi = mid;
-        else lo = mid + 1;
-    }
-    int64_t rem = at - (lo ? upto[lo - 1] : 0);
-    int64_t pair = lo * per;
-    HeadWork w = head_work(p, (int)pair, tpi, tt);
+    // the last place of [lo, hi] for which before(place) <= at holds: it does for lo, and up to some place
+    auto search = [&](int lo, int hi, auto before) {
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32;
+            const int n = __popc(__ballot_sync(all, before(min(lo + (lane + 1) * step, hi))));
+            const int next = n < 32 ? min(lo + (n + 1) * step, hi) - 1 : hi;
+            lo = min(lo + n * step, hi);
+            hi = max(next, lo);
+        }
+        return lo;
+    };
+    // the first slot whose pairs pass `at`
+    const int slot = search(0, slots - 1, [&](int k) { return upto[k - 1] <= at; });
+    int64_t rem = at - (slot ? upto[slot - 1] : 0);
+    int64_t pair = slot * per;
+    HeadWork w = head_work(p, (int)pair, tpi, half, tt);
     int64_t head = work_before(w, w.nq);
     while (rem >= head * p.Hkv) {  // `at` lies in one of this slot's pairs
         rem -= head * p.Hkv;
-        w = head_work(p, (int)++pair, tpi, tt);
+        w = head_work(p, (int)++pair, tpi, half, tt);
         head = work_before(w, w.nq);
     }
     const int b = (int)(pair / p.N), r = (int)(pair - (int64_t)b * p.N);
     const int hkv = (int)(rem / head);
     rem -= hkv * head;
-    int q0 = 0, q1 = w.nq - 1;  // the last block whose work starts at or before rem
-    while (q0 < q1) {
-        const int mid = (q0 + q1 + 1) >> 1;
-        if (work_before(w, mid) <= rem) q0 = mid;
-        else q1 = mid - 1;
-    }
-    const int64_t begin = work_before(w, q0);
-    const int n = (int)(work_before(w, q0 + 1) - begin) - kItemCost, off = (int)(rem - begin);
-    x = {b, r * p.Hkv + hkv, q0, max(off - kItemCost, 0)};
+    // the last block whose work starts at or before rem
+    const int q0 = search(0, w.nq - 1, [&](int k) { return work_before(w, k) <= rem; });
+    const int64_t begin = work_before(w, q0 + (lane & 1));  // of q0 and of the block after it
+    const int weight = w.weight(q0);
+    const int work = (int)(__shfl_sync(all, begin, 1) - __shfl_sync(all, begin, 0)) - kItemCost;
+    const int off = (int)(rem - __shfl_sync(all, begin, 0));
+    const int n = work / weight;
+    x = {b, r * p.Hkv + hkv, q0, max(off - kItemCost, 0) / weight};
     // a cut near an end of its item, or into a short one, moves to the nearer end
-    if (2 * off < n + kItemCost) {
+    if (2 * off < work + kItemCost) {
         if (x.tile < kMinPart || n < 2 * kMinPart) x.tile = 0;
     } else if (n - x.tile < kMinPart || n < 2 * kMinPart) {
         x = next_item(p, x, tpi);
@@ -211,14 +227,14 @@ __device__ __forceinline__ ChunkPos range_start(const ChunkParams& p, int tpi, i
 // ranges left in pos for the merge.  `scratch` holds THREADS + 32 numbers.  All
 // threads of the CTA; ends with a barrier.
 template <int THREADS>
-__device__ __forceinline__ void find_range(const ChunkParams& p, int tpi, int tt, ChunkPos* pos, int64_t* scratch,
-                                           ChunkPos* range) {
+__device__ __forceinline__ void find_range(const ChunkParams& p, int tpi, int half, int tt, ChunkPos* pos,
+                                           int64_t* scratch, ChunkPos* range) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t npairs = (int64_t)p.B * p.N;
     const int64_t per = (npairs + THREADS - 1) / THREADS;
     int64_t sum = 0;
     for (int64_t i = tid * per; i < min((tid + 1) * per, npairs); ++i) {
-        const HeadWork w = head_work(p, (int)i, tpi, tt);
+        const HeadWork w = head_work(p, (int)i, tpi, half, tt);
         sum += work_before(w, w.nq) * p.Hkv;
     }
 #pragma unroll
@@ -231,11 +247,13 @@ __device__ __forceinline__ void find_range(const ChunkParams& p, int tpi, int tt
     for (int w = 0; w < warp; ++w) sum += scratch[THREADS + w];
     scratch[tid] = sum;
     __syncthreads();
-    if (lane == 0 && warp < 2) {
+    if (warp < 2) {
         const int c = (int)blockIdx.x + warp;
-        const ChunkPos x = range_start(p, tpi, tt, (int)gridDim.x, c, scratch, THREADS, per);
-        range[warp] = x;
-        if (warp == 0 || c == (int)gridDim.x) pos[c] = x;
+        const ChunkPos x = range_start(p, tpi, half, tt, (int)gridDim.x, c, scratch, THREADS, per);
+        if (lane == 0) {
+            range[warp] = x;
+            if (warp == 0 || c == (int)gridDim.x) pos[c] = x;
+        }
     }
     __syncthreads();
 }

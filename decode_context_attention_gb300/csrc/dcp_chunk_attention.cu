@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
     __shared__ unsigned poison[4][2];  // tokens of the item's masked tiles whose V row is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     __shared__ ChunkPos range[2];
-    find_range<kThreadsMma>(p, tpi, kTile, ws.pos, reinterpret_cast<int64_t*>(smem), range);
+    find_range<kThreadsMma>(p, tpi, tpi, kTile, ws.pos, reinterpret_cast<int64_t*>(smem), range);
     ChunkPos x = range[0];
     const ChunkPos end = range[1];
     const ChunkPos first = x;

@@ -144,6 +144,14 @@ __device__ __forceinline__ void exp_store(const uint32_t (&v)[128], uint32_t tP,
     tmem_st16(tP, w);
 }
 
+// mbar_wait with its long path out of line: the loops around it fit the instruction cache.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return mbar_wait(bar, parity, &g_chunk_status, DCP_ERR_TIMEOUT, abort);
+}
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     chunk_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int rblk = tj * p.gq;    // its rows (at most 128)
 
     // the Q blocks are not in use yet
-    find_range<kThreadsTc>(p, tpi, kTT, ws.pos, reinterpret_cast<int64_t*>(smem), bar->range);
+    find_range<kThreadsTc>(p, tpi, tj, kTT, ws.pos, reinterpret_cast<int64_t*>(smem), bar->range);
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&bar->full[s], 1);
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     int go = 1;
                     if (lane == 0) {
                         if (qn[u] > 0)
-                            go = mbar_wait(&bar->q_empty[u], (qn[u] - 1) & 1, status, DCP_ERR_TIMEOUT, abort);
+                            go = wait_short(&bar->q_empty[u], (qn[u] - 1) & 1, abort);
                         if (go) {
                             mbar_arrive_expect_tx(&bar->q_full[u], (uint32_t)(NCH * rblk * 128));
                             for (int c = 0; c < NCH; ++c)
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     int go = 1;
                     if (lane == 0) {
                         if (pos >= kSlots)
-                            go = mbar_wait(&bar->empty[s], (pos / kSlots - 1) & 1, status, DCP_ERR_TIMEOUT, abort);
+                            go = wait_short(&bar->empty[s], (pos / kSlots - 1) & 1, abort);
                         if (go) {
                             mbar_arrive_expect_tx(&bar->full[s], (uint32_t)(NCH * nseg * pb * 128));
                             __threadfence_block();
@@ -327,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 auto pos_k = [&](int i) { return base + (pair ? 2 * i : (i < 2 ? i : 2 * i - 1)); };
                 auto pos_v = [&](int i) { return base + (pair ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1)); };
                 auto wait = [&](uint64_t* b, int parity) -> bool {
-                    return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
+                    return __all_sync(kAllLanes, wait_short(b, parity & 1, abort));
                 };
                 auto issue_s = [&](int u, int i, bool release, bool last) -> bool {
                     const int j = pos_k(i), s = j % kSlots;
@@ -336,10 +344,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const uint64_t da = smem_desc(qa + u * kTileBytes, 16, 1024, kSwizzle128B);
                     const uint64_t db = smem_desc(ra + s * kTileBytes, 16, 1024, kSwizzle128B);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kChunkB + (kk & 3) * 32) >> 4);
-                        mma_ss_warp(tm + kM * u, da + off, db + off, idesc_s, kk > 0 ? 1u : 0u);
-                    }
+                    for (int c = 0; c < NCH; ++c)  // 64 elements of D a time: 16 are 32 bytes of a swizzled row
+                        mma_ss4_warp<2, 2>(tm + kM * u, (uint32_t)da + c * (kChunkB >> 4), (uint32_t)(da >> 32),
+                                           (uint32_t)db + c * (kChunkB >> 4), (uint32_t)(db >> 32), idesc_s, c > 0);
                     mma_commit_warp(&bar->s_full[u]);
                     if (release) mma_commit_warp(&bar->empty[s]);
                     if (last) mma_commit_warp(&bar->q_empty[u]);
@@ -358,9 +365,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     tc_fence_after();
                     const uint64_t dv = smem_desc(ra + s * kTileBytes, kChunkB, 1024, kSwizzle128B);
 #pragma unroll
-                    for (int kk = 0; kk < kTT / 16; ++kk)
-                        mma_ts_warp(tm + kColO + D * u, tm + kM * u + 8 * kk, dv + (uint64_t)((2048 * kk) >> 4), idesc_o,
-                                    (!begin || kk > 0) ? 1u : 0u);
+                    for (int c = 0; c < kTT / 64; ++c)  // 16 tokens are 8 columns of P and 2 KB of V
+                        mma_ts4_warp<8, 128>(tm + kColO + D * u, tm + kM * u + 32 * c, (uint32_t)dv + 512 * c,
+                                             (uint32_t)(dv >> 32), idesc_o, !begin || c > 0);
                     mma_commit_warp(&bar->pv_done[u]);
                     if (release) mma_commit_warp(&bar->empty[s]);
                     return true;
@@ -409,6 +416,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     // way (and the slot cannot pass on before this tile is clean)
                     const uint64_t t_start = global_timer_ns();
                     while (*(volatile int*)&bar->issued <= j && !*abort) {
+                        __nanosleep(200);
                         if (global_timer_ns() - t_start > kWaitLimitNs) {
                             atomicCAS(status, 0, DCP_ERR_TIMEOUT);
                             *abort = 1;
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     __threadfence_block();
                     ok = !__any_sync(kAllLanes, *abort != 0) &&
                          __all_sync(kAllLanes,
-                                    mbar_wait(&bar->full[s], (j / kSlots) & 1, status, DCP_ERR_TIMEOUT, abort));
+                                    wait_short(&bar->full[s], (j / kSlots) & 1, abort));
                     if (!ok) break;
                     uint8_t* tile = ring + s * kTileBytes;
                     // 16 bytes a lane, 4 rows of 128 bytes a step
@@ -466,8 +474,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 g.b = -1;
                 if (more) g = load_seg(p, x, first, end, tpi, kTT);
                 if (k >= kSegs)
-                    ok = __all_sync(kAllLanes, mbar_wait(&bar->seg_empty[k % kSegs], (k / kSegs - 1) & 1, status,
-                                                         DCP_ERR_TIMEOUT, abort));
+                    ok = __all_sync(kAllLanes, wait_short(&bar->seg_empty[k % kSegs], (k / kSegs - 1) & 1, abort));
                 if (!ok) break;
                 if (lane == 0) {
                     int4* at = bar->seg[k % kSegs];

@@ -44,38 +44,42 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p, c
 #pragma unroll
         for (int v = 0; v < NV; ++v) acc[k][v] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int c = c0; c <= c1; ++c) {
-        if (c != c0 && empty(c)) continue;
-        const int64_t at = (int64_t)(c == c0 ? s0 : 2 * c) * rows + row0;
+    // two parts at a time, all their rows in flight
+    for (int c = c0; c <= c1; c += 2) {
+        float w[2][kMergeRows];
+        float4 o[2][kMergeRows][NV];
 #pragma unroll
-        for (int k = 0; k < kMergeRows; ++k)
-            if (row0 + k < nrows) mx[k] = fmaxf(mx[k], ws.lse[at + k]);
-    }
-    for (int c = c0; c <= c1; ++c) {
-        if (c != c0 && empty(c)) continue;
-        const int64_t at = (int64_t)(c == c0 ? s0 : 2 * c) * rows + row0;
-        float w[kMergeRows];
-        float4 o[kMergeRows][NV];
+        for (int e = 0; e < 2; ++e) {
+            const bool there = c + e <= c1 && (c + e == c0 || !empty(c + e));
+            const int64_t at = (int64_t)(c + e == c0 ? s0 : 2 * (c + e)) * rows + row0;
 #pragma unroll
-        for (int k = 0; k < kMergeRows; ++k) {
-            w[k] = row0 + k < nrows ? ws.lse[at + k] : -INFINITY;
+            for (int k = 0; k < kMergeRows; ++k) {
+                const bool ok = there && row0 + k < nrows;
+                w[e][k] = ok ? ws.lse[at + k] : -INFINITY;
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (row0 + k < nrows && 4 * lane + 128 * v < D)
-                    o[k][v] = *reinterpret_cast<const float4*>(ws.o + (at + k) * D + 4 * lane + 128 * v);
-                else o[k][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int v = 0; v < NV; ++v)
+                    if (ok && 4 * lane + 128 * v < D)
+                        o[e][k][v] = *reinterpret_cast<const float4*>(ws.o + (at + k) * D + 4 * lane + 128 * v);
+                    else o[e][k][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
 #pragma unroll
         for (int k = 0; k < kMergeRows; ++k) {
-            if (w[k] == -INFINITY) continue;
-            w[k] = exp2f(w[k] - mx[k]);  // mx is finite, infinite or NaN with w: as the formula has it
-            sum[k] += w[k];
+            // mx becomes finite, infinite or NaN with the parts: as the formula has it
+            const float m = fmaxf(mx[k], fmaxf(w[0][k], w[1][k]));
+            const float old = mx[k] == -INFINITY ? 0.f : exp2f(mx[k] - m);
+            const float w0 = w[0][k] == -INFINITY ? 0.f : exp2f(w[0][k] - m);
+            const float w1 = w[1][k] == -INFINITY ? 0.f : exp2f(w[1][k] - m);
+            mx[k] = m;
+            sum[k] = fmaf(sum[k], old, w0 + w1);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                acc[k][v].x = fmaf(w[k], o[k][v].x, acc[k][v].x);
-                acc[k][v].y = fmaf(w[k], o[k][v].y, acc[k][v].y);
-                acc[k][v].z = fmaf(w[k], o[k][v].z, acc[k][v].z);
-                acc[k][v].w = fmaf(w[k], o[k][v].w, acc[k][v].w);
+                float4& x = acc[k][v];
+                const float4 &x0 = o[0][k][v], &x1 = o[1][k][v];
+                x.x = fmaf(w1, x1.x, fmaf(w0, x0.x, x.x * old));
+                x.y = fmaf(w1, x1.y, fmaf(w0, x0.y, x.y * old));
+                x.z = fmaf(w1, x1.z, fmaf(w0, x0.z, x.z * old));
+                x.w = fmaf(w1, x1.w, fmaf(w0, x0.w, x.w * old));
             }
         }
     }
@@ -102,12 +106,12 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p, c
 }
 
 template <typename T>
-void launch_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int rows, dim3 grid, cudaStream_t stream) {
-    switch (p.D) {
-        case 64: chunk_merge_kernel<T, 64><<<grid, 256, 0, stream>>>(p, ws, tpi, rows); break;
-        case 128: chunk_merge_kernel<T, 128><<<grid, 256, 0, stream>>>(p, ws, tpi, rows); break;
-        default: chunk_merge_kernel<T, 256><<<grid, 256, 0, stream>>>(p, ws, tpi, rows); break;
-    }
+cudaError_t launch_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int rows, dim3 grid,
+                         cudaStream_t stream) {
+    const void* k = p.D == 64 ? (const void*)chunk_merge_kernel<T, 64>
+                              : p.D == 128 ? (const void*)chunk_merge_kernel<T, 128> : (const void*)chunk_merge_kernel<T, 256>;
+    void* args[] = {const_cast<ChunkParams*>(&p), const_cast<ChunkPartials*>(&ws), &tpi, &rows};
+    return cudaLaunchKernel(k, grid, dim3(256), args, 0, stream);
 }
 
 constexpr size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -131,9 +135,8 @@ cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, in
     const int64_t cap = ((int64_t)p.max_seq_len + p.N - 1) / p.N;
     if ((cap + tt - 1) / tt < 2 * kMinPart) return cudaSuccess;
     const dim3 grid(ctas, (tpi * p.gq + 8 * kMergeRows - 1) / (8 * kMergeRows));
-    if (dtype == DCP_F16) launch_merge<__half>(p, ws, tpi, rows, grid, stream);
-    else launch_merge<__nv_bfloat16>(p, ws, tpi, rows, grid, stream);
-    return cudaGetLastError();
+    return dtype == DCP_F16 ? launch_merge<__half>(p, ws, tpi, rows, grid, stream)
+                            : launch_merge<__nv_bfloat16>(p, ws, tpi, rows, grid, stream);
 }
 
 }  // namespace dcp

@@ -215,6 +215,44 @@ __device__ __forceinline__ void mma_ts_warp(uint32_t d, uint32_t a_tmem, uint64_
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
         : "memory");
 }
+// Four products in a row, their operands A_STEP and B_STEP apart (in the descriptors'
+// 16-byte units, or TMEM columns).  The descriptors are put together here, from
+// their low words: held across a loop, the 64-bit descriptors of every step took
+// more registers than the issuing warp has.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_ss4_warp(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                             uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p, t, e;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+        " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %6, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n"
+        " add.u32 x, %1, %7;\n add.u32 y, %3, %8;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
+        " add.u32 x, x, %7;\n add.u32 y, y, %8;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
+        " add.u32 x, x, %7;\n add.u32 y, y, %8;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum), "n"(A_STEP), "n"(B_STEP)
+        : "memory");
+}
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_ts4_warp(uint32_t d, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                             uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p, t, e;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+        " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " mov.b64 b, {%2, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
+        " add.u32 x, %1, %6;\n add.u32 y, %2, %7;\n mov.b64 b, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+        " add.u32 x, x, %6;\n add.u32 y, y, %7;\n mov.b64 b, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n"
+        " add.u32 x, x, %6;\n add.u32 y, y, %7;\n mov.b64 b, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n}" ::"r"(d),
+        "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum), "n"(A_STEP), "n"(B_STEP)
+        : "memory");
+}
 __device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
     asm volatile(
         "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
