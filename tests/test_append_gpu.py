@@ -136,6 +136,11 @@ def test_append_many_rows_per_group():
     run(bt, 128, False)
 
 
+@pytest.mark.parametrize("D", [64, 128, 16])
+def test_append_finds_the_owner_among_many_requests(D):
+    run(Batch([(b % 4, 3 + b % 4 + 13 * b % 97) for b in range(1100)], 3, 4, 2, D, 16, torch.bfloat16, 3, seed=D), D, False)
+
+
 def test_append_in_place_strided_pool_and_stream():
     bt = Batch([(5, 9), (33, 70)], 2, 4, 2, 128, 16, torch.bfloat16, 2, seed=4, strided=True)
     s = torch.cuda.Stream()

@@ -90,6 +90,20 @@ def test_long_requests_are_split_and_joined(D, page):
     run(bt, causal=False, base="2")
 
 
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16), (256, 32)])
+def test_full_and_partial_row_blocks_share_the_ranges(D, page):
+    # every request ends in a block of a few new tokens: their tiles weigh less in the split
+    run(Batch([(276, 1500 + 37 * b) for b in range(10)], 2, 4, 4, D, page, HF, 2, seed=D))
+    run(Batch([(40, 900 + 100 * b) for b in range(6)], 2, 16, 2, D, page, BF, 0, seed=D + 1), causal=False)
+
+
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 8), (256, 8)])
+def test_more_requests_and_ranks_than_threads_of_a_block(D, page):
+    lens = [(b % 4, 3 + b % 4 + 13 * b % 97) for b in range(450)]
+    lens[200] = (33, 6000)
+    run(Batch(lens, 3, 4, 2, D, page, BF, 1, seed=D))
+
+
 @pytest.mark.parametrize("D,page", [(128, 64), (64, 16), (256, 32), (128, 1)])
 def test_scores_that_keep_rising(D, page):
     # keys ordered so that the running maximum moves with every tile, by up to hundreds of powers of two

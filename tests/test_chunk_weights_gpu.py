@@ -89,6 +89,14 @@ def test_weights_match_the_definition(lens, N, H, Hkv, D, page, dtype, pad, stri
         assert abs(acc.sum().item() - lens[0][0] * H) < 1e-3 * H
 
 
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 8), (256, 8)])
+def test_more_requests_and_ranks_than_threads_of_a_block(D, page):
+    lens = [(b % 4, 3 + b % 4 + 13 * b % 97) for b in range(450)]
+    lens[200] = (33, 6000)
+    bt = Batch(lens, 3, 4, 2, D, page, BF, 1, seed=D)
+    run(bt, merged_lse(bt))
+
+
 @pytest.mark.parametrize("D,page", [(128, 16), (64, 64), (256, 16)])
 def test_rows_without_a_finite_log_sum_exp_add_nothing(D, page):
     bt = Batch([(9, 400), (200, 260)], 2, 8, 2, D, page, BF, 0, seed=21)
