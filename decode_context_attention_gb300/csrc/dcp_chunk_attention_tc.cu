@@ -29,14 +29,17 @@
 // Warp 11 hands out the parts of the CTA's range, computed ahead of everyone.
 // Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
 // Measured (bf16, 32 query heads over 4, D = 128): 4096 new tokens over 32768, 4
-// ranks: 1475 us, 1.40 PFLOP/s (0.71 of cuBLAS's burst, 0.81 of its rate under the
-// power cap); 2048 over 8192: 370 us, the tensor core busy 58% of the cycles, the
-// multi-function unit 29%, the issue slots 38%: a stage's chain (scores to
-// registers, exponentials, P's store, two products) is longer than the other
-// stage's products, and there is no third stage in 512 columns.
-// Four new tokens of 32 requests of 16384: 213 us, 5.05 TB/s (161 us at the copy
+// ranks: 1403 us, 1.47 PFLOP/s (0.75 of cuBLAS's burst, 0.85 of its rate under the
+// power cap); 2048 over 8192: 353 us.  The tensor core is busy under two thirds of
+// the cycles: a stage's chain (scores to registers, exponentials, P's store, two
+// products; 3100 cycles a pair of tiles) is longer than the other stage's
+// products, and there is no third stage in 512 columns.
+// Four new tokens of 32 requests of 16384: 199 us, 5.4 TB/s (161 us at the copy
 // rate), bound by the ends of items, where the ring runs dry.  D = 64 has as many
-// exponentials for half the products: 2048 over 8192 316 us.
+// exponentials for half the products: 2048 over 8192 292 us.
+// What the loops of all warps run has to fit the instruction cache, and the issuing
+// warps have 56 registers: long waits are out of line and descriptors are made where
+// they are used (chunk 373 -> 355 us, drafts 211 -> 199 us).
 #include <cuda.h>
 #include <math.h>
 #include <stdlib.h>
@@ -765,8 +768,8 @@ size_t chunk_attention_tc_workspace(int D) {
 bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
     // the maximum of the scaled scores is that of the scores for a positive scale
     // only; boxes hold whole 8-row swizzle atoms.  Where both kernels can run this
-    // one is faster at every size measured: 213 against 326 us (drafts), 168 against
-    // 358 us (mixed, D = 64), 370 against 1891 and 1475 against 8085 us (chunks)
+    // one is faster at every size measured: 199 against 326 us (drafts), 144 against
+    // 358 us (mixed, D = 64), 353 against 1891 and 1403 against 8085 us (chunks)
     if ((p.D != 64 && p.D != 128) || !(p.sm_scale > 0.f) || p.page_shift < 3) return false;
     const EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
