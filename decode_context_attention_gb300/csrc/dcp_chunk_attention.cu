@@ -16,7 +16,7 @@
 // The kernel runs on mma.sync (m16n8k16): 64 rows a CTA, 16 a warp, tiles of 64
 // tokens staged in shared memory by cp.async, two or three CTAs an SM covering one
 // another's copies.  It is bound by the warp-level products' rate: 255 TFLOP/s at
-// D = 128 (4096 new tokens over 32768), 218 at D = 256 (1024 over 4096, 552 us).
+// D = 128 (4096 new tokens over 32768), 224 at D = 256 (1024 over 4096, 536 us).
 // The tcgen05 kernel takes over for D = 64 and 128, positive scales and pages of 8
 // tokens and more.
 #include "dcp_chunk.cuh"

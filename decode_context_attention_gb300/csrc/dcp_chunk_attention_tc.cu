@@ -48,7 +48,7 @@
 
 #include "dcp_chunk.cuh"
 #include "dcp_mma.cuh"
-#include "dcp_sm100.cuh"
+#include "dcp_sm100_warp.cuh"
 
 namespace dcp {
 

@@ -23,7 +23,7 @@
 // log-sum-exps of the even and the odd query tiles' rows.
 // Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
 // Measured (D = 128, bf16, 32 query heads over 4): one new token of 64 requests of
-// 8192 tokens, 4 ranks: 98 us, 5.7 TB/s, bound by the keys' bytes (83 us at the copy
+// 8192 tokens, 4 ranks: 96 us, 5.8 TB/s, bound by the keys' bytes (83 us at the copy
 // rate); 2048 new tokens over 16384, 2 ranks: 275 us, 0.94 PFLOP/s: the two tiles'
 // 2 x 128 exponentials a row of threads take the multi-function unit as long as
 // their products take the tensor core, each is busy half the time, and 256 blocks
@@ -35,7 +35,7 @@
 #include <type_traits>
 
 #include "dcp_chunk.cuh"
-#include "dcp_sm100.cuh"
+#include "dcp_sm100_warp.cuh"
 
 namespace dcp {
 
@@ -375,10 +375,10 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                     const uint64_t da = smem_desc(ka + (2 * kb + u) * kTileBytes, 16, 1024, kSwizzle128B);
                     const uint64_t db = smem_desc(qa + s * kTileBytes, 16, 1024, kSwizzle128B);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kChunkB + (kk & 3) * 32) >> 4);
-                        mma_ss_warp(tm + 256 * u + kM * buf, da + off, db + off, idesc, kk > 0 ? 1u : 0u);
-                    }
+                    for (int c = 0; c < D / 64; ++c)  // 64 elements of D a time: 16 are 32 bytes of a swizzled row
+                        mma_ss4_warp<2, 2>(tm + 256 * u + kM * buf, (uint32_t)da + c * (kChunkB >> 4),
+                                           (uint32_t)(da >> 32), (uint32_t)db + c * (kChunkB >> 4),
+                                           (uint32_t)(db >> 32), idesc, c > 0);
                     mma_commit_warp(&bar->s_full[u][buf]);
                     issued_any = true;
                 }
@@ -558,7 +558,7 @@ cudaError_t launch_weights_tc(const ChunkParams& p, const CUtensorMap (&maps)[2]
 
 bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
     // boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one is
-    // faster at every size measured: 98 against 147 us (64 single tokens, 8192),
+    // faster at every size measured: 96 against 147 us (64 single tokens, 8192),
     // 74 against 178 us (ragged, 12 heads a group), 275 against 1412 us (2048 new)
     if ((p.D != 64 && p.D != 128) || p.page_shift < 3) return false;
     const EncodeTiledFn enc = tensor_map_encoder();
