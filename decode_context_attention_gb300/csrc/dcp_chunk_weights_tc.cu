@@ -458,7 +458,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                     const int cols = min(tj, g.q.n - j) * p.gq;
                     // every row has a finite log-sum-exp and sees every token of the tile
                     const bool plain = *(volatile int*)&bar->plain[buf] != 0 && j >= all;
-                    const int first = (from - j) * p.gq;  // the first column that sees this token
+                    // the first column that sees this token, 0 when all do: `from` falls to minus the
+                    // request's length, which times the group passes 32 bits
+                    const int first = max(from - j, 0) * p.gq;
                     unsigned long long acc[2] = {0ull, 0ull};
                     float part[2] = {0.f, 0.f};
                     for (int c0 = 0; c0 < cols; c0 += 32) {
