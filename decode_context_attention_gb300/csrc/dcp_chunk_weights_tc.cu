@@ -508,10 +508,13 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->i_empty[buf]);
             }
-            // the sums of an item's even and odd tiles, in a fixed order.  The writer is
-            // at most three items ahead of the other warps: the score buffers hold it
-            // back there.
+            // the sums of an item's even and odd tiles, in a fixed order.  A tile without
+            // tokens has none to exchange, and its warps wait for no scores: they would not
+            // be held back.  In the others the writer is at most two exchanges ahead of the
+            // reader: of the items after the reader's, each has a tile of the reader's score
+            // buffer, the first of them fills it, and the next item's products stop there.
             if (g.nq > 1) {
+                if (!active) continue;
                 if (lead) {
                     if (ok && tok < g.held) __stcg(a, before + total);
                     __threadfence();
