@@ -555,7 +555,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         m3 = max3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
                     }
                     const float vt = fmaxf(max3(m0, m1, m2), m3);
-                    const bool grow = vt * qscale > mref + kGrow;
+                    // rows of no query (of the next request, of the padding, or of none at all) have
+                    // no say in how the warp's other rows are rounded; a query's row that sees
+                    // nothing (lim 0) has a maximum of -infinity anyway
+                    const bool grow = lim > 0 && vt * qscale > mref + kGrow;
                     if (__any_sync(kAllLanes, grow)) {
                         float alpha = 1.f;
                         if (grow) {

@@ -400,8 +400,9 @@ dcp_status_t dcp_decode_attention_mla(int dtype, int N, int B, int H, int Dk, in
  *   query_start [B + 1] int32 (device)  request b owns token rows t in
  *               [query_start[b], query_start[b + 1]) of the [T, ...] operands;
  *               query_start[0] = 0, non-decreasing; a request may own none;
- *               rows t >= query_start[B] belong to no request and are neither
- *               read nor written (padding of a fixed-size batch).
+ *               rows t >= query_start[B] belong to no request (padding of a
+ *               fixed-size batch): they are not written, and what they hold
+ *               changes no bit of a result, but they have to be readable memory.
  *   seq_lens [B] int32 (device)  tokens of each request in the caches WITH its
  *               new tokens: row j of request b is the token of global index
  *               g = seq_lens[b] - Q_b + j, Q_b = query_start[b+1] - query_start[b].
