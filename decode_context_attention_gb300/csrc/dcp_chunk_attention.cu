@@ -19,6 +19,8 @@
 // D = 128 (4096 new tokens over 32768), 224 at D = 256 (1024 over 4096, 536 us).
 // The tcgen05 kernel takes over for D = 64 and 128, positive scales and pages of 8
 // tokens and more.
+#include <type_traits>
+
 #include "dcp_chunk.cuh"
 #include "dcp_mma.cuh"
 
@@ -34,6 +36,14 @@ struct MmaShape {
     static constexpr int kPitch = D * 2 + 16;  // bytes of a staged row: 16 more keep ldmatrix free of bank conflicts
     static constexpr int kSmem = (kRows + 2 * kTile) * kPitch;
 };
+
+// A row's weights are 2^(s - m + kBias): fp16's smallest normal is 2^-14, so beside a
+// largest weight of 1 the weights below it lose bits and those below 2^-25 are lost,
+// while the row sum keeps them.  With 2^15 for the largest the same holds from 2^-29
+// and 2^-40 of it; the factor cancels in O, and m is kept less kBias, so that the
+// log-sum-exp is m + log2 l as without it.
+template <typename T>
+constexpr float kBias = std::is_same<T, __half>::value ? 15.f : 0.f;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const ChunkParams p, const ChunkPartials ws,
@@ -157,7 +167,7 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
                     }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[i], mx);
+                const float mn = fmaxf(m[i], mx - kBias<T>);
                 const float base = mn == -INFINITY ? 0.f : mn;
                 const float alpha = exp2_fast(m[i] - base);
                 m[i] = mn;
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
             const int row = warp * 16 + (lane >> 2) + 8 * i;
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            // l is 0 only where the row sees nothing (the largest term is 1); NaN stays NaN
+            // l is 0 only where the row sees nothing (the largest term is 2^kBias); NaN stays NaN
             const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
             const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
             if (row >= nrows) continue;

@@ -24,8 +24,8 @@
 // the rows that do see them at the end).
 // The reference maximum moves only when a row's maximum grows by more than 2^8,
 // so O is rarely rescaled; P then reaches 2^8, which a 16-bit type holds and
-// fp32 sums do too.  P is rounded to the payload type, half a step per term;
-// the row sums use it unrounded.
+// fp32 sums do too.  P is rounded to the payload type, half a step per term (fp16:
+// and at least 2^-32 of the row's largest term); the row sums use it unrounded.
 // Warp 11 hands out the parts of the CTA's range, computed ahead of everyone.
 // Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
 // Measured (bf16, 32 query heads over 4, D = 128): 4096 new tokens over 32768, 4
@@ -61,7 +61,22 @@ constexpr int kM = 128;         // rows of a stage
 constexpr int kThreadsTc = 384;
 constexpr int kChunkB = 128 * 128;  // 64 columns of 128 rows
 constexpr int kMisc = 2048;
-constexpr float kGrow = 8.f;
+// A row's weights are 2^(s - m + kBias), m the reference maximum, which moves when the
+// row's maximum has passed it by more than kGrow powers of two.  fp16's smallest normal
+// is 2^-14: beside a largest weight of 1 the weights of a long tail lose bits from
+// there on and are gone below 2^-25, while the row sum keeps them.  The bias uses the
+// room above, up to 2^15 with the lag, and cancels in O; the reference is kept less
+// the bias, so that a log-sum-exp is the reference plus log2 of the sum as without it.
+// A smaller lag leaves more room (kGrow 4: bias 11) but rescales O more often: 355
+// against 398 us (2048 over 8192, fp16), 1410 against 1561 (4096 over 32768).
+template <typename T>
+struct PRange {
+    static constexpr float kGrow = 8.f, kBias = 0.f;
+};
+template <>
+struct PRange<__half> {
+    static constexpr float kGrow = 8.f, kBias = 7.f;
+};
 // 2^(s qscale - m) takes one fused step, exact but for one rounding; m itself is
 // rounded, which moves a row's weights all alike and its log-sum-exp back, and
 // is harmless while m's rounding error (2^-24 |m|) is small.  Beyond this the
@@ -502,6 +517,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int mtok = m / p.gq, hh = m - mtok * p.gq;  // new token of the row block, head of the group
         const uint32_t tS = tmem + kM * u + lanes, tO = tmem + kColO + D * u + lanes;
         const float qscale = p.sm_scale * kLog2e;
+        constexpr float kGrow = PRange<T>::kGrow, kBias = PRange<T>::kBias;
         int sn = 0, vn = 0, xn = 0;  // phases of s_full and pv_done, exchanges
         bool ok = true;
         auto wait = [&](uint64_t* b, int parity) -> bool {
@@ -524,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 lim0 = g.lim0;
                 live = __any_sync(kAllLanes, valid);
             }
-            float mref = -INFINITY, vref = 0.f;  // the reference maximum, scaled and as a score
+            float mref = -INFINITY, vref = 0.f;  // the reference: scaled less kBias, and as a score
             bool far = false;                    // a row of the warp has one beyond kFar
             unsigned long long l2[2] = {0ull, 0ull};
             for (int i = 0; i < mine; ++i) {
@@ -558,13 +574,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     // rows of no query (of the next request, of the padding, or of none at all) have
                     // no say in how the warp's other rows are rounded; a query's row that sees
                     // nothing (lim 0) has a maximum of -infinity anyway
-                    const bool grow = lim > 0 && vt * qscale > mref + kGrow;
+                    const bool grow = lim > 0 && vt * qscale > mref + (kGrow + kBias);
                     if (__any_sync(kAllLanes, grow)) {
                         float alpha = 1.f;
                         if (grow) {
                             alpha = mref == -INFINITY ? 0.f : exp2_fast((vref - vt) * qscale);
                             vref = vt;
-                            mref = vt * qscale;
+                            mref = vt * qscale - kBias;
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const float2 l = unpack2(l2[e]);
@@ -587,7 +603,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             }
                         }
                     }
-                    const float off = mref == -INFINITY || far ? 0.f : -mref;
+                    const float off = far ? kBias : mref == -INFINITY ? 0.f : -mref;
                     if (far) {
                         const float sub = mref == -INFINITY ? 0.f : vref;
 #pragma unroll
@@ -639,7 +655,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const int row = (pair ? u * rblk : 0) + m;  // row of the item
             const bool valid = m < rblk && row < g.nrows;
             const int tok = (pair ? u * tj : 0) + mtok;
-            // l is 0 only where the row sees nothing (a visible row's largest term is at least 2^-8); NaN stays NaN
+            // l is 0 only where the row sees nothing (a visible row's largest term is at least 2^kBias); NaN stays NaN
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : mref + log2f(l);
             const bool writes = ok && live && (pair || u == 0);

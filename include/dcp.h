@@ -480,8 +480,9 @@ dcp_status_t dcp_qk_norm_rope_append(int dtype, int N, int B, int T, int H, int 
  *   q [T, H, D] strides (q_st, q_sh); o [N, T, H, D]; lse [N, T, H] fp32
  * dtype DCP_F16 or DCP_BF16; D in {64, 128, 256}; 1 <= H / Hkv <= 64.  Page
  * indices outside [0, num_pages) read as zero rows.  Probabilities enter the
- * value product rounded to the payload type; scores, sums and outputs
- * accumulate in fp32.  `workspace` (device, 16-byte aligned) of at least
+ * value product rounded to the payload type (off by half a step of theirs; for
+ * DCP_F16 by up to 2^-32 of the row's largest probability where that is more);
+ * scores, sums and outputs accumulate in fp32.  `workspace` (device, 16-byte aligned) of at least
  * dcp_extend_attention_workspace_size(...) bytes for the current device; calls
  * that may run at the same time need workspaces of their own, and so do graphs
  * that may be replayed at the same time.  Waits in the tensor-core kernel are
