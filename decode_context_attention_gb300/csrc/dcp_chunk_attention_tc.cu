@@ -27,7 +27,8 @@
 // fp32 sums do too.  P is rounded to the payload type, half a step per term (fp16:
 // and at least 2^-32 of the row's largest term); the row sums use it unrounded.
 // Warp 11 hands out the parts of the CTA's range, computed ahead of everyone.
-// Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
+// Waits are bounded (1 s, or 1 s in which no load is issued): one that runs out records
+// DCP_ERR_TIMEOUT.
 // Measured (bf16, 32 query heads over 4, D = 128): 4096 new tokens over 32768, 4
 // ranks: 1403 us, 1.47 PFLOP/s (0.75 of cuBLAS's burst, 0.85 of its rate under the
 // power cap); 2048 over 8192: 353 us.  The tensor core is busy under two thirds of
@@ -106,8 +107,7 @@ struct TcBars {
     uint64_t x_full, x_done;  // an item of one row block: stage 1's sums written, its O read
     uint64_t mma_done;
     uint32_t tmem_base;
-    int abort;
-    int issued;               // ring positions whose loads are under way
+    int state[2];             // abort; ring positions whose loads are under way
     unsigned poison[kPoison][12];  // 3 masked tiles of 128 tokens
     float xm[kM], xl[kM];
     alignas(16) ChunkPos range[2];
@@ -162,12 +162,40 @@ __device__ __forceinline__ void exp_store(const uint32_t (&v)[128], uint32_t tP,
     tmem_st16(tP, w);
 }
 
-// mbar_wait with its long path out of line: the loops around it fit the instruction cache.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return mbar_wait(bar, parity, &g_chunk_status, DCP_ERR_TIMEOUT, abort);
+// Waits for a part, not for a tile, last as long as the cache is long (a second at some
+// 85 million tokens of a part): their limit counts the time in which no load is issued.
+struct Moving {
+    int seen = -1;
+    uint64_t since = 0;
+    __device__ bool stalled(int issued) {
+        const uint64_t now = global_timer_ns();
+        if (issued != seen) {
+            seen = issued;
+            since = now;
+        }
+        return now - since > kWaitLimitNs;
+    }
+};
+// state: TcBars::state.  (Out of line it costs the mixed batch 2%.)
+__device__ __forceinline__ bool wait_part(uint64_t* bar, uint32_t parity, volatile int* state) {
+    if (mbar_try_wait(bar, parity)) return true;
+    Moving m;
+    while (!mbar_try_wait(bar, parity)) {
+        if (state[0]) return false;
+        if (m.stalled(state[1])) {
+            atomicCAS(&g_chunk_status, 0, DCP_ERR_TIMEOUT);
+            state[0] = 1;
+            return false;
+        }
+    }
+    return true;
 }
-__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
+// mbar_wait with its long path out of line: the loops around it fit the instruction cache.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* state) {
+    return mbar_wait(bar, parity, &g_chunk_status, DCP_ERR_TIMEOUT, state);
+}
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volatile int* state) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, state);
 }
 
 template <typename T, int D>
@@ -208,8 +236,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         mbar_init(&bar->x_full, 4);
         mbar_init(&bar->x_done, 4);
         mbar_init(&bar->mma_done, 1);
-        bar->abort = 0;
-        bar->issued = 0;
+        bar->state[0] = bar->state[1] = 0;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -226,7 +253,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem_base;
-    volatile int* abort = &bar->abort;
+    volatile int* abort = bar->state;
     int* status = &g_chunk_status;
     // the k-th part of this CTA's range, from warp 11; false behind the last one
     auto get_seg = [&](int k, ChunkSeg* g) -> bool {
@@ -285,7 +312,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (go) {
                             mbar_arrive_expect_tx(&bar->full[s], (uint32_t)(NCH * nseg * pb * 128));
                             __threadfence_block();
-                            *(volatile int*)&bar->issued = pos + 1;
+                            abort[1] = pos + 1;
                         }
                     }
                     if (!__shfl_sync(kAllLanes, go, 0)) return false;
@@ -418,7 +445,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             int base = 0;
             bool ok = true;
             ChunkSeg g;
-            for (int seg = 0; ok && get_seg(seg, &g); ++seg) {
+            // this warp passes over parts without masked tiles, ahead of everyone: the next
+            // ones come when the first of them is done
+            auto next_seg = [&](int k) -> bool {
+                return __all_sync(kAllLanes, wait_part(&bar->seg_full[k % kSegs], (k / kSegs) & 1, abort)) &&
+                       get_seg(k, &g);
+            };
+            for (int seg = 0; ok && next_seg(seg); ++seg) {
                 release_seg(seg);
                 const int n = g.t1 - g.t0;
                 const bool pair = g.nrows > rblk;
@@ -432,10 +465,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     // this warp does not wait for every tile, so the slot's barrier may still
                     // be phases behind: its parity means something once the load is under
                     // way (and the slot cannot pass on before this tile is clean)
-                    const uint64_t t_start = global_timer_ns();
-                    while (*(volatile int*)&bar->issued <= j && !*abort) {
+                    Moving m;
+                    for (int got; (got = abort[1]) <= j && !*abort;) {
                         __nanosleep(200);
-                        if (global_timer_ns() - t_start > kWaitLimitNs) {
+                        if (m.stalled(got)) {
                             atomicCAS(status, 0, DCP_ERR_TIMEOUT);
                             *abort = 1;
                         }
@@ -492,7 +525,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 g.b = -1;
                 if (more) g = load_seg(p, x, first, end, tpi, kTT);
                 if (k >= kSegs)
-                    ok = __all_sync(kAllLanes, wait_short(&bar->seg_empty[k % kSegs], (k / kSegs - 1) & 1, abort));
+                    ok = __all_sync(kAllLanes, wait_part(&bar->seg_empty[k % kSegs], (k / kSegs - 1) & 1, abort));
                 if (!ok) break;
                 if (lane == 0) {
                     int4* at = bar->seg[k % kSegs];
