@@ -564,6 +564,13 @@ def _word_args(t: torch.Tensor, shape: tuple, name: str):
     return (t.data_ptr(), *t.stride())
 
 
+def _workspace_args(workspace: torch.Tensor):
+    """Pointer and bytes of a caller's workspace, whose memory the kernels take from front to back."""
+    if not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, got strides {workspace.stride()} of shape {tuple(workspace.shape)}")
+    return (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
 def _append_args(q, k, v, q_weight, k_weight, eps, cos_sin, positions, k_pages, v_pages, block_table, query_start,
                  seq_lens, max_seq_len, q_out, interleaved, stream):
     dev = _chunk_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_pages, v_pages, block_table, query_start,
@@ -669,8 +676,7 @@ def _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_se
             with torch.cuda.device(dev):
                 nbytes = size(N, B, T, H, Hkv, D, max_seq_len)
         workspace = _scratch(nbytes, dev, stream)
-    return dev, workspace, (*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                            _stream_on(dev, stream))
+    return dev, workspace, (*args, *_workspace_args(workspace), _stream_on(dev, stream))
 
 
 def prepare_extend_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,

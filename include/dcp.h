@@ -514,8 +514,8 @@ dcp_status_t dcp_extend_attention_paged(int dtype, int N, int B, int T, int H, i
  *     acc[r, b, kh, i] = (i*N + r < seq_lens[b] - Q_b ? acc[r, b, kh, i] : 0)
  *                        + sum over new tokens j that see i (i*N + r <= g) and the
  *                          query heads h of kh of exp(s - lse[t, h])
- * so the new tokens' own entries start from zero.  Rows whose lse is not
- * finite add nothing.  Entries i >= L_r(seq_lens[b]) and requests without new
+ * so the new tokens' own entries start from zero.  Rows whose lse (in base 2)
+ * is not a finite fp32 add nothing.  Entries i >= L_r(seq_lens[b]) and requests without new
  * tokens are left as they are.  Sums are fp32 in a fixed order: equal calls
  * give equal bits.
  *
