@@ -39,7 +39,8 @@ __device__ __forceinline__ unsigned weight_key(float f) {
 }
 
 struct SelectShared {
-    int hist[2][kBins];    // of alternate passes, so that a neighbour may still read the last one
+    // of alternate passes, so that a neighbour may still read the last one; read as int4
+    alignas(16) int hist[2][kBins];
     int part[kSelWarps];
     int found, above;      // the bin of the K-th largest key, and how many keys lie above it
     int counts[2];         // keys of this slice above the K-th largest, and equal to it
