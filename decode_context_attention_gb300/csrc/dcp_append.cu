@@ -26,7 +26,6 @@ constexpr int kAppendCtas = 8;  // per SM: 64 registers a thread, 1024 threads w
 
 // Eight 16-bit elements as four fp32 pairs (two fp32 operations an instruction:
 // with one at a time this kernel was bound by its instructions).
-using Pair = unsigned long long;
 template <typename T>
 __device__ __forceinline__ void widen(const uint4& v, Pair (&x)[4]) {
     x[0] = word_to_pair<T>(v.x);
@@ -39,17 +38,6 @@ __device__ __forceinline__ uint4 narrow(const Pair (&x)[4]) {
     return make_uint4(f32_to_pair(unpack2(x[0]), T()), f32_to_pair(unpack2(x[1]), T()),
                       f32_to_pair(unpack2(x[2]), T()), f32_to_pair(unpack2(x[3]), T()));
 }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // The request that owns row t: the largest b with query_start[b] <= t, -1 when
 // t lies before the first or behind the last.  The group's LPR lanes probe as
 // many places per step.

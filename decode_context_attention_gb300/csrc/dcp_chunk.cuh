@@ -57,8 +57,27 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// sum over i < n of floor((a i + b) / m), for b >= 0, m > 0, by Euclid's steps;
-// 32-bit divisions where the terms fit.
+// Two fp32 operations an instruction, each rounded to nearest, on pairs held in one
+// 64-bit register.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ void add2(Pair& a, Pair b) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b)); }
+
+// sum over i < n of floor((a i + b) / m), for b >= 0, m > 0: whole multiples of m in a
+// and b come out in closed form, and what is left counts the lattice points under a
+// line, which read from the other axis is a sum of the same kind with m and a swapped
+// (the classical reduction, as in Graham, Knuth, Patashnik, "Concrete Mathematics",
+// chapter 3, and in the sum-of-floors routines of algorithm collections).  32-bit
+// divisions where the terms fit.
 __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
     auto div = [](int64_t x, int64_t y) -> int64_t {
         return ((x | y) >> 32) ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);

@@ -116,14 +116,6 @@ struct TcBars {
 };
 static_assert(sizeof(TcBars) <= kMisc, "misc region too small");
 
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ void add2(unsigned long long& a, unsigned long long b) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -149,8 +141,8 @@ __device__ __forceinline__ ChunkSeg read_seg(const int4* at) {
 }
 // P of the 32 scores v[OFF ..], 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
 template <typename T, int OFF>
-__device__ __forceinline__ void exp_store(const uint32_t (&v)[128], uint32_t tP, unsigned long long qs2,
-                                          unsigned long long off2, unsigned long long (&l2)[2]) {
+__device__ __forceinline__ void exp_store(const uint32_t (&v)[128], uint32_t tP, Pair qs2,
+                                          Pair off2, Pair (&l2)[2]) {
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -575,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             float mref = -INFINITY, vref = 0.f;  // the reference: scaled less kBias, and as a score
             bool far = false;                    // a row of the warp has one beyond kFar
-            unsigned long long l2[2] = {0ull, 0ull};
+            Pair l2[2] = {0ull, 0ull};
             for (int i = 0; i < mine; ++i) {
                 if (!(ok = wait(&bar->s_full[u], sn))) break;
                 ++sn;
@@ -642,7 +634,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                         for (int c = 0; c < 128; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) - sub);
                     }
-                    const unsigned long long qs2 = pack2f(qscale, qscale), off2 = pack2f(off, off);
+                    const Pair qs2 = pack2f(qscale, qscale), off2 = pack2f(off, off);
                     exp_store<T, 0>(v, tS, qs2, off2, l2);
                     exp_store<T, 32>(v, tS + 16, qs2, off2, l2);
                     exp_store<T, 64>(v, tS + 32, qs2, off2, l2);

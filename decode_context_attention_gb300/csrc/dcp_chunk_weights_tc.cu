@@ -353,12 +353,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         unsigned used = 0u;  // phase of s_empty by tile and buffer (a barrier's phase before its first counts as done)
         bool ok = true;
         for (; ok && more(); g.next(p, tj), ++it) {
-            int nq, rows, two;
-            {
-                    nq = __shfl_sync(kAllLanes, g.nq, 0);
-                rows = __shfl_sync(kAllLanes, (g.q.n - g.j0) * p.gq, 0);
-                two = __shfl_sync(kAllLanes, g.held - g.tb > kM ? 1 : 0, 0);
-            }
+            const int nq = __shfl_sync(kAllLanes, g.nq, 0);
+            const int rows = __shfl_sync(kAllLanes, (g.q.n - g.j0) * p.gq, 0);
+            const int two = __shfl_sync(kAllLanes, g.held - g.tb > kM ? 1 : 0, 0);
             const int kb = it & 1;
             if (!(ok = wait(&bar->k_full[kb], it >> 1))) break;
             for (int k = 0; k < nq; ++k, ++qc) {
@@ -428,7 +425,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
         const int u = (warp >> 2) & 1, buf = warp >> 3, m = tid & 127;
         const uint32_t tS = tmem + 256 * u + kM * buf + ((uint32_t)(32 * (warp & 3)) << 16);
         const float qscale = p.sm_scale * kLog2e;
-        const unsigned long long qs2 = pack2f(qscale, qscale);
+        const Pair qs2 = pack2f(qscale, qscale);
         const float* nl = lse_s + buf * kM;  // negated log-sum-exps
         auto wait = [&](uint64_t* b, int parity) -> bool {
             return __all_sync(kAllLanes, mbar_wait(b, parity & 1, status, DCP_ERR_TIMEOUT, abort));
@@ -461,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                     // the first column that sees this token, 0 when all do: `from` falls to minus the
                     // request's length, which times the group passes 32 bits
                     const int first = max(from - j, 0) * p.gq;
-                    unsigned long long acc[2] = {0ull, 0ull};
+                    Pair acc[2] = {0ull, 0ull};
                     float part[2] = {0.f, 0.f};
                     for (int c0 = 0; c0 < cols; c0 += 32) {
                         uint32_t v[32];
@@ -474,14 +471,9 @@ __global__ void __launch_bounds__(kThreadsW, 1)
                                 const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + c0 + e);
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
-                                    unsigned long long f;
-                                    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-                                        : "=l"(f)
-                                        : "l"(pack2(v[e + 2 * h], v[e + 2 * h + 1])), "l"(qs2), "l"(h ? l.y : l.x));
-                                    const float2 y = unpack2(f);
-                                    asm("add.rn.f32x2 %0, %0, %1;"
-                                        : "+l"(acc[h])
-                                        : "l"(pack2f(exp2_fast(y.x), exp2_fast(y.y))));
+                                    const float2 y =
+                                        unpack2(fma2(pack2(v[e + 2 * h], v[e + 2 * h + 1]), qs2, h ? l.y : l.x));
+                                    add2(acc[h], pack2f(exp2_fast(y.x), exp2_fast(y.y)));
                                 }
                             }
                         } else {
