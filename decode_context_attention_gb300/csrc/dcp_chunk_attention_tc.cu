@@ -25,7 +25,12 @@
 // The reference maximum moves only when a row's maximum grows by more than 2^8,
 // so O is rarely rescaled; P then reaches 2^8, which a 16-bit type holds and
 // fp32 sums do too.  P is rounded to the payload type, half a step per term (fp16:
-// and at least 2^-32 of the row's largest term); the row sums use it unrounded.
+// and at least 2^-32 of the row's largest term); the row sums use it unrounded.  The
+// output's error against an unrounded P is 2.6e-3 of its norm in bf16, 2.9e-4 in fp16,
+// where its own rounding is 1.7e-3 and 2.1e-4.  A second product with what the rounding
+// leaves, for items of one row block, brings it to 1.6e-4 in bf16 and costs every item:
+// drafts 239 instead of 200 us, 2048 over 8192 386 instead of 352 (the pairs' loop
+// shares the registers and the instruction cache); not taken.
 // Warp 11 hands out the parts of the CTA's range, computed ahead of everyone.
 // Waits are bounded (1 s, or 1 s in which no load is issued): one that runs out records
 // DCP_ERR_TIMEOUT.
