@@ -37,13 +37,12 @@ struct MmaShape {
     static constexpr int kSmem = (kRows + 2 * kTile) * kPitch;
 };
 
-// A row's weights are 2^(s - m + kBias): fp16's smallest normal is 2^-14, so beside a
-// largest weight of 1 the weights below it lose bits and those below 2^-25 are lost,
-// while the row sum keeps them.  With 2^15 for the largest the same holds from 2^-29
-// and 2^-40 of it; the factor cancels in O, and m is kept less kBias, so that the
-// log-sum-exp is m + log2 l as without it.
+// The weights, at most 1, are multiplied by this for the value product: fp16's smallest
+// normal is 2^-14, so weights below it would lose bits and those below 2^-25 be lost,
+// while the row sum keeps them.  Beside 2^15 the same holds from 2^-29 and 2^-40 of the
+// row's largest on.  A power of two, exact; O is divided by it at the end.
 template <typename T>
-constexpr float kBias = std::is_same<T, __half>::value ? 15.f : 0.f;
+constexpr float kWeightUnit = std::is_same<T, __half>::value ? 32768.f : 1.f;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const ChunkParams p, const ChunkPartials ws,
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
                     }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[i], mx - kBias<T>);
+                const float mn = fmaxf(m[i], mx);
                 const float base = mn == -INFINITY ? 0.f : mn;
                 const float alpha = exp2_fast(m[i] - base);
                 m[i] = mn;
@@ -190,11 +189,12 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
             // 16-bit type per term, averages out over the terms)
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk) {
+                constexpr float w = kWeightUnit<T>;
                 unsigned a[4];
-                a[0] = f32_to_pair(make_float2(s[2 * kk][0], s[2 * kk][1]), T());
-                a[1] = f32_to_pair(make_float2(s[2 * kk][2], s[2 * kk][3]), T());
-                a[2] = f32_to_pair(make_float2(s[2 * kk + 1][0], s[2 * kk + 1][1]), T());
-                a[3] = f32_to_pair(make_float2(s[2 * kk + 1][2], s[2 * kk + 1][3]), T());
+                a[0] = f32_to_pair(make_float2(w * s[2 * kk][0], w * s[2 * kk][1]), T());
+                a[1] = f32_to_pair(make_float2(w * s[2 * kk][2], w * s[2 * kk][3]), T());
+                a[2] = f32_to_pair(make_float2(w * s[2 * kk + 1][0], w * s[2 * kk + 1][1]), T());
+                a[3] = f32_to_pair(make_float2(w * s[2 * kk + 1][2], w * s[2 * kk + 1][3]), T());
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
                     unsigned b[4];
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
             const int row = warp * 16 + (lane >> 2) + 8 * i;
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            // l is 0 only where the row sees nothing (the largest term is 2^kBias); NaN stays NaN
-            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            // l is 0 only where the row sees nothing (the largest term is 1); NaN stays NaN
+            const float inv = l[i] == 0.f ? 0.f : 1.f / (l[i] * kWeightUnit<T>);
             const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
             if (row >= nrows) continue;
             const int t = q.start + j0 + row / p.gq, h = hkv * p.gq + row % p.gq;

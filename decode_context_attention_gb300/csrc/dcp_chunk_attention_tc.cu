@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 lim0 = g.lim0;
                 live = __any_sync(kAllLanes, valid);
             }
-            float mref = -INFINITY, vref = 0.f;  // the reference: scaled less kBias, and as a score
+            float mref = -INFINITY, vref = -INFINITY;  // the reference: scaled less kBias, and as a score
             bool far = false;                    // a row of the warp has one beyond kFar
             Pair l2[2] = {0ull, 0ull};
             for (int i = 0; i < mine; ++i) {
@@ -604,7 +604,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     // rows of no query (of the next request, of the padding, or of none at all) have
                     // no say in how the warp's other rows are rounded; a query's row that sees
                     // nothing (lim 0) has a maximum of -infinity anyway
-                    const bool grow = lim > 0 && vt * qscale > mref + (kGrow + kBias);
+                    // (the difference of the scores is exact where they are near each other; that of
+                    // two scaled maxima is off by more than kGrow from 2^26 on)
+                    const bool grow = lim > 0 && (vt - vref) * qscale > kGrow;
                     if (__any_sync(kAllLanes, grow)) {
                         float alpha = 1.f;
                         if (grow) {

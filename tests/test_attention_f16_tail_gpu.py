@@ -55,3 +55,37 @@ def test_a_long_tail_keeps_its_mass(below, D, page, far, n):
     o_tol = o_tol + 2.0 ** (-32 if tc else -40) * bt.v[0].double().abs().sum(0).amax()
     assert_within(o, want, o_tol, "o")
     assert_within(lse, want_lse, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 16), (128, 4), (256, 16)])
+@pytest.mark.parametrize("step", [2.0 ** 20, 2.0 ** 26, 2.0 ** 27, 2.0 ** 28, 2.0 ** 30])
+@pytest.mark.parametrize("n", [1, 40])
+def test_scores_beyond_what_32_bits_resolve(D, page, step, n):
+    """Scores around `step` differ by a few of their own units in the last place, which are many powers of two of
+    weight each: whatever they round to, a row's output is a mean of the values it sees."""
+    L = 1500
+    bt = Batch([(n, L)], 1, 2, 1, D, page, torch.float16, seed=7)
+    bt.scale = 1.0
+    # 2^a times (2^b + i 2^(b - 10)): rising by an fp16 step of the keys from tile to tile; the queries' second
+    # element adds less than that
+    a, b = (15, round(math.log2(step)) - 15) if step > 2.0 ** 24 else (10, round(math.log2(step)) - 10)
+    i = torch.arange(L, device=DEV)
+    bt.q.zero_()
+    bt.q[..., 0] = 2.0 ** a
+    bt.q[..., 1] = 2.0 ** (a - 11)
+    bt.k[0].zero_()
+    bt.k[0][:, 0, 0] = (2.0 ** b + (i // 300) * 2.0 ** (b - 10)).to(torch.float16)
+    bt.k[0][:, 0, 1] = ((i // 100) % 3 * 2.0 ** (b - 9)).to(torch.float16)
+    bt.v[0] = (1 + torch.rand(bt.v[0].shape, generator=bt.g, device=DEV)).to(torch.float16)
+    bt.fill()
+    for sign in (1.0, -1.0):
+        bt.q[..., :2] = bt.q[..., :2].abs() * sign
+        o = torch.empty((1, bt.T, 2, D), dtype=torch.float16, device=DEV)
+        lse = torch.empty((1, bt.T, 2), device=DEV)
+        binding.extend_attention_paged(bt.q, bt.k_pages, bt.v_pages, bt.block_table, bt.query_start, bt.seq_lens,
+                                       bt.max_len, o, lse, bt.scale)
+        torch.cuda.synchronize()
+        assert binding.device_status() == 0
+        assert bool(lse.isfinite().all())
+        # P and o are rounded to fp16 once each (2^-11), the values lie in [1, 2]
+        assert bool((o >= 1 - 2.0 ** -9).all()) and bool((o <= 2 + 2.0 ** -8).all())
