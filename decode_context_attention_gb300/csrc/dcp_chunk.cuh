@@ -143,7 +143,10 @@ __device__ __forceinline__ ChunkPos next_item(const ChunkParams& p, const ChunkP
 
 constexpr int kPairTile = 4, kBlockTile = 3;  // work of a tile of two row blocks, and of one
 constexpr int kItemCost = 13;                 // fixed part of an item's work (about 4.8 us against 1.5 us a pair's tile)
-// A mixed batch of 17 requests: 144 us; with 4, 3, 9: 146, with 4, 3, 18: 165, with 2, 1, 5: 161
+// Chosen on a mixed batch of 17 requests at D = 64: 145 us; with 4, 3, 9: 147, with 4, 3,
+// 18: 160, with 2, 1, 5: 165.  At D = 128, where a tile costs more, 23 requests with 8
+// heads a group take 413, with 18 386; 17 with a head a group 222 and 221; 5 requests
+// 49.9, with 9 47.1 and with 18 51.4: no setting is best for all
 constexpr int kMinPart = 4;   // a cut leaves at least this many tiles on both sides
 
 // The work of one KV head of a (request, rank), by blocks of new tokens.

@@ -26,8 +26,8 @@
 // so O is rarely rescaled; P then reaches 2^8, which a 16-bit type holds and
 // fp32 sums do too.  P is rounded to the payload type, half a step per term (fp16:
 // and at least 2^-32 of the row's largest term); the row sums use it unrounded.  The
-// output's error against an unrounded P is 2.6e-3 of its norm in bf16, 2.9e-4 in fp16,
-// where its own rounding is 1.7e-3 and 2.1e-4.  A second product with what the rounding
+// output differs from that of an unrounded P by 2.6e-3 of its norm in bf16 and 2.9e-4
+// in fp16 (from 64 bits by 2.3e-3 and 2.7e-4; its own rounding is 1.7e-3 and 2.1e-4).  A second product with what the rounding
 // leaves, for items of one row block, brings it to 1.6e-4 in bf16 and costs every item:
 // drafts 239 instead of 200 us, 2048 over 8192 386 instead of 352 (the pairs' loop
 // shares the registers and the instruction cache); not taken.
@@ -35,14 +35,14 @@
 // Waits are bounded (1 s, or 1 s in which no load is issued): one that runs out records
 // DCP_ERR_TIMEOUT.
 // Measured (bf16, 32 query heads over 4, D = 128): 4096 new tokens over 32768, 4
-// ranks: 1403 us, 1.47 PFLOP/s (0.75 of cuBLAS's burst, 0.85 of its rate under the
-// power cap); 2048 over 8192: 353 us.  The tensor core is busy under two thirds of
-// the cycles: a stage's chain (scores to registers, exponentials, P's store, two
+// ranks: 1403 to 1437 us, 1.46 PFLOP/s (0.77 of cuBLAS's burst, 0.86 of its rate under
+// the power cap); 2048 over 8192: 352 us.  The tensor core is busy 60% of the active
+// cycles, the multi-function unit 30%: a stage's chain (scores to registers, exponentials, P's store, two
 // products; 3100 cycles a pair of tiles) is longer than the other stage's
 // products, and there is no third stage in 512 columns.
-// Four new tokens of 32 requests of 16384: 199 us, 5.4 TB/s (161 us at the copy
-// rate), bound by the ends of items, where the ring runs dry.  D = 64 has as many
-// exponentials for half the products: 2048 over 8192 292 us.
+// Four new tokens of 32 requests of 16384: 200 us, 5.4 TB/s (159 us at the copy
+// rate), bound by the ends of items, where the ring runs dry.  At D = 64 a tile's chain
+// is as long and its products half as long: 2048 over 8192 291 us.
 // What the loops of all warps run has to fit the instruction cache, and the issuing
 // warps have 56 registers: long waits are out of line and descriptors are made where
 // they are used (chunk 373 -> 355 us, drafts 211 -> 199 us).
@@ -818,9 +818,14 @@ size_t chunk_attention_tc_workspace(int D) {
 
 bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
     // the maximum of the scaled scores is that of the scores for a positive scale
-    // only; boxes hold whole 8-row swizzle atoms.  Where both kernels can run this
-    // one is faster at every size measured: 199 against 326 us (drafts), 144 against
-    // 358 us (mixed, D = 64), 353 against 1891 and 1403 against 8085 us (chunks)
+    // only; boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one
+    // takes 199 against 326 us (drafts), 144 against 358 (mixed, D = 64), 353 against
+    // 1891 and 1403 against 8085 (chunks), 35 against 41 (32 ragged requests of up to
+    // 40 over 500), 12.5 against 13.0 (8 single tokens over 200).  It loses where every
+    // request is short, by its fixed part per item: 27 against 15 (64 single tokens over
+    // 128), 109 against 47 (256 requests, 2 over 100), 12 against 9.5 (one over 64).
+    // The lengths that tell these apart are on the device, where a captured graph
+    // follows them; max_seq_len bounds them only
     if ((p.D != 64 && p.D != 128) || !(p.sm_scale > 0.f) || p.page_shift < 3) return false;
     const EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;

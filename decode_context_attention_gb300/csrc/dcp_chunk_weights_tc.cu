@@ -23,11 +23,11 @@
 // log-sum-exps of the even and the odd query tiles' rows.
 // Waits are bounded (1 s): one that runs out records DCP_ERR_TIMEOUT.
 // Measured (D = 128, bf16, 32 query heads over 4): one new token of 64 requests of
-// 8192 tokens, 4 ranks: 96 us, 5.8 TB/s, bound by the keys' bytes (83 us at the copy
-// rate); 2048 new tokens over 16384, 2 ranks: 275 us, 0.94 PFLOP/s: the two tiles'
+// 8192 tokens, 4 ranks: 97 us, 5.7 TB/s, bound by the keys' bytes (82 us at the copy
+// rate); 2048 new tokens over 16384, 2 ranks: 277 us, 0.93 PFLOP/s: the two tiles'
 // 2 x 128 exponentials a row of threads take the multi-function unit as long as
-// their products take the tensor core, each is busy half the time, and 256 blocks
-// over 152 CTAs leave a sixth of it idle.
+// their products take the tensor core, each is busy under half of the cycles, and
+// 256 blocks over 152 CTAs leave a sixth of them idle.
 #include <cuda.h>
 #include <math.h>
 #include <stdlib.h>
@@ -554,9 +554,13 @@ cudaError_t launch_weights_tc(const ChunkParams& p, const CUtensorMap (&maps)[2]
 }  // namespace
 
 bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
-    // boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one is
-    // faster at every size measured: 96 against 147 us (64 single tokens, 8192),
-    // 74 against 178 us (ragged, 12 heads a group), 275 against 1412 us (2048 new)
+    // boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one takes
+    // 97 against 147 us (64 single tokens over 8192), 74 against 178 (ragged, 12 heads a
+    // group), 277 against 1412 (2048 new), 20 against 26 (32 ragged requests of up to 40
+    // over 500), 11.8 against 12.2 (8 of up to 20 over 300).  It loses by its set-up where
+    // there is little to do: 8.7 against 4.3 (one token over 64), 12.7 against 5.7 (64
+    // single tokens over 128), 26 against 13 (256 requests, 2 over 100).  The lengths
+    // that tell these apart are on the device; max_seq_len bounds them only
     if ((p.D != 64 && p.D != 128) || p.page_shift < 3) return false;
     const EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
