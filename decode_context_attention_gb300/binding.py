@@ -40,7 +40,7 @@ EXPORTS = ("dcp_lse_pack_dim", "dcp_status_string", "dcp_last_error_message", "d
            "dcp_decode_attention", "dcp_decode_attention_paged", "dcp_decode_attention_noalloc",
            "dcp_decode_attention_mla", "dcp_qk_norm_rope_append", "dcp_extend_attention_workspace_size",
            "dcp_extend_attention_paged", "dcp_attention_weights_paged", "dcp_cache_evict_paged",
-           "dcp_device_status")
+           "dcp_page_reserve", "dcp_page_release", "dcp_device_status")
 
 
 class DcpError(RuntimeError):
@@ -115,6 +115,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.dcp_cache_evict_paged.restype = i32
         lib.dcp_cache_evict_paged.argtypes = ([i32] * 5 + pool * 2 + table + [vp, i32] + rows3 + [vp, i32, i32]
                                               + [vp, i64, i64, i32] + rows3 * 2 + [vp])
+        groups, pages = [i32, vp, vp], [vp, i64, i64, i32] + [vp, i64, i32, vp, vp]
+        lib.dcp_page_reserve.restype = i32
+        lib.dcp_page_reserve.argtypes = [i32] * 6 + [vp, vp] + groups + pages + [vp] * 7
+        lib.dcp_page_release.restype = i32
+        lib.dcp_page_release.argtypes = [i32] * 5 + [vp, vp] + groups + pages + [vp, vp]
         lib.dcp_device_status.restype = i32
         lib.dcp_device_status.argtypes = []
         _lib = lib
@@ -180,6 +185,14 @@ def dcp_attention_weights_paged(*args) -> int:
 
 def dcp_cache_evict_paged(*args) -> int:
     return load().dcp_cache_evict_paged(*args)
+
+
+def dcp_page_reserve(*args) -> int:
+    return load().dcp_page_reserve(*args)
+
+
+def dcp_page_release(*args) -> int:
+    return load().dcp_page_release(*args)
 
 
 def dcp_device_status() -> int:
@@ -790,6 +803,117 @@ def cache_evict_paged(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc,
     dev, args = _evict_args(k_pages, v_pages, block_table, seq_lens, max_seq_len, acc, keep_lens, max_keep, recent,
                             dst_table, kept, acc_out, stream)
     _run_on(dev, load().dcp_cache_evict_paged, "dcp_cache_evict_paged", args)
+
+
+# ---------------------------------------------------------------------------
+# pages: a step's index arrays and new pages, and pages given back
+# ---------------------------------------------------------------------------
+
+def _group_args(group_start, prefix_lens):
+    """Number of groups and the pointers of group_start [G + 1], prefix_lens [G] int32 (both None: no groups)."""
+    if (group_start is None) != (prefix_lens is None):
+        raise ValueError("group_start and prefix_lens are given together")
+    if group_start is None:
+        return (0, None, None)
+    G = prefix_lens.shape[0] if prefix_lens.dim() == 1 else -1
+    return (G, _int32("group_start", group_start, G + 1), _int32("prefix_lens", prefix_lens, G))
+
+
+def _free_args(N: int, free_pages, free_count, free_count_out):
+    """The ranks' stacks free_pages [N, capacity] int32 with their numbers of pages, before and after."""
+    if free_pages.dtype != torch.int32 or free_pages.dim() != 2 or free_pages.shape[0] != N or (
+            free_pages.shape[1] > 1 and free_pages.stride(1) != 1):
+        raise ValueError(f"free_pages is int32 [N, capacity] = [{N}, ..] with unit stride along the pages")
+    return (free_pages.data_ptr(), free_pages.stride(0), free_pages.shape[1], _int32("free_count", free_count, N),
+            _int32("free_count_out", free_count_out, N))
+
+
+def _reserve_args(cached_lens, new_lens, max_seq_len, num_tokens, num_pages, page_size, block_table, free_pages,
+                  free_count, free_count_out, missing, query_start, seq_lens, positions, slots, requests, group_start,
+                  prefix_lens, stream):
+    dev = _chunk_device(block_table, cached_lens, new_lens, free_pages, free_count, free_count_out, missing,
+                        query_start, seq_lens, positions, slots, requests, group_start, prefix_lens)
+    N, B, _ = block_table.shape
+    T, num_pages = _length("num_tokens", num_tokens), _length("num_pages", num_pages)
+    if slots is not None and (slots.dtype != torch.int64 or slots.shape != (T,) or not slots.is_contiguous()):
+        raise ValueError(f"slots must be a contiguous int64 tensor of {T} elements")
+    return dev, (N, B, T, _length("page_size", page_size), num_pages, _length("max_seq_len", max_seq_len),
+                 _int32("cached_lens", cached_lens, B), _int32("new_lens", new_lens, B),
+                 *_group_args(group_start, prefix_lens), *_table_args(block_table, N, B),
+                 *_free_args(N, free_pages, free_count, free_count_out), _int32("missing", missing, N),
+                 _int32("query_start", query_start, B + 1), _int32("seq_lens", seq_lens, B),
+                 None if positions is None else _int32("positions", positions, T),
+                 None if slots is None else slots.data_ptr(),
+                 None if requests is None else _int32("requests", requests, T), _stream_on(dev, stream))
+
+
+def prepare_page_reserve(cached_lens: torch.Tensor, new_lens: torch.Tensor, max_seq_len: int, num_tokens: int,
+                         num_pages: int, page_size: int, block_table: torch.Tensor, free_pages: torch.Tensor,
+                         free_count: torch.Tensor, free_count_out: torch.Tensor, missing: torch.Tensor,
+                         query_start: torch.Tensor, seq_lens: torch.Tensor, positions: torch.Tensor | None = None,
+                         slots: torch.Tensor | None = None, requests: torch.Tensor | None = None,
+                         group_start: torch.Tensor | None = None, prefix_lens: torch.Tensor | None = None,
+                         stream=None) -> _Prepared:
+    """A step's index arrays, and pages for its new tokens from the ranks' free lists.
+
+    cached_lens, new_lens [B] int32; block_table [N,B,max_pages] int32, updated in
+    place; free_pages [N,capacity] int32 with free_count [N] int32 (read) and
+    free_count_out [N] (may be free_count); missing [N] int32: entries that got no
+    page (-1 in the table).  Written: query_start [B+1], seq_lens [B], and where
+    given positions, requests [num_tokens] int32 and slots [num_tokens] int64.
+    group_start [G+1] with prefix_lens [G] int32: requests whose whole pages of a
+    common prefix are their group's first request's."""
+    dev, args = _reserve_args(cached_lens, new_lens, max_seq_len, num_tokens, num_pages, page_size, block_table,
+                              free_pages, free_count, free_count_out, missing, query_start, seq_lens, positions, slots,
+                              requests, group_start, prefix_lens, stream)
+    return _PreparedOn(load().dcp_page_reserve, "dcp_page_reserve", dev, args,
+                       (cached_lens, new_lens, block_table, free_pages, free_count, free_count_out, missing,
+                        query_start, seq_lens, positions, slots, requests, group_start, prefix_lens))
+
+
+def page_reserve(cached_lens, new_lens, max_seq_len, num_tokens, num_pages, page_size, block_table, free_pages,
+                 free_count, free_count_out, missing, query_start, seq_lens, positions=None, slots=None, requests=None,
+                 group_start=None, prefix_lens=None, stream=None) -> None:
+    dev, args = _reserve_args(cached_lens, new_lens, max_seq_len, num_tokens, num_pages, page_size, block_table,
+                              free_pages, free_count, free_count_out, missing, query_start, seq_lens, positions, slots,
+                              requests, group_start, prefix_lens, stream)
+    _run_on(dev, load().dcp_page_reserve, "dcp_page_reserve", args)
+
+
+def _release_args(seq_lens, keep_lens, max_seq_len, num_pages, page_size, block_table, free_pages, free_count,
+                  free_count_out, lens_out, group_start, prefix_lens, stream):
+    dev = _chunk_device(block_table, seq_lens, keep_lens, free_pages, free_count, free_count_out, lens_out,
+                        group_start, prefix_lens)
+    N, B, _ = block_table.shape
+    return dev, (N, B, _length("page_size", page_size), _length("num_pages", num_pages),
+                 _length("max_seq_len", max_seq_len), _int32("seq_lens", seq_lens, B),
+                 _int32("keep_lens", keep_lens, B), *_group_args(group_start, prefix_lens),
+                 *_table_args(block_table, N, B), *_free_args(N, free_pages, free_count, free_count_out),
+                 None if lens_out is None else _int32("lens_out", lens_out, B), _stream_on(dev, stream))
+
+
+def prepare_page_release(seq_lens: torch.Tensor, keep_lens: torch.Tensor, max_seq_len: int, num_pages: int,
+                         page_size: int, block_table: torch.Tensor, free_pages: torch.Tensor,
+                         free_count: torch.Tensor, free_count_out: torch.Tensor, lens_out: torch.Tensor | None = None,
+                         group_start: torch.Tensor | None = None, prefix_lens: torch.Tensor | None = None,
+                         stream=None) -> _Prepared:
+    """Pages of the tokens that requests give up, back onto the ranks' free lists.
+
+    seq_lens, keep_lens [B] int32 (negative: the request stays as it is); lens_out
+    [B] int32 or None: the lengths afterwards; the rest as for prepare_page_reserve
+    (free_pages is written, block_table is not)."""
+    dev, args = _release_args(seq_lens, keep_lens, max_seq_len, num_pages, page_size, block_table, free_pages,
+                              free_count, free_count_out, lens_out, group_start, prefix_lens, stream)
+    return _PreparedOn(load().dcp_page_release, "dcp_page_release", dev, args,
+                       (seq_lens, keep_lens, block_table, free_pages, free_count, free_count_out, lens_out, group_start,
+                        prefix_lens))
+
+
+def page_release(seq_lens, keep_lens, max_seq_len, num_pages, page_size, block_table, free_pages, free_count,
+                 free_count_out, lens_out=None, group_start=None, prefix_lens=None, stream=None) -> None:
+    dev, args = _release_args(seq_lens, keep_lens, max_seq_len, num_pages, page_size, block_table, free_pages,
+                              free_count, free_count_out, lens_out, group_start, prefix_lens, stream)
+    _run_on(dev, load().dcp_page_release, "dcp_page_release", args)
 
 
 def device_status() -> int:

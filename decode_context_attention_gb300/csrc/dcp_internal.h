@@ -171,6 +171,35 @@ struct EvictParams {
     int64_t ao_sn, ao_sb, ao_sh;
 };
 
+// Page bookkeeping: a step's index arrays and new pages, and pages given back.
+struct PageParams {
+    int N, B, T, page_shift, num_pages, max_seq_len;
+    int G;                               // groups of requests with a common prefix
+    const int* group_start;              // [G + 1]
+    const int* prefix_lens;              // [G]
+    int* bt;                             // (release: read only)
+    int64_t bt_sn, bt_sb;                // int32 elements
+    int max_pages;
+    int* free_pages;                     // [N][free_capacity] (reserve: read only)
+    int64_t fp_sn;
+    int free_capacity;
+    const int* free_count;               // [N]
+    int* free_out;                       // [N], may be free_count
+    // reserve
+    const int* cached_lens;              // [B]
+    const int* new_lens;                 // [B]
+    int* missing;                        // [N]
+    int* query_start;                    // [B + 1]
+    int* seq_lens;                       // [B]
+    int* positions;                      // [T], or NULL; the same for the next two
+    int64_t* slots;
+    int* requests;
+    // release
+    const int* lens;                     // [B]
+    const int* keep_lens;                // [B]
+    int* lens_out;                       // [B], or NULL
+};
+
 // Records `msg` as this host thread's dcp_last_error_message() and returns s.
 dcp_status_t set_error(dcp_status_t s, const char* msg);
 
@@ -212,6 +241,8 @@ cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t s
 bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
 int chunk_weights_tc_status(bool clear);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_page_reserve(const PageParams& p, cudaStream_t stream);
+cudaError_t launch_page_release(const PageParams& p, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();

@@ -1,0 +1,250 @@
+// dcp_pages.cu -- the bookkeeping of round-robin paged caches on the device: a
+// step's index arrays and the pages of its new tokens from the requests' lengths,
+// and the way of pages back to the ranks' free lists.
+//
+// sglang PR #33926 report, "关键源码片段" (`get_dcp_lens`): rank r holds n / N of
+// n tokens, one more when r < n % N; "实现拆解" item 1 builds the tables over that
+// slice.  The pages build them on the host; here lengths never leave the device, so
+// a captured step stays valid while requests grow.
+//
+// With share(n, r) = n / N + (r < n % N) and S the entries a request has in common
+// with its group's first one, request b needs new pages for the entries
+//     [max(ceil(share(cached, r) / page), S), ceil(share(cached + n, r) / page))
+// of rank r's row.  The k-th entry of a rank, counted over the requests in order, takes
+// the k-th page from the top of the rank's stack.  Entry numbers are sums over the
+// requests before: one scan of the new tokens, then one of the entries, by one CTA for
+// a rank.  Everything else (common entries, the tokens' arrays) follows from the scans'
+// results entry by entry.
+#include "dcp_groups.cuh"
+#include "dcp_internal.h"
+
+namespace dcp {
+namespace {
+
+constexpr int kThreadsPages = 1024;
+
+__device__ __forceinline__ int share_of(int n, int r, int N) { return n / N + (r < n % N ? 1 : 0); }
+// Table entries that n tokens take on rank r.
+__device__ __forceinline__ int entries_of(const PageParams& p, int n, int r) {
+    return (int)(((int64_t)share_of(n, r, p.N) + (1 << p.page_shift) - 1) >> p.page_shift);
+}
+__device__ __forceinline__ Groups groups_of(const PageParams& p) {
+    return {p.G, p.group_start, p.prefix_lens, p.N, p.page_shift, p.max_seq_len, p.max_pages};
+}
+__device__ __forceinline__ int cached_of(const PageParams& p, int b) {
+    return min(max(__ldg(p.cached_lens + b), 0), p.max_seq_len);
+}
+
+// Inclusive sum over the block's threads; `warps` holds 33 numbers, free again
+// after the next barrier.  Ends behind a barrier.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) warps[warp] = v;
+    __syncthreads();
+    int64_t w = lane < (int)(blockDim.x >> 5) ? warps[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += x;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    if (warp) v += __shfl_sync(0xffffffffu, w, warp - 1);
+    __syncthreads();
+    return v;
+}
+
+// The last index i of [0, n) with at[i] <= x, for at[0] <= x and `at` non-decreasing.
+template <typename I>
+__device__ __forceinline__ int last_at_or_before(const I* at, int n, I x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Lengths, and rank r's new pages.  One CTA.
+__device__ void reserve_rank(const PageParams& p, int r, bool lengths) {
+    __shared__ int64_t warps[32];
+    __shared__ int64_t off[kThreadsPages];
+    __shared__ int have[kThreadsPages];
+    const int tid = threadIdx.x;
+    const Groups groups = groups_of(p);
+    const int left = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
+    const int* free = p.free_pages + (int64_t)r * p.fp_sn;
+    int* row = p.bt + (int64_t)r * p.bt_sn;
+    int64_t rows = 0, used = 0;  // new tokens and entries of the requests before
+    if (lengths && tid == 0) p.query_start[0] = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreadsPages) {
+        const int b = b0 + tid;
+        const bool there = b < p.B;
+        const int cached = there ? cached_of(p, b) : 0;
+        int n = there ? min(max(__ldg(p.new_lens + b), 0), p.max_seq_len - cached) : 0;
+        int64_t total;
+        // token rows end at T: what does not fit is cut off
+        const int64_t end = rows + block_scan(n, warps, &total);
+        const int s1 = (int)min(end, (int64_t)p.T), s0 = (int)min(end - n, (int64_t)p.T);
+        n = s1 - s0;
+        rows = min(rows + total, (int64_t)p.T);
+        if (there && lengths) {
+            p.query_start[b + 1] = s1;
+            p.seq_lens[b] = cached + n;
+        }
+        int low = 0, count = 0;
+        if (there) {
+            low = max(entries_of(p, cached, r), p.G ? member_of(groups, b).entries : 0);
+            count = max(entries_of(p, cached + n, r) - low, 0);
+        }
+        const int64_t upto = block_scan(count, warps, &total);
+        off[tid] = upto - count;
+        have[tid] = low;
+        __syncthreads();
+        for (int64_t k = tid; k < total; k += kThreadsPages) {
+            const int i = last_at_or_before(off, kThreadsPages, k);
+            const int64_t at = left - 1 - (used + k);
+            row[(int64_t)(b0 + i) * p.bt_sb + have[i] + (k - off[i])] = at >= 0 ? __ldg(free + at) : -1;
+        }
+        used += total;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        p.free_out[r] = (int)max(left - used, (int64_t)0);
+        p.missing[r] = (int)min(max(used - left, (int64_t)0), (int64_t)0x7fffffff);
+    }
+}
+
+// Common entries and the tokens' arrays, by worker `worker` of `workers` threads (whole
+// warps), from what reserve_rank left in memory.
+__device__ __forceinline__ void reserve_rest(const PageParams& p, int64_t worker, int64_t workers) {
+    const Groups groups = groups_of(p);
+    if (p.G) {
+        const int lane = worker & 31;
+        for (int64_t pair = worker >> 5; pair < (int64_t)p.N * p.B; pair += workers >> 5) {
+            const int b = (int)(pair / p.N), r = (int)(pair - (int64_t)b * p.N);
+            const Member m = member_of(groups, b);
+            const int* from = p.bt + (int64_t)r * p.bt_sn + (int64_t)m.first * p.bt_sb;
+            int* to = p.bt + (int64_t)r * p.bt_sn + (int64_t)b * p.bt_sb;
+            for (int j = lane; j < m.entries; j += 32) to[j] = from[j];
+        }
+    }
+    if (!p.positions && !p.slots && !p.requests) return;
+    const int n = p.query_start[p.B];
+    for (int64_t t = worker; t < n; t += workers) {
+        const int b = last_at_or_before(p.query_start, p.B + 1, (int)t);
+        const int g = cached_of(p, b) + (int)t - p.query_start[b];
+        if (p.positions) p.positions[t] = g;
+        if (p.requests) p.requests[t] = b;
+        if (p.slots) {
+            const int r = g % p.N, i = g / p.N, j = i >> p.page_shift;
+            // a common entry is read where it comes from, whether or not its copy is made yet
+            int from = b;
+            if (p.G) {
+                const Member m = member_of(groups, b);
+                if (j < m.entries) from = m.first;
+            }
+            const int pg = p.bt[(int64_t)r * p.bt_sn + (int64_t)from * p.bt_sb + j];
+            p.slots[t] = (unsigned)pg < (unsigned)p.num_pages
+                             ? ((((int64_t)r * p.num_pages + pg) << p.page_shift) | (i & ((1 << p.page_shift) - 1)))
+                             : -1;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreadsPages) reserve_pages_kernel(const PageParams p) {
+    reserve_rank(p, blockIdx.x, blockIdx.x == 0);
+}
+__global__ void __launch_bounds__(256) reserve_rest_kernel(const PageParams p) {
+    reserve_rest(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+// Rank r's pages of the entries that requests give up, onto its stack in order.  The
+// requests' entries, end to end, are dealt to the warps in equal shares: each counts
+// its valid pages, the counts' sums say where it writes.  One CTA for a rank.
+constexpr int kReleaseRequests = 2048;  // requests whose entries are dealt at once
+__global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const PageParams p) {
+    __shared__ int64_t warps[32];
+    __shared__ int64_t off[kReleaseRequests + 1];
+    __shared__ int low[kReleaseRequests];
+    constexpr int kPer = kReleaseRequests / kThreadsPages;
+    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Groups groups = groups_of(p);
+    const int have = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
+    int* free = p.free_pages + (int64_t)r * p.fp_sn;
+    const int* row = p.bt + (int64_t)r * p.bt_sn;
+    int64_t pushed = have;
+    for (int b0 = 0; b0 < p.B; b0 += kReleaseRequests) {
+        const int nb = min(kReleaseRequests, p.B - b0);
+        int64_t sum = 0, mine[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int i = kPer * tid + e, b = b0 + i;
+            int count = 0;
+            if (i < nb) {
+                const int L = min(max(__ldg(p.lens + b), 0), p.max_seq_len);
+                int keep = __ldg(p.keep_lens + b);
+                keep = keep < 0 ? L : min(keep, L);
+                low[i] = max(entries_of(p, keep, r), p.G ? member_of(groups, b).entries : 0);
+                count = max(entries_of(p, L, r) - low[i], 0);
+                if (p.lens_out && r == 0) p.lens_out[b] = keep;
+            }
+            mine[e] = sum;
+            sum += count;
+        }
+        int64_t total;
+        const int64_t before = block_scan(sum, warps, &total) - sum;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) off[kPer * tid + e] = before + mine[e];
+        __syncthreads();
+        const int64_t per = ((total + kThreadsPages - 1) / kThreadsPages) * 32;  // entries of a warp
+        const int64_t e0 = min(warp * per, total), e1 = min(e0 + per, total);
+        auto page_at = [&](int64_t e) {
+            if (e >= e1) return -1;
+            const int i = last_at_or_before(off, nb, e);
+            const int pg = __ldg(row + (int64_t)(b0 + i) * p.bt_sb + low[i] + (e - off[i]));
+            return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
+        };
+        int64_t valid = 0;
+        for (int64_t e = e0; e < e1; e += 32) valid += __popc(__ballot_sync(0xffffffffu, page_at(e + lane) >= 0));
+        const int64_t upto = block_scan(lane == 0 ? valid : 0, warps, &total);
+        int64_t at = pushed + __shfl_sync(0xffffffffu, upto, 0) - valid;
+        for (int64_t e = e0; e < e1; e += 32) {
+            const int pg = page_at(e + lane);
+            const unsigned on = __ballot_sync(0xffffffffu, pg >= 0);
+            const int64_t to = at + __popc(on & ((1u << lane) - 1u));
+            if (pg >= 0 && to < p.free_capacity) free[to] = pg;
+            at += __popc(on);
+        }
+        pushed += total;
+        __syncthreads();
+    }
+    __syncthreads();  // free_out may be free_count
+    if (tid == 0) p.free_out[r] = (int)min(pushed, (int64_t)p.free_capacity);
+}
+
+}  // namespace
+
+cudaError_t launch_page_reserve(const PageParams& p, cudaStream_t stream) {
+    reserve_pages_kernel<<<p.N, kThreadsPages, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const bool arrays = p.positions || p.slots || p.requests;
+    if (p.B == 0 || (!p.G && (!arrays || p.T == 0))) return cudaSuccess;
+    const int64_t copies = p.G ? (int64_t)p.N * p.B * 32 : 0, tokens = arrays ? p.T : 0;
+    const int64_t blocks = ((copies > tokens ? copies : tokens) + 255) / 256, most = 8ll * device_sm_count();
+    reserve_rest_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_page_release(const PageParams& p, cudaStream_t stream) {
+    release_pages_kernel<<<p.N, kThreadsPages, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace dcp

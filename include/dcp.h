@@ -21,7 +21,8 @@
  * and the steps around it when a request brings more than one new token:
  *
  *   dcp_qk_norm_rope_append, dcp_extend_attention_paged,
- *   dcp_attention_weights_paged, dcp_cache_evict_paged
+ *   dcp_attention_weights_paged, dcp_cache_evict_paged,
+ *   dcp_page_reserve, dcp_page_release
  *
  * The cross-rank exchange itself (NCCL all-to-all, MNNVL, all-gather /
  * all-reduce) is not part of this library.  A group's N ranks can be held as
@@ -569,6 +570,76 @@ dcp_status_t dcp_cache_evict_paged(int dtype, int N, int B, int Hkv, int D,
                                    const int* dst_table, int64_t dt_sn, int64_t dt_sb, int dst_max_pages,
                                    int* kept, int64_t kp_sn, int64_t kp_sb, int64_t kp_sh,
                                    float* acc_out, int64_t ao_sn, int64_t ao_sb, int64_t ao_sh, void* stream);
+
+/*
+ * dcp_page_reserve -- a step's index arrays and the pages of its new tokens,
+ * from the requests' lengths on the device.  (sglang PR #33926 report, "实现拆解"
+ * item 1 and "关键源码片段", `get_dcp_lens`, `_fill_dcp_block_kv_indices`: tables
+ * over each rank's round-robin slice, there filled on the way to the device.)
+ *
+ * Request b holds cached_lens[b] tokens and asks for new_lens[b] more:
+ *     n_b = new_lens[b], cut to max_seq_len - cached_lens[b] and, in order, so
+ *           that the rows of all requests end at T;  0 when negative
+ *     query_start[b] = n_0 + .. + n_{b-1},  seq_lens[b] = cached_lens[b] + n_b
+ * and for each new token t = query_start[b] + j, of index g = cached_lens[b] + j:
+ *     positions[t] = g,  requests[t] = b,  slots[t] = row of its keys and values in
+ *     the pools seen as [N * num_pages * page_size, ...], -1 where its table entry
+ *     is not in [0, num_pages).
+ * With e_r(n) = ceil(L_r(n) / page_size) the table entries of n tokens on rank r,
+ * the entries [max(e_r(cached_lens[b]), S_b), e_r(seq_lens[b])) of
+ * block_table[r][b] get new pages: rank r's stack is free_pages[r][0 .. free_count[r])
+ * and the k-th entry that it fills, counted over the requests in order, takes
+ * free_pages[r][free_count[r] - 1 - k], or -1 when the stack is empty.
+ * free_count_out[r] is what is left (free_count_out may be free_count) and
+ * missing[r] the number of entries that got none.  free_pages is not written.
+ *
+ * Groups: requests group_start[g] <= b < group_start[g + 1] have their first
+ * prefix_lens[g] tokens in common, and S_b = floor(prefix_lens[g] / (N * page_size))
+ * pages of them on every rank are the first request's: entries [0, S_b) of the
+ * other requests are written from it on every call.  A request that joins a group
+ * therefore holds S_b * N * page_size cached tokens and brings what follows them
+ * itself; the first one keeps the pages for all, and may be a request that never
+ * brings a token.  S_b = 0 outside of groups and for a group's first request.
+ *
+ *   cached_lens, new_lens [B] int32;  group_start [G + 1], prefix_lens [G] int32
+ *           (G may be 0); group_start is non-decreasing
+ *   block_table [N][B, max_pages] strides (bt_sn, bt_sb), only the entries named
+ *           above are written;  free_pages [N][free_capacity] stride fp_sn
+ *   query_start [B + 1], seq_lens [B], missing [N], free_count(_out) [N]
+ *   positions, requests [T] int32, slots [T] int64: each may be NULL; rows from
+ *           query_start[B] on are not written
+ * Everything is a sum of integers in a fixed order: equal calls give equal results.
+ * page_size a power of two up to 65536.  No workspace.
+ */
+dcp_status_t dcp_page_reserve(int N, int B, int T, int page_size, int num_pages, int max_seq_len,
+                              const int* cached_lens, const int* new_lens,
+                              int G, const int* group_start, const int* prefix_lens,
+                              int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                              const int* free_pages, int64_t fp_sn, int free_capacity, const int* free_count,
+                              int* free_count_out, int* missing, int* query_start, int* seq_lens,
+                              int* positions, int64_t* slots, int* requests, void* stream);
+
+/*
+ * dcp_page_release -- the pages of tokens that requests give up, back onto the
+ * ranks' stacks.
+ *
+ * Request b shrinks from seq_lens[b] to min(seq_lens[b], keep_lens[b]) tokens
+ * (keep_lens[b] < 0: it stays as it is), which lens_out[b] says unless NULL.  On
+ * each rank the pages of its entries [max(e_r(kept), S_b), e_r(seq_lens[b])), with
+ * e_r and S_b as for dcp_page_reserve, are pushed in order, of the requests in
+ * order: free_pages[r][free_count[r] + i] for the i-th of them.  Entries outside
+ * [0, num_pages) hold no page and are passed over; pages beyond free_capacity are
+ * dropped.  free_count_out[r] (may be free_count) is the new number.  The table is
+ * not written: its entries behind a request's tokens mean nothing.  A group's
+ * common pages go back when its first request gives them up: that is the caller's
+ * to do last.
+ */
+dcp_status_t dcp_page_release(int N, int B, int page_size, int num_pages, int max_seq_len,
+                              const int* seq_lens, const int* keep_lens,
+                              int G, const int* group_start, const int* prefix_lens,
+                              const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                              int* free_pages, int64_t fp_sn, int free_capacity, const int* free_count,
+                              int* free_count_out, int* lens_out, void* stream);
 
 /*
  * dcp_device_status -- DCP_OK, or DCP_ERR_TIMEOUT when a tensor-core kernel
