@@ -40,7 +40,8 @@ EXPORTS = ("dcp_lse_pack_dim", "dcp_status_string", "dcp_last_error_message", "d
            "dcp_decode_attention", "dcp_decode_attention_paged", "dcp_decode_attention_noalloc",
            "dcp_decode_attention_mla", "dcp_qk_norm_rope_append", "dcp_extend_attention_workspace_size",
            "dcp_extend_attention_paged", "dcp_attention_weights_paged", "dcp_cache_evict_paged",
-           "dcp_page_reserve", "dcp_page_release", "dcp_device_status")
+           "dcp_page_reserve", "dcp_page_release", "dcp_prefix_attention_workspace_size",
+           "dcp_prefix_attention_paged", "dcp_device_status")
 
 
 class DcpError(RuntimeError):
@@ -120,6 +121,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.dcp_page_reserve.argtypes = [i32] * 6 + [vp, vp] + groups + pages + [vp] * 7
         lib.dcp_page_release.restype = i32
         lib.dcp_page_release.argtypes = [i32] * 5 + [vp, vp] + groups + pages + [vp, vp]
+        lib.dcp_prefix_attention_workspace_size.restype = ctypes.c_size_t
+        lib.dcp_prefix_attention_workspace_size.argtypes = [i32] * 8
+        extend = lib.dcp_extend_attention_paged.argtypes
+        lib.dcp_prefix_attention_paged.restype = i32
+        lib.dcp_prefix_attention_paged.argtypes = extend[:29] + groups + extend[29:]
         lib.dcp_device_status.restype = i32
         lib.dcp_device_status.argtypes = []
         _lib = lib
@@ -193,6 +199,15 @@ def dcp_page_reserve(*args) -> int:
 
 def dcp_page_release(*args) -> int:
     return load().dcp_page_release(*args)
+
+
+def dcp_prefix_attention_workspace_size(N: int, B: int, T: int, H: int, Hkv: int, D: int, max_seq_len: int,
+                                        G: int) -> int:
+    return load().dcp_prefix_attention_workspace_size(N, B, T, H, Hkv, D, max_seq_len, G)
+
+
+def dcp_prefix_attention_paged(*args) -> int:
+    return load().dcp_prefix_attention_paged(*args)
 
 
 def dcp_device_status() -> int:
@@ -665,9 +680,11 @@ def _scratch(nbytes: int, device, stream):
     return ws
 
 
-def _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse, sm_scale, base, causal,
-                 workspace, stream):
-    dev = _chunk_device(q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace)
+def _attend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, groups, o, lse, sm_scale, base,
+                 causal, workspace, stream):
+    """Arguments of extend_attention_paged (groups None) and of prefix_attention_paged (groups: its group_start and
+    prefix_lens)."""
+    dev = _chunk_device(q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace, *(groups or ()))
     T, H, D = q.shape
     max_seq_len = _length("max_seq_len", max_seq_len)
     pool = k_pages.shape
@@ -676,18 +693,20 @@ def _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_se
     if pool[4] != D:
         raise ValueError(f"pages of head dimension {pool[4]}, heads of {D}")
     code = _same_dtype(q, k_pages, v_pages, o)
+    shared = () if groups is None else _group_args(*groups)
     args = (code, N, B, T, H, Hkv, D, *_rows_args(q, (T, H, D), "q"), *_pool_args(k_pages, pool),
             *_pool_args(v_pages, pool), num_pages, page_size, *_table_args(block_table, N, B),
-            _int32("query_start", query_start, B + 1), _int32("seq_lens", seq_lens, B), max_seq_len, float(sm_scale),
-            1 if causal else 0, *_rows_args(o, (N, T, H, D), "o"), *_word_args(lse, (N, T, H), "lse"),
+            _int32("query_start", query_start, B + 1), _int32("seq_lens", seq_lens, B), max_seq_len, *shared,
+            float(sm_scale), 1 if causal else 0, *_rows_args(o, (N, T, H, D), "o"), *_word_args(lse, (N, T, H), "lse"),
             _base_code(base))
     if workspace is None:
-        size = load().dcp_extend_attention_workspace_size
+        size = load().dcp_extend_attention_workspace_size if groups is None else load().dcp_prefix_attention_workspace_size
+        sizes = (N, B, T, H, Hkv, D, max_seq_len, *shared[:1])
         if dev.index == torch.cuda.current_device():
-            nbytes = size(N, B, T, H, Hkv, D, max_seq_len)
+            nbytes = size(*sizes)
         else:
             with torch.cuda.device(dev):
-                nbytes = size(N, B, T, H, Hkv, D, max_seq_len)
+                nbytes = size(*sizes)
         workspace = _scratch(nbytes, dev, stream)
     return dev, workspace, (*args, *_workspace_args(workspace), _stream_on(dev, stream))
 
@@ -703,17 +722,48 @@ def prepare_extend_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pag
     [N,B,max_pages] int32; query_start [B+1], seq_lens [B] int32; o [N,T,H,D],
     lse [N,T,H] fp32: the partials that lse_combine merges.  `workspace` (uint8,
     device, extend_workspace_bytes() long) is allocated here when not given."""
-    dev, workspace, args = _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse,
-                                        sm_scale, base, causal, workspace, stream)
+    dev, workspace, args = _attend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, None, o,
+                                        lse, sm_scale, base, causal, workspace, stream)
     return _PreparedOn(load().dcp_extend_attention_paged, "dcp_extend_attention_paged", dev, args,
                        (q, k_pages, v_pages, block_table, query_start, seq_lens, o, lse, workspace))
 
 
 def extend_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse, sm_scale,
                            base="e", causal=True, workspace=None, stream=None) -> None:
-    dev, _, args = _extend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, o, lse,
+    dev, _, args = _attend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, None, o, lse,
                                 sm_scale, base, causal, workspace, stream)
     _run_on(dev, load().dcp_extend_attention_paged, "dcp_extend_attention_paged", args)
+
+
+def prefix_workspace_bytes(N: int, B: int, T: int, H: int, Hkv: int, D: int, max_seq_len: int, G: int) -> int:
+    """Bytes of workspace prefix_attention_paged needs on the current device."""
+    return dcp_prefix_attention_workspace_size(N, B, T, H, Hkv, D, _length("max_seq_len", max_seq_len), G)
+
+
+def prepare_prefix_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                   block_table: torch.Tensor, query_start: torch.Tensor, seq_lens: torch.Tensor,
+                                   max_seq_len: int, group_start: torch.Tensor | None,
+                                   prefix_lens: torch.Tensor | None, o: torch.Tensor, lse: torch.Tensor,
+                                   sm_scale: float, base: str = "e", causal: bool = True,
+                                   workspace: torch.Tensor | None = None, stream=None) -> _Prepared:
+    """prepare_extend_attention_paged for requests that share prefixes: requests
+    group_start[g]..group_start[g+1] have their first prefix_lens[g] tokens in common,
+    whose whole pages are attended once for all of them.
+
+    group_start [G+1], prefix_lens [G] int32 (None: no groups).  `workspace` (uint8,
+    device, prefix_workspace_bytes() long) is allocated here when not given."""
+    dev, workspace, args = _attend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len,
+                                        (group_start, prefix_lens), o, lse, sm_scale, base, causal, workspace, stream)
+    return _PreparedOn(load().dcp_prefix_attention_paged, "dcp_prefix_attention_paged", dev, args,
+                       (q, k_pages, v_pages, block_table, query_start, seq_lens, group_start, prefix_lens, o, lse,
+                        workspace))
+
+
+def prefix_attention_paged(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len, group_start,
+                           prefix_lens, o, lse, sm_scale, base="e", causal=True, workspace=None, stream=None) -> None:
+    dev, _, args = _attend_args(q, k_pages, v_pages, block_table, query_start, seq_lens, max_seq_len,
+                                (group_start, prefix_lens), o, lse, sm_scale, base, causal, workspace, stream)
+    _run_on(dev, load().dcp_prefix_attention_paged, "dcp_prefix_attention_paged", args)
 
 
 def _weights_args(q, k_pages, block_table, query_start, seq_lens, max_seq_len, lse, acc, sm_scale, base, stream):

@@ -27,9 +27,53 @@ __device__ __forceinline__ Request load_request(const ChunkParams& p, int b) {
     return {s, e - s, L};
 }
 
+// A request as the plan of a batch that shares prefixes has it: the common part of a
+// group (the rows of all its requests, tokens before them) or a request's own part
+// (tokens from table entry `first` on, their number a multiple of N before it, so that
+// the round-robin shares of what is left stay those of a request that begins there).
+enum { kAlone = 0, kCommon = 1, kOwn = 2 };
+struct Planned : Request {
+    int b, first;  // row of the block table, first entry
+    int kind;      // kAlone: no common part, nothing to join
+    int common;    // kOwn: the index of its common part
+};
+template <class P>
+struct RequestOf {
+    using type = Request;
+};
+template <>
+struct RequestOf<PrefixParams> {
+    using type = Planned;
+};
+__device__ __forceinline__ Planned load_request(const PrefixParams& p, int v) {
+    const int4 a = __ldg(p.plan + 2 * (int64_t)v), b = __ldg(p.plan + 2 * (int64_t)v + 1);
+    Planned q;
+    q.start = a.x; q.n = a.y; q.L = a.z; q.b = a.w;
+    q.first = b.x; q.kind = b.y; q.common = b.z;
+    return q;
+}
+__device__ __forceinline__ bool is_causal(const ChunkParams& p, const Request&) { return p.causal != 0; }
+__device__ __forceinline__ bool is_causal(const PrefixParams& p, const Planned& q) {
+    return p.causal && q.kind != kCommon;
+}
+
 // Local tokens of rank r that new token j of the request sees.
-__device__ __forceinline__ int visible(const ChunkParams& p, const Request& q, int j, int r) {
-    return rank_share(p.causal ? q.L - q.n + j + 1 : q.L, r, p.N);
+template <class P, class R>
+__device__ __forceinline__ int visible(const P& p, const R& q, int j, int r) {
+    return rank_share(is_causal(p, q) ? q.L - q.n + j + 1 : q.L, r, p.N);
+}
+
+// Where the table entries of (rank, request b = q) begin.
+__device__ __forceinline__ int64_t table_at(const ChunkParams& p, const Request&, int r, int b) {
+    return (int64_t)r * p.bt_sn + (int64_t)b * p.bt_sb;
+}
+__device__ __forceinline__ int64_t table_at(const PrefixParams& p, const Planned& q, int r, int) {
+    return (int64_t)r * p.bt_sn + (int64_t)q.b * p.bt_sb + q.first;
+}
+// Page of local token i from the entries at `at`, or -1 when they name none of the pool's.
+__device__ __forceinline__ int page_in(const ChunkParams& p, int64_t at, int i) {
+    const int pg = __ldg(p.bt + at + (i >> p.page_shift));
+    return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
 }
 
 // Page of local token i, or -1 when the table names none of the pool's.
@@ -123,13 +167,15 @@ __device__ __forceinline__ bool same_item(const ChunkPos& x, const ChunkPos& y) 
 }
 
 // Tiles that block qt of the request sees on rank r.
-__device__ __forceinline__ int item_tiles(const ChunkParams& p, const Request& q, int r, int qt, int tpi, int tt) {
+template <class P, class R>
+__device__ __forceinline__ int item_tiles(const P& p, const R& q, int r, int qt, int tpi, int tt) {
     const int last = min((qt + 1) * tpi, q.n) - 1;
     return (visible(p, q, last, r) + tt - 1) / tt;
 }
 
 // The first position of the item after `x`.
-__device__ __forceinline__ ChunkPos next_item(const ChunkParams& p, const ChunkPos& x, int tpi) {
+template <class P>
+__device__ __forceinline__ ChunkPos next_item(const P& p, const ChunkPos& x, int tpi) {
     ChunkPos y = x;
     y.tile = 0;
     if (++y.qt * tpi < load_request(p, y.b).n) return y;
@@ -158,17 +204,18 @@ struct HeadWork {
     int64_t a, b, m;
     __device__ int weight(int q) const { return q < nq - 1 ? wf : wl; }
 };
-__device__ inline HeadWork head_work(const ChunkParams& p, int pair, int tpi, int half, int tt) {
+template <class P>
+__device__ inline HeadWork head_work(const P& p, int pair, int tpi, int half, int tt) {
     HeadWork w;
     const int r = pair % p.N;
-    const Request q = load_request(p, pair / p.N);
+    const auto q = load_request(p, pair / p.N);
     w.nq = (q.n + tpi - 1) / tpi;
     w.last = (rank_share(q.L, r, p.N) + tt - 1) / tt;  // its last row is the request's last token
     w.q0 = 0;
     w.wf = tpi > half ? kPairTile : kBlockTile;
     w.wl = q.n - (w.nq - 1) * tpi > half ? kPairTile : kBlockTile;
     w.m = (int64_t)p.N * tt;
-    if (p.causal) {
+    if (is_causal(p, q)) {
         // block qt's last row has x = L - n + (qt + 1) tpi tokens before or at it: rank_share(x) =
         // floor((x + N - 1 - r) / N), tiles = floor((x + m - 1 - r) / m), 0 below zero
         w.a = tpi;
@@ -195,7 +242,8 @@ __device__ inline int64_t work_before(const HeadWork& w, int q) {
 // The start of range c of `ctas`.  upto[t] is the work up to and with the pairs of
 // slot t (`per` (request, rank) pairs each, `slots` slots).  One warp, whose lanes
 // try as many places of a search at once.
-__device__ __forceinline__ ChunkPos range_start(const ChunkParams& p, int tpi, int half, int tt, int ctas, int c,
+template <class P>
+__device__ __forceinline__ ChunkPos range_start(const P& p, int tpi, int half, int tt, int ctas, int c,
                                                 const int64_t* upto, int slots, int64_t per) {
     const unsigned all = 0xffffffffu;
     const int lane = threadIdx.x & 31;
@@ -248,8 +296,8 @@ __device__ __forceinline__ ChunkPos range_start(const ChunkParams& p, int tpi, i
 // Every CTA finds its own range: range[0] and range[1], with the starts of all
 // ranges left in pos for the merge.  `scratch` holds THREADS + 32 numbers.  All
 // threads of the CTA; ends with a barrier.
-template <int THREADS>
-__device__ __forceinline__ void find_range(const ChunkParams& p, int tpi, int half, int tt, ChunkPos* pos,
+template <int THREADS, class P>
+__device__ __forceinline__ void find_range(const P& p, int tpi, int half, int tt, ChunkPos* pos,
                                            int64_t* scratch, ChunkPos* range) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t npairs = (int64_t)p.B * p.N;
@@ -281,22 +329,28 @@ __device__ __forceinline__ void find_range(const ChunkParams& p, int tpi, int ha
 }
 
 // A CTA's part of an item.
-struct ChunkSeg {
+template <class R>
+struct ChunkSegOf {
     int b, r, hkv;
     int row0, nrows;     // first token row, rows (token, head) of the item
     int j0;              // first new token of the item within its request
     int t0, t1;          // tiles [t0, t1) of its ntiles
     int lim0, lim_last;  // tokens its first and its last row see: the tiles from lim0 / tt on are masked
     int slot;            // where a partial result goes, -1 when the part is the whole item
-    Request q;
+    int64_t table;       // where the request's table entries begin
+    R q;
 };
-__device__ __forceinline__ ChunkSeg load_seg(const ChunkParams& p, const ChunkPos& x, const ChunkPos& first,
-                                             const ChunkPos& end, int tpi, int tt) {
-    ChunkSeg s;
+template <class P>
+using ChunkSegFor = ChunkSegOf<typename RequestOf<P>::type>;
+template <class P>
+__device__ __forceinline__ ChunkSegFor<P> load_seg(const P& p, const ChunkPos& x, const ChunkPos& first,
+                                                   const ChunkPos& end, int tpi, int tt) {
+    ChunkSegFor<P> s;
     s.b = x.b;
     s.r = x.rh / p.Hkv;
     s.hkv = x.rh - s.r * p.Hkv;
     s.q = load_request(p, x.b);
+    s.table = table_at(p, s.q, s.r, s.b);
     s.j0 = x.qt * tpi;
     const int tokens = min(tpi, s.q.n - s.j0);
     s.row0 = s.q.start + s.j0;
@@ -323,18 +377,34 @@ ChunkPartials chunk_partials_in(unsigned char* ws, int ctas, int rows, int D);
 cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int tt, int rows, int ctas,
                                int dtype, cudaStream_t stream);
 
+// The same for a batch that shares prefixes, with its common and own parts.
+cudaError_t launch_prefix_join(const PrefixParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
+                               cudaStream_t stream);
+
+// Where the row of a part goes in fp32 when it is not the whole result: the slot of a
+// cut item, else the plan's row of a part that is joined; -1: the output itself.
+__device__ __forceinline__ int64_t partial_row(const ChunkParams&, const Request&, int, int64_t, int) { return -1; }
+__device__ __forceinline__ int64_t partial_row(const PrefixParams& p, const Planned& q, int r, int64_t t, int h) {
+    if (q.kind == kAlone) return -1;
+    return (((int64_t)(q.kind - 1) * p.N + r) * p.T + t) * p.H + h;
+}
+__device__ __forceinline__ float* partial_o(const ChunkParams&) { return nullptr; }
+__device__ __forceinline__ float* partial_o(const PrefixParams& p) { return p.wo; }
+__device__ __forceinline__ float* partial_lse(const ChunkParams&) { return nullptr; }
+__device__ __forceinline__ float* partial_lse(const PrefixParams& p) { return p.wl; }
+
 // Adds what the tokens set in `mask` (local tokens tile0 + bit, tokens whose V row
 // holds NaN or infinities and was zeroed for the product) give to a row that
 // sees them (i < lim): out[d] += p_i v_i[d] for the elements that are not
-// finite.  lse2 is the row's base-2 log-sum-exp.  One thread, a rare path.
+// finite.  `table`: where the request's entries begin.  lse2 is the row's base-2 log-sum-exp.  One thread, a rare path.
 template <typename T, typename O>
-__device__ __noinline__ void add_nonfinite(const ChunkParams& p, int r, int b, int hkv, const T* q, int tile0,
+__device__ __noinline__ void add_nonfinite(const ChunkParams& p, int r, int64_t table, int hkv, const T* q, int tile0,
                                            const unsigned* mask, int words, int lim, float lse2, O* out) {
     for (int w = 0; w < words; ++w) {
         for (unsigned m = mask[w]; m; m &= m - 1) {
             const int i = tile0 + 32 * w + __ffs(m) - 1;
             if (i >= lim) return;
-            const int pg = page_of(p, r, b, i);
+            const int pg = page_in(p, table, i);
             if (pg < 0) continue;
             const T* k = reinterpret_cast<const T*>(p.k + k_offset(p, r, pg, i, hkv));
             const T* v = reinterpret_cast<const T*>(p.v + v_offset(p, r, pg, i, hkv));

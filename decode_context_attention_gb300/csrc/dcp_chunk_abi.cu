@@ -93,6 +93,70 @@ bool pools_disjoint(const Pool& k, const Pool& v, const View& kp, const View& vp
     return both.dim(2, (int64_t)(k_first ? vp.base - kp.base : kp.base - vp.base)).rows_disjoint();
 }
 
+// dcp_extend_attention_paged and dcp_prefix_attention_paged (G groups; 0: none).
+dcp_status_t attend(const char* who, int dtype, int N, int B, int T, int H, int Hkv, int D, const void* q, int64_t q_st,
+                    int64_t q_sh, const Pool& pk, const Pool& pv, int num_pages, int page_size, const int* block_table,
+                    int64_t bt_sn, int64_t bt_sb, int max_pages, const int* query_start, const int* seq_lens,
+                    int max_seq_len, int G, const int* group_start, const int* prefix_lens, float sm_scale, int causal,
+                    void* o, int64_t o_sn, int64_t o_st, int64_t o_sh, float* lse, int64_t l_sn, int64_t l_st,
+                    int64_t l_sh, int lse_base, void* workspace, size_t workspace_bytes, void* stream) {
+    if (const dcp_status_t s = check_batch(who, dtype, N, B, T, Hkv, num_pages, page_size, max_pages, max_seq_len))
+        return s;
+    if (const dcp_status_t s = check_heads(who, T, H, Hkv, D)) return s;
+    if (!finite(sm_scale)) return fail(DCP_ERR_INVALID_ARG, "%s: sm_scale is not finite", who);
+    if (lse_base != DCP_LSE_BASE_E && lse_base != DCP_LSE_BASE_2)
+        return fail(DCP_ERR_INVALID_ARG, "%s: lse_base %d", who, lse_base);
+    // the plan's requests are counted in 32 bits, too
+    if (G < 0 || (int64_t)N * ((int64_t)G + B) * Hkv >= (1ll << 31) || (int64_t)G + B >= (1 << 30))
+        return fail(DCP_ERR_INVALID_ARG, "%s: G=%d (N * (G + B) * Hkv below 2^31)", who, G);
+    if (B == 0 || T == 0) return ok();
+    if (!q || !pk.p || !pv.p || !block_table || !query_start || !seq_lens || !o || !lse ||
+        (G && (!group_start || !prefix_lens)))
+        return fail(DCP_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (bad_stride({q_st, q_sh, pk.sn, pk.sp, pk.st, pk.sh, pv.sn, pv.sp, pv.st, pv.sh, bt_sn, bt_sb, o_sn, o_st, o_sh, l_sn,
+                    l_st, l_sh}))
+        return fail(DCP_ERR_INVALID_ARG, "%s: negative stride or one above 2^52 elements", who);
+    const int64_t rb = (int64_t)D * 2;
+    View vq = View(q, rb).dim(T, q_st * 2).dim(H, q_sh * 2);
+    View kp = pk.view(N, num_pages, page_size, Hkv, D), vp = pv.view(N, num_pages, page_size, Hkv, D);
+    View vo = View(o, rb).dim(N, o_sn * 2).dim(T, o_st * 2).dim(H, o_sh * 2);
+    View vl = View(lse, 4).dim(N, l_sn * 4).dim(T, l_st * 4).dim(H, l_sh * 4);
+    View qs = View(query_start, 4).dim((int64_t)B + 1, 4), sl = View(seq_lens, 4).dim(B, 4);
+    View gs = View(group_start, G ? 4 : 0).dim((int64_t)G + 1, 4), pl = View(prefix_lens, G ? 4 : 0).dim(G, 4);
+    View bt = View(block_table, 4).dim(N, bt_sn * 4).dim(B, bt_sb * 4).dim(max_pages, 4);
+    if (!all_fit({&vq, &kp, &vp, &vo, &vl, &bt}))
+        return fail(DCP_ERR_INVALID_ARG, "%s: an operand's strides span more than 2^56 bytes", who);
+    if (vq.align() < 16 || kp.align() < 16 || vp.align() < 16 || vo.align() < 16)
+        return fail(DCP_ERR_MISALIGNED, "%s: q, o and page rows must start on 16-byte boundaries", who);
+    if ((uintptr_t)lse % 4 || (uintptr_t)block_table % 4 || (uintptr_t)query_start % 4 || (uintptr_t)seq_lens % 4 ||
+        (G && ((uintptr_t)group_start % 4 || (uintptr_t)prefix_lens % 4)))
+        return fail(DCP_ERR_MISALIGNED, "%s: pointer not aligned to its element type", who);
+    for (const View* out : {&vo, &vl})
+        if (any_overlap(*out, {&vq, &kp, &vp, &qs, &sl, &bt, &gs, &pl}))
+            return fail(DCP_ERR_ALIAS, "%s: an output overlaps an input", who);
+    if (overlap(vo, vl) || !vo.rows_disjoint() || !vl.rows_disjoint())
+        return fail(DCP_ERR_ALIAS, "%s: outputs overlap", who);
+    const size_t need = prefix_attention_workspace(N, B, T, H, Hkv, D, max_seq_len, G);
+    if (!workspace || workspace_bytes < need)
+        return fail(DCP_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed (%zu given)", who, need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if ((uintptr_t)workspace % 16) return fail(DCP_ERR_MISALIGNED, "%s: workspace not 16-byte aligned", who);
+    if (any_overlap(View(workspace, (int64_t)need), {&vq, &kp, &vp, &vo, &vl, &qs, &sl, &bt, &gs, &pl}))
+        return fail(DCP_ERR_ALIAS, "%s: workspace overlaps an operand", who);
+    PrefixParams p{};
+    fill_batch(p, N, B, T, H, Hkv, D, max_seq_len, page_size, num_pages, block_table, bt_sn, bt_sb, query_start,
+               seq_lens, pk, pv);
+    p.causal = causal != 0;
+    p.base2 = lse_base == DCP_LSE_BASE_2;
+    p.sm_scale = sm_scale;
+    p.q = (const unsigned char*)q; p.q_st = q_st * 2; p.q_sh = q_sh * 2;
+    p.o = (unsigned char*)o; p.o_sn = o_sn * 2; p.o_st = o_st * 2; p.o_sh = o_sh * 2;
+    p.lse = lse; p.l_sn = l_sn; p.l_st = l_st; p.l_sh = l_sh;
+    p.ws = (unsigned char*)workspace;
+    p.requests = B; p.groups = G; p.group_start = group_start; p.prefix_lens = prefix_lens; p.max_pages = max_pages;
+    return launched(launch_prefix_attention(p, dtype, (cudaStream_t)stream), who);
+}
+
 }  // namespace
 
 extern "C" {
@@ -205,56 +269,35 @@ dcp_status_t dcp_extend_attention_paged(int dtype, int N, int B, int T, int H, i
                                         void* o, int64_t o_sn, int64_t o_st, int64_t o_sh,
                                         float* lse, int64_t l_sn, int64_t l_st, int64_t l_sh,
                                         int lse_base, void* workspace, size_t workspace_bytes, void* stream) {
-    const char* who = "dcp_extend_attention_paged";
-    if (const dcp_status_t s = check_batch(who, dtype, N, B, T, Hkv, num_pages, page_size, max_pages, max_seq_len))
-        return s;
-    if (const dcp_status_t s = check_heads(who, T, H, Hkv, D)) return s;
-    if (!finite(sm_scale)) return fail(DCP_ERR_INVALID_ARG, "%s: sm_scale is not finite", who);
-    if (lse_base != DCP_LSE_BASE_E && lse_base != DCP_LSE_BASE_2)
-        return fail(DCP_ERR_INVALID_ARG, "%s: lse_base %d", who, lse_base);
-    if (B == 0 || T == 0) return ok();
-    if (!q || !k_pages || !v_pages || !block_table || !query_start || !seq_lens || !o || !lse)
-        return fail(DCP_ERR_INVALID_ARG, "%s: NULL pointer", who);
-    if (bad_stride({q_st, q_sh, k_sn, k_sp, k_st, k_sh, v_sn, v_sp, v_st, v_sh, bt_sn, bt_sb, o_sn, o_st, o_sh, l_sn,
-                    l_st, l_sh}))
-        return fail(DCP_ERR_INVALID_ARG, "%s: negative stride or one above 2^52 elements", who);
-    const int64_t rb = (int64_t)D * 2;
-    const Pool pk{k_pages, k_sn, k_sp, k_st, k_sh}, pv{v_pages, v_sn, v_sp, v_st, v_sh};
-    View vq = View(q, rb).dim(T, q_st * 2).dim(H, q_sh * 2);
-    View kp = pk.view(N, num_pages, page_size, Hkv, D), vp = pv.view(N, num_pages, page_size, Hkv, D);
-    View vo = View(o, rb).dim(N, o_sn * 2).dim(T, o_st * 2).dim(H, o_sh * 2);
-    View vl = View(lse, 4).dim(N, l_sn * 4).dim(T, l_st * 4).dim(H, l_sh * 4);
-    View qs = View(query_start, 4).dim((int64_t)B + 1, 4), sl = View(seq_lens, 4).dim(B, 4);
-    View bt = View(block_table, 4).dim(N, bt_sn * 4).dim(B, bt_sb * 4).dim(max_pages, 4);
-    if (!all_fit({&vq, &kp, &vp, &vo, &vl, &bt}))
-        return fail(DCP_ERR_INVALID_ARG, "%s: an operand's strides span more than 2^56 bytes", who);
-    if (vq.align() < 16 || kp.align() < 16 || vp.align() < 16 || vo.align() < 16)
-        return fail(DCP_ERR_MISALIGNED, "%s: q, o and page rows must start on 16-byte boundaries", who);
-    if ((uintptr_t)lse % 4 || (uintptr_t)block_table % 4 || (uintptr_t)query_start % 4 || (uintptr_t)seq_lens % 4)
-        return fail(DCP_ERR_MISALIGNED, "%s: pointer not aligned to its element type", who);
-    for (const View* out : {&vo, &vl})
-        if (any_overlap(*out, {&vq, &kp, &vp, &qs, &sl, &bt}))
-            return fail(DCP_ERR_ALIAS, "%s: an output overlaps an input", who);
-    if (overlap(vo, vl) || !vo.rows_disjoint() || !vl.rows_disjoint())
-        return fail(DCP_ERR_ALIAS, "%s: outputs overlap", who);
-    const size_t need = chunk_attention_workspace(N, B, T, H, Hkv, D, max_seq_len);
-    if (!workspace || workspace_bytes < need)
-        return fail(DCP_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed (%zu given)", who, need,
-                    workspace ? workspace_bytes : (size_t)0);
-    if ((uintptr_t)workspace % 16) return fail(DCP_ERR_MISALIGNED, "%s: workspace not 16-byte aligned", who);
-    if (any_overlap(View(workspace, (int64_t)need), {&vq, &kp, &vp, &vo, &vl, &qs, &sl, &bt}))
-        return fail(DCP_ERR_ALIAS, "%s: workspace overlaps an operand", who);
-    ChunkParams p;
-    fill_batch(p, N, B, T, H, Hkv, D, max_seq_len, page_size, num_pages, block_table, bt_sn, bt_sb, query_start,
-               seq_lens, pk, pv);
-    p.causal = causal != 0;
-    p.base2 = lse_base == DCP_LSE_BASE_2;
-    p.sm_scale = sm_scale;
-    p.q = (const unsigned char*)q; p.q_st = q_st * 2; p.q_sh = q_sh * 2;
-    p.o = (unsigned char*)o; p.o_sn = o_sn * 2; p.o_st = o_st * 2; p.o_sh = o_sh * 2;
-    p.lse = lse; p.l_sn = l_sn; p.l_st = l_st; p.l_sh = l_sh;
-    p.ws = (unsigned char*)workspace;
-    return launched(launch_chunk_attention(p, dtype, (cudaStream_t)stream), who);
+    return attend("dcp_extend_attention_paged", dtype, N, B, T, H, Hkv, D, q, q_st, q_sh,
+                  Pool{k_pages, k_sn, k_sp, k_st, k_sh}, Pool{v_pages, v_sn, v_sp, v_st, v_sh}, num_pages, page_size,
+                  block_table, bt_sn, bt_sb, max_pages, query_start, seq_lens, max_seq_len, 0, nullptr, nullptr,
+                  sm_scale, causal, o, o_sn, o_st, o_sh, lse, l_sn, l_st, l_sh, lse_base, workspace, workspace_bytes,
+                  stream);
+}
+
+size_t dcp_prefix_attention_workspace_size(int N, int B, int T, int H, int Hkv, int D, int max_seq_len, int G) {
+    if (G < 0 || dcp_extend_attention_workspace_size(N, B, T, H, Hkv, D, max_seq_len) == 0) return 0;
+    return prefix_attention_workspace(N, B, T, H, Hkv, D, max_seq_len, G);
+}
+
+dcp_status_t dcp_prefix_attention_paged(int dtype, int N, int B, int T, int H, int Hkv, int D,
+                                        const void* q, int64_t q_st, int64_t q_sh,
+                                        const void* k_pages, int64_t k_sn, int64_t k_sp, int64_t k_st, int64_t k_sh,
+                                        const void* v_pages, int64_t v_sn, int64_t v_sp, int64_t v_st, int64_t v_sh,
+                                        int num_pages, int page_size,
+                                        const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                                        const int* query_start, const int* seq_lens, int max_seq_len,
+                                        int G, const int* group_start, const int* prefix_lens,
+                                        float sm_scale, int causal,
+                                        void* o, int64_t o_sn, int64_t o_st, int64_t o_sh,
+                                        float* lse, int64_t l_sn, int64_t l_st, int64_t l_sh,
+                                        int lse_base, void* workspace, size_t workspace_bytes, void* stream) {
+    return attend("dcp_prefix_attention_paged", dtype, N, B, T, H, Hkv, D, q, q_st, q_sh,
+                  Pool{k_pages, k_sn, k_sp, k_st, k_sh}, Pool{v_pages, v_sn, v_sp, v_st, v_sh}, num_pages, page_size,
+                  block_table, bt_sn, bt_sb, max_pages, query_start, seq_lens, max_seq_len, G, group_start, prefix_lens,
+                  sm_scale, causal, o, o_sn, o_st, o_sh, lse, l_sn, l_st, l_sh, lse_base, workspace, workspace_bytes,
+                  stream);
 }
 
 dcp_status_t dcp_attention_weights_paged(int dtype, int N, int B, int T, int H, int Hkv, int D,

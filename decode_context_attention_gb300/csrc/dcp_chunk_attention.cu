@@ -44,9 +44,10 @@ struct MmaShape {
 template <typename T>
 constexpr float kWeightUnit = std::is_same<T, __half>::value ? 32768.f : 1.f;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const ChunkParams p, const ChunkPartials ws,
+template <typename T, int D, class Params>
+__global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Params p, const ChunkPartials ws,
                                                                       int tpi) {
+    constexpr bool kPlanned = std::is_same<Params, PrefixParams>::value;
     constexpr int P = MmaShape<D>::kPitch;
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char* qs = smem;
@@ -62,8 +63,9 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
     const float qscale = p.sm_scale * kLog2e;
 
     while (x.b < p.B && !(same_item(x, end) && x.tile == end.tile)) {
-        const Request q = load_request(p, x.b);
+        const auto q = load_request(p, x.b);
         const int r = x.rh / p.Hkv, hkv = x.rh % p.Hkv;
+        const int64_t table = table_at(p, q, r, x.b);
         const int j0 = x.qt * tpi;
         const int nrows = min(tpi, q.n - j0) * p.gq;
         const int ntiles = item_tiles(p, q, r, x.qt, tpi, kTile);
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
             __syncthreads();  // every warp is done with the previous tile
             for (int id = tid; id < kTile * (D / 8); id += kThreadsMma) {
                 const int row = id / (D / 8), u = id % (D / 8), i = tb + row;
-                const int pg = i < lim_last ? page_of(p, r, x.b, i) : -1;
+                const int pg = i < lim_last ? page_in(p, table, i) : -1;
                 const unsigned char *ka = p.k, *va = p.v;
                 if (pg >= 0) {
                     ka += k_offset(p, r, pg, i, hkv) + 16 * u;
@@ -215,7 +217,8 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
             const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
             if (row >= nrows) continue;
             const int t = q.start + j0 + row / p.gq, h = hkv * p.gq + row % p.gq;
-            if (whole) {
+            const int64_t kept = whole ? partial_row(p, q, r, t, h) : (int64_t)slot * kRows + row;
+            if (whole && (!kPlanned || kept < 0)) {
                 T* out = reinterpret_cast<T*>(p.o + (int64_t)r * p.o_sn + (int64_t)t * p.o_st + (int64_t)h * p.o_sh);
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
@@ -225,12 +228,12 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
                     p.lse[(int64_t)r * p.l_sn + (int64_t)t * p.l_st + (int64_t)h * p.l_sh] =
                         p.base2 ? lse2 : lse2 * kLn2;
             } else {
-                float* out = ws.o + ((int64_t)slot * kRows + row) * D;
+                float* out = (kPlanned && whole ? partial_o(p) : ws.o) + kept * D;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
                     *reinterpret_cast<float2*>(out + n * 8 + (lane & 3) * 2) =
                         make_float2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
-                if ((lane & 3) == 0) ws.lse[(int64_t)slot * kRows + row] = lse2;
+                if ((lane & 3) == 0) (kPlanned && whole ? partial_lse(p) : ws.lse)[kept] = lse2;
             }
         }
         __syncthreads();
@@ -243,16 +246,17 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
             const T* qrow = reinterpret_cast<const T*>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
             const int lm = visible(p, q, j0 + tid / p.gq, r);
             const int64_t at = (int64_t)r * p.l_sn + (int64_t)t * p.l_st + (int64_t)h * p.l_sh;
+            const int64_t kept = whole ? partial_row(p, q, r, t, h) : (int64_t)slot * kRows + tid;
             for (int i = 0; i < 4; ++i) {
-                if (whole)
-                    add_nonfinite<T, T>(p, r, x.b, hkv, qrow, (mtile + i) * kTile, poison[i], 2, lm,
+                if (whole && (!kPlanned || kept < 0))
+                    add_nonfinite<T, T>(p, r, table, hkv, qrow, (mtile + i) * kTile, poison[i], 2, lm,
                                         p.base2 ? p.lse[at] : p.lse[at] * kLog2e,
                                         reinterpret_cast<T*>(p.o + (int64_t)r * p.o_sn + (int64_t)t * p.o_st +
                                                              (int64_t)h * p.o_sh));
                 else
-                    add_nonfinite<T, float>(p, r, x.b, hkv, qrow, (mtile + i) * kTile, poison[i], 2, lm,
-                                            ws.lse[(int64_t)slot * kRows + tid],
-                                            ws.o + ((int64_t)slot * kRows + tid) * D);
+                    add_nonfinite<T, float>(p, r, table, hkv, qrow, (mtile + i) * kTile, poison[i], 2, lm,
+                                            (kPlanned && whole ? partial_lse(p) : ws.lse)[kept],
+                                            (kPlanned && whole ? partial_o(p) : ws.o) + kept * D);
             }
         }
         if (cut) break;
@@ -262,21 +266,25 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Chun
 
 int mma_ctas(int D) { return device_sm_count() * (D == 256 ? 2 : 3); }
 
-template <typename T, int D>
-cudaError_t launch_mma(const ChunkParams& p, int dtype, cudaStream_t stream) {
+template <typename T, int D, class Params>
+cudaError_t launch_mma(const Params& p, int dtype, cudaStream_t stream) {
     const int ctas = mma_ctas(D), tpi = kRows / p.gq;
     const ChunkPartials ws = chunk_partials_in(p.ws, ctas, kRows, D);
     constexpr int smem = MmaShape<D>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(chunk_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const auto kernel = chunk_attention_kernel<T, D, Params>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    chunk_attention_kernel<T, D><<<ctas, kThreadsMma, smem, stream>>>(p, ws, tpi);
+    kernel<<<ctas, kThreadsMma, smem, stream>>>(p, ws, tpi);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge(p, ws, tpi, kTile, kRows, ctas, dtype, stream);
+    if constexpr (std::is_same<Params, PrefixParams>::value)
+        return launch_prefix_join(p, ws, tpi, kRows, ctas, dtype, stream);
+    else
+        return launch_chunk_merge(p, ws, tpi, kTile, kRows, ctas, dtype, stream);
 }
 
-template <typename T>
-cudaError_t launch_mma_d(const ChunkParams& p, int dtype, cudaStream_t stream) {
+template <typename T, class Params>
+cudaError_t launch_mma_d(const Params& p, int dtype, cudaStream_t stream) {
     switch (p.D) {
         case 64: return launch_mma<T, 64>(p, dtype, stream);
         case 128: return launch_mma<T, 128>(p, dtype, stream);
@@ -295,6 +303,12 @@ size_t chunk_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int
 cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t stream) {
     cudaError_t e;
     if (launch_chunk_attention_tc(p, dtype, stream, &e)) return e;
+    return dtype == DCP_F16 ? launch_mma_d<__half>(p, dtype, stream) : launch_mma_d<__nv_bfloat16>(p, dtype, stream);
+}
+
+cudaError_t launch_planned_attention(const PrefixParams& p, int dtype, cudaStream_t stream) {
+    cudaError_t e;
+    if (launch_planned_attention_tc(p, dtype, stream, &e)) return e;
     return dtype == DCP_F16 ? launch_mma_d<__half>(p, dtype, stream) : launch_mma_d<__nv_bfloat16>(p, dtype, stream);
 }
 

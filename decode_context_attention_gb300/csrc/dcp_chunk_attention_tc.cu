@@ -135,13 +135,36 @@ __device__ __forceinline__ int4 ld_shared4(const int4* at) {
                  : "r"(smem_u32(at)));
     return x;
 }
-__device__ __forceinline__ ChunkSeg read_seg(const int4* at) {
+// A part as warp 11 hands it out.  A plan's part also says its kind (above the rank, which has
+// 12 bits) and where its table entries begin.
+template <class Params>
+__device__ __forceinline__ void write_seg(int4* at, const ChunkSegFor<Params>& g) {
+    int r = g.r, lo = 0, hi = 0;
+    if constexpr (std::is_same<Params, PrefixParams>::value) {
+        if (g.b >= 0) r |= g.q.kind << 16;
+        lo = (int)(uint32_t)g.table;
+        hi = (int)(g.table >> 32);
+    }
+    at[0] = make_int4(g.b, r, g.hkv, g.row0);
+    at[1] = make_int4(g.nrows, g.j0, g.t0, g.t1);
+    at[2] = make_int4(g.lim0, g.lim_last, g.slot, g.q.n);
+    at[3] = make_int4(g.q.L, g.q.start, lo, hi);
+}
+template <class Params>
+__device__ __forceinline__ ChunkSegFor<Params> read_seg(const Params& p, const int4* at) {
     const int4 a = ld_shared4(at), b = ld_shared4(at + 1), c = ld_shared4(at + 2), d = ld_shared4(at + 3);
-    ChunkSeg s;
+    ChunkSegFor<Params> s;
     s.b = a.x; s.r = a.y; s.hkv = a.z; s.row0 = a.w;
     s.nrows = b.x; s.j0 = b.y; s.t0 = b.z; s.t1 = b.w;
     s.lim0 = c.x; s.lim_last = c.y; s.slot = c.z; s.q.n = c.w;
     s.q.L = d.x; s.q.start = d.y;
+    if constexpr (std::is_same<Params, PrefixParams>::value) {
+        s.r = a.y & 0xffff;
+        s.q.kind = a.y >> 16;
+        s.table = (int64_t)((uint64_t)(uint32_t)d.w << 32 | (uint32_t)d.z);
+    } else {
+        s.table = table_at(p, s.q, s.r, s.b);
+    }
     return s;
 }
 // P of the 32 scores v[OFF ..], 2^(s qscale + off), as 16 columns of pairs at tP; its sum is added to l2.
@@ -195,12 +218,14 @@ __device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volat
     return mbar_try_wait(bar, parity) || wait_long(bar, parity, state);
 }
 
-template <typename T, int D>
+template <typename T, int D, class Params>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     chunk_attention_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                              const __grid_constant__ CUtensorMap vmap, const ChunkParams p, const ChunkPartials ws,
+                              const __grid_constant__ CUtensorMap vmap, const Params p, const ChunkPartials ws,
                               const int tpi) {
     using S = TcShape<D>;
+    using ChunkSeg = ChunkSegFor<Params>;
+    constexpr bool kPlanned = std::is_same<Params, PrefixParams>::value;
     constexpr int kSlots = S::kSlots, kTileBytes = S::kTileBytes;
     constexpr int NCH = D / 64;
     extern __shared__ uint8_t smem_raw[];
@@ -256,7 +281,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     auto get_seg = [&](int k, ChunkSeg* g) -> bool {
         if (!__all_sync(kAllLanes, mbar_wait(&bar->seg_full[k % kSegs], (k / kSegs) & 1, status, DCP_ERR_TIMEOUT, abort)))
             return false;
-        *g = read_seg(bar->seg[k % kSegs]);
+        *g = read_seg(p, bar->seg[k % kSegs]);
         return g->b >= 0;
     };
     auto release_seg = [&](int k) {
@@ -298,8 +323,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const int nseg = (min(kTT, g.lim_last - tb) + pb - 1) / pb;
                     int pg = 0;
                     if (lane < nseg) {  // entries of tokens that exist only
-                        pg = __ldg(p.bt + (int64_t)g.r * p.bt_sn + (int64_t)g.b * p.bt_sb +
-                                   ((tb + lane * pb) >> p.page_shift));
+                        pg = __ldg(p.bt + g.table + ((tb + lane * pb) >> p.page_shift));
                         if ((unsigned)pg >= (unsigned)p.num_pages) pg = p.num_pages;  // reads zeros
                     }
                     int go = 1;
@@ -525,11 +549,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     ok = __all_sync(kAllLanes, wait_part(&bar->seg_empty[k % kSegs], (k / kSegs - 1) & 1, abort));
                 if (!ok) break;
                 if (lane == 0) {
-                    int4* at = bar->seg[k % kSegs];
-                    at[0] = make_int4(g.b, g.r, g.hkv, g.row0);
-                    at[1] = make_int4(g.nrows, g.j0, g.t0, g.t1);
-                    at[2] = make_int4(g.lim0, g.lim_last, g.slot, g.q.n);
-                    at[3] = make_int4(g.q.L, g.q.start, 0, 0);
+                    write_seg<Params>(bar->seg[k % kSegs], g);
                     mbar_arrive(&bar->seg_full[k % kSegs]);
                 }
                 __syncwarp();
@@ -683,7 +703,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             // the item again, for where its rows go: held through the tiles it would take
             // the registers of their scores
-            const ChunkSeg g = read_seg(bar->seg[seg % kSegs]);
+            const ChunkSeg g = read_seg(p, bar->seg[seg % kSegs]);
             const int row = (pair ? u * rblk : 0) + m;  // row of the item
             const bool valid = m < rblk && row < g.nrows;
             const int tok = (pair ? u * tj : 0) + mtok;
@@ -695,7 +715,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const int64_t t = g.row0 + tok;
             if (writes) {
                 unsigned char* orow = p.o + (int64_t)g.r * p.o_sn + t * p.o_st + (int64_t)h * p.o_sh;
-                const int64_t prow = (int64_t)g.slot * (2 * kM) + row;
+                // fp32 rows: of a cut item, and of a plan's parts, which are joined later
+                int64_t prow = (int64_t)g.slot * (2 * kM) + row;
+                float *part_o = ws.o, *part_lse = ws.lse;
+                bool partial = g.slot >= 0;
+                if constexpr (kPlanned) {
+                    const int64_t at = partial_row(p, g.q, g.r, t, h);
+                    if (!partial && at >= 0) {
+                        prow = at;
+                        part_o = partial_o(p);
+                        part_lse = partial_lse(p);
+                        partial = true;
+                    }
+                }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -723,7 +755,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = 0u;
                         }
-                        if (g.slot < 0) {
+                        if (!partial) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 uint32_t w[4];
@@ -736,17 +768,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         } else {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4*>(ws.o + prow * D + 32 * c + 4 * e) =
+                                *reinterpret_cast<uint4*>(part_o + prow * D + 32 * c + 4 * e) =
                                     make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     }
                     __syncwarp();
                 }
                 if (valid) {
-                    if (g.slot < 0)
+                    if (!partial)
                         p.lse[(int64_t)g.r * p.l_sn + t * p.l_st + (int64_t)h * p.l_sh] = p.base2 ? lse2 : lse2 * kLn2;
                     else
-                        ws.lse[prow] = lse2;
+                        part_lse[prow] = lse2;
                     // what the zeroed values of masked tiles give to the rows that do see them
                     const int mt0 = g.lim0 / kTT;
                     if (g.lim0 < g.lim_last && g.t1 > mt0) {
@@ -757,14 +789,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         if (any) {
                             const T* qrow = reinterpret_cast<const T*>(p.q + t * p.q_st + (int64_t)h * p.q_sh);
                             for (int e = 0; e < 3; ++e) {
-                                if (g.slot < 0)
-                                    add_nonfinite<T, T>(p, g.r, g.b, g.hkv, qrow, (mt0 + e) * kTT,
+                                if (!partial)
+                                    add_nonfinite<T, T>(p, g.r, g.table, g.hkv, qrow, (mt0 + e) * kTT,
                                                         (const unsigned*)mask + 4 * e, 4, lim, lse2,
                                                         reinterpret_cast<T*>(orow));
                                 else
-                                    add_nonfinite<T, float>(p, g.r, g.b, g.hkv, qrow, (mt0 + e) * kTT,
+                                    add_nonfinite<T, float>(p, g.r, g.table, g.hkv, qrow, (mt0 + e) * kTT,
                                                             (const unsigned*)mask + 4 * e, 4, lim, lse2,
-                                                            ws.o + prow * D);
+                                                            part_o + prow * D);
                             }
                         }
                     }
@@ -795,28 +827,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_tc(const ChunkParams& p, const CUtensorMap (&maps)[3], int dtype, cudaStream_t stream) {
+template <typename T, int D, class Params>
+cudaError_t launch_tc(const Params& p, const CUtensorMap (&maps)[3], int dtype, cudaStream_t stream) {
     const int ctas = device_sm_count(), tpi = 2 * (kM / p.gq);
     const ChunkPartials ws = chunk_partials_in(p.ws, ctas, 2 * kM, D);
-    const void* k = (const void*)chunk_attention_tc_kernel<T, D>;
+    const auto kernel = chunk_attention_tc_kernel<T, D, Params>;
     // the shared-memory opt-in is a per-device function attribute
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
     if (e != cudaSuccess) return e;
-    chunk_attention_tc_kernel<T, D>
-        <<<ctas, kThreadsTc, TcShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, ws, tpi);
+    kernel<<<ctas, kThreadsTc, TcShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, ws, tpi);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge(p, ws, tpi, kTT, 2 * kM, ctas, dtype, stream);
+    if constexpr (std::is_same<Params, PrefixParams>::value)
+        return launch_prefix_join(p, ws, tpi, 2 * kM, ctas, dtype, stream);
+    else
+        return launch_chunk_merge(p, ws, tpi, kTT, 2 * kM, ctas, dtype, stream);
 }
 
-}  // namespace
-
-size_t chunk_attention_tc_workspace(int D) {
-    return D == 64 || D == 128 ? chunk_partials_bytes(device_sm_count(), 2 * kM, D) : 0;
-}
-
-bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
+template <class Params>
+bool launch_tc_any(const Params& p, int dtype, cudaStream_t stream, cudaError_t* err) {
     // the maximum of the scaled scores is that of the scores for a positive scale
     // only; boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one
     // takes 199 against 326 us (drafts), 144 against 358 (mixed, D = 64), 353 against
@@ -856,7 +885,7 @@ bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t str
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;  // strides a tensor map cannot describe: the register-tiled kernel takes it
     }
-    ChunkParams q = p;
+    Params q = p;
     // DCP_TEST_STALL_LOADS=1 (tests of the failure path only): no loads are
     // issued, so the first wait on them runs out.  Unset in normal use.
     const char* stall = getenv("DCP_TEST_STALL_LOADS");
@@ -868,6 +897,19 @@ bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t str
         *err = dtype == DCP_F16 ? launch_tc<__half, 64>(q, maps, dtype, stream)
                                 : launch_tc<__nv_bfloat16, 64>(q, maps, dtype, stream);
     return true;
+}
+
+}  // namespace
+
+size_t chunk_attention_tc_workspace(int D) {
+    return D == 64 || D == 128 ? chunk_partials_bytes(device_sm_count(), 2 * kM, D) : 0;
+}
+
+bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
+    return launch_tc_any(p, dtype, stream, err);
+}
+bool launch_planned_attention_tc(const PrefixParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
+    return launch_tc_any(p, dtype, stream, err);
 }
 
 int chunk_attention_tc_status(bool clear) {

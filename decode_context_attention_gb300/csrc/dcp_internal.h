@@ -141,6 +141,19 @@ struct ChunkParams {
     int stall_loads;                     // test of the bounded waits (tensor-core paths): no loads issued
 };
 
+// The chunk attention of a batch whose requests share prefixes: a batch of `groups`
+// common parts, then of every request's own part (B of both), as the plan lays them
+// out.  Parts that are joined afterwards leave fp32 rows.
+struct PrefixParams : ChunkParams {
+    int requests, groups;
+    const int* group_start;              // [groups + 1]
+    const int* prefix_lens;              // [groups]
+    int max_pages;
+    int4* plan;                          // [B][2]
+    float* wo;                           // [2][N][T][H][D]: common, own
+    float* wl;                           // [2][N][T][H], base 2
+};
+
 struct AppendParams {
     ChunkParams c;                       // q, the pages and the batch
     int rot, interleaved, num_positions;
@@ -236,6 +249,12 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t
 // describe): false without launching anything otherwise.
 size_t chunk_attention_tc_workspace(int D);
 bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
+// The same kernels over the plan of a batch that shares prefixes (p.ws: their partials), and
+// the plan and the join around them.
+cudaError_t launch_planned_attention(const PrefixParams& p, int dtype, cudaStream_t stream);
+bool launch_planned_attention_tc(const PrefixParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
+size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len, int G);
+cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stream);
 int chunk_attention_tc_status(bool clear);
 cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t stream);
 bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);

@@ -22,7 +22,7 @@
  *
  *   dcp_qk_norm_rope_append, dcp_extend_attention_paged,
  *   dcp_attention_weights_paged, dcp_cache_evict_paged,
- *   dcp_page_reserve, dcp_page_release
+ *   dcp_page_reserve, dcp_page_release, dcp_prefix_attention_paged
  *
  * The cross-rank exchange itself (NCCL all-to-all, MNNVL, all-gather /
  * all-reduce) is not part of this library.  A group's N ranks can be held as
@@ -498,6 +498,43 @@ dcp_status_t dcp_extend_attention_paged(int dtype, int N, int B, int T, int H, i
                                         int num_pages, int page_size,
                                         const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
                                         const int* query_start, const int* seq_lens, int max_seq_len,
+                                        float sm_scale, int causal,
+                                        void* o, int64_t o_sn, int64_t o_st, int64_t o_sh,
+                                        float* lse, int64_t l_sn, int64_t l_st, int64_t l_sh,
+                                        int lse_base, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dcp_prefix_attention_paged -- dcp_extend_attention_paged for a batch whose
+ * requests share prefixes: the same results, with the keys and values of a common
+ * prefix read once for all the requests of its group.  (sglang PR #34213 report,
+ * "功能与动机": partials over disjoint tokens joined by their log-sum-exps, there of
+ * ranks; here also of a prefix and what follows it.)
+ *
+ * Groups as for dcp_page_reserve: requests group_start[g] <= b < group_start[g + 1]
+ * have their first prefix_lens[g] tokens in common, and their table entries of the
+ * whole pages of it, S_g = floor(prefix_lens[g] / (N * page_size)) on every rank, name
+ * pages that hold the same keys and values (the group's first request's entries are
+ * read for all).  Requests outside of groups are attended as they are.  A group
+ * shares no more than every new token of it sees: when one of its requests has fewer
+ * than S_g * N * page_size tokens before its new ones (causal; or in all, not
+ * causal), the common part ends at the last whole page before that.
+ *
+ *   group_start [G + 1], prefix_lens [G] int32 (device), group_start non-decreasing;
+ *           G = 0 makes this dcp_extend_attention_paged
+ * `workspace` of at least dcp_prefix_attention_workspace_size(...) bytes: beside that
+ * of dcp_extend_attention_paged 8 * N * T * H * (D + 1) bytes for the fp32 rows that
+ * are joined.  Everything else as for dcp_extend_attention_paged.
+ */
+size_t dcp_prefix_attention_workspace_size(int N, int B, int T, int H, int Hkv, int D, int max_seq_len, int G);
+
+dcp_status_t dcp_prefix_attention_paged(int dtype, int N, int B, int T, int H, int Hkv, int D,
+                                        const void* q, int64_t q_st, int64_t q_sh,
+                                        const void* k_pages, int64_t k_sn, int64_t k_sp, int64_t k_st, int64_t k_sh,
+                                        const void* v_pages, int64_t v_sn, int64_t v_sp, int64_t v_st, int64_t v_sh,
+                                        int num_pages, int page_size,
+                                        const int* block_table, int64_t bt_sn, int64_t bt_sb, int max_pages,
+                                        const int* query_start, const int* seq_lens, int max_seq_len,
+                                        int G, const int* group_start, const int* prefix_lens,
                                         float sm_scale, int causal,
                                         void* o, int64_t o_sn, int64_t o_st, int64_t o_sh,
                                         float* lse, int64_t l_sn, int64_t l_st, int64_t l_sh,
