@@ -45,12 +45,15 @@ template <>
 struct RequestOf<PrefixParams> {
     using type = Planned;
 };
-__device__ __forceinline__ Planned load_request(const PrefixParams& p, int v) {
-    const int4 a = __ldg(p.plan + 2 * (int64_t)v), b = __ldg(p.plan + 2 * (int64_t)v + 1);
+__device__ __forceinline__ Planned load_planned(const int4* at) {
+    const int4 a = __ldg(at), b = __ldg(at + 1);
     Planned q;
     q.start = a.x; q.n = a.y; q.L = a.z; q.b = a.w;
     q.first = b.x; q.kind = b.y; q.common = b.z;
     return q;
+}
+__device__ __forceinline__ Planned load_request(const PrefixParams& p, int v) {
+    return load_planned(p.plan + 2 * (int64_t)v);
 }
 __device__ __forceinline__ bool is_causal(const ChunkParams& p, const Request&) { return p.causal != 0; }
 __device__ __forceinline__ bool is_causal(const PrefixParams& p, const Planned& q) {
@@ -377,9 +380,12 @@ ChunkPartials chunk_partials_in(unsigned char* ws, int ctas, int rows, int D);
 cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int tt, int rows, int ctas,
                                int dtype, cudaStream_t stream);
 
-// The same for a batch that shares prefixes, with its common and own parts.
-cudaError_t launch_prefix_join(const PrefixParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
-                               cudaStream_t stream);
+// For a batch that shares prefixes: which own parts are slim, and what follows the chunk
+// kernel (rows of an item: tpi tokens x gq heads, at most `rows`): slim parts, and the
+// join of common and own parts.
+void slim_limits(PrefixParams& p);
+cudaError_t launch_prefix_finish(const PrefixParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
+                                 cudaStream_t stream);
 
 // Where the row of a part goes in fp32 when it is not the whole result: the slot of a
 // cut item, else the plan's row of a part that is joined; -1: the output itself.

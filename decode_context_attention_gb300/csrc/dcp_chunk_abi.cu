@@ -106,9 +106,9 @@ dcp_status_t attend(const char* who, int dtype, int N, int B, int T, int H, int 
     if (!finite(sm_scale)) return fail(DCP_ERR_INVALID_ARG, "%s: sm_scale is not finite", who);
     if (lse_base != DCP_LSE_BASE_E && lse_base != DCP_LSE_BASE_2)
         return fail(DCP_ERR_INVALID_ARG, "%s: lse_base %d", who, lse_base);
-    // the plan's requests are counted in 32 bits, too
-    if (G < 0 || (int64_t)N * ((int64_t)G + B) * Hkv >= (1ll << 31) || (int64_t)G + B >= (1 << 30))
-        return fail(DCP_ERR_INVALID_ARG, "%s: G=%d (N * (G + B) * Hkv below 2^31)", who, G);
+    // the plan's (request, rank, head) triples are counted in 32 bits, too
+    if (G < 0 || (G && (int64_t)N * ((int64_t)G + B) * Hkv >= (1ll << 30)))
+        return fail(DCP_ERR_INVALID_ARG, "%s: G=%d (N * (G + B) * Hkv below 2^30)", who, G);
     if (B == 0 || T == 0) return ok();
     if (!q || !pk.p || !pv.p || !block_table || !query_start || !seq_lens || !o || !lse ||
         (G && (!group_start || !prefix_lens)))

@@ -48,6 +48,7 @@ template <typename T, int D, class Params>
 __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Params p, const ChunkPartials ws,
                                                                       int tpi) {
     constexpr bool kPlanned = std::is_same<Params, PrefixParams>::value;
+    if constexpr (kPlanned) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int P = MmaShape<D>::kPitch;
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char* qs = smem;
@@ -278,7 +279,7 @@ cudaError_t launch_mma(const Params& p, int dtype, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if constexpr (std::is_same<Params, PrefixParams>::value)
-        return launch_prefix_join(p, ws, tpi, kRows, ctas, dtype, stream);
+        return launch_prefix_finish(p, ws, tpi, kRows, ctas, dtype, stream);
     else
         return launch_chunk_merge(p, ws, tpi, kTile, kRows, ctas, dtype, stream);
 }

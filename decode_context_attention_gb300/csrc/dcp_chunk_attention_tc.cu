@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint8_t* ring = smem + 2 * kTileBytes;
     TcBars* bar = reinterpret_cast<TcBars*>(ring + kSlots * kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // what follows a plan's parts starts on the SMs that are done
+    if constexpr (kPlanned) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tj = tpi / 2;        // new tokens of a row block
     const int rblk = tj * p.gq;    // its rows (at most 128)
 
@@ -839,7 +841,7 @@ cudaError_t launch_tc(const Params& p, const CUtensorMap (&maps)[3], int dtype, 
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if constexpr (std::is_same<Params, PrefixParams>::value)
-        return launch_prefix_join(p, ws, tpi, 2 * kM, ctas, dtype, stream);
+        return launch_prefix_finish(p, ws, tpi, 2 * kM, ctas, dtype, stream);
     else
         return launch_chunk_merge(p, ws, tpi, kTT, 2 * kM, ctas, dtype, stream);
 }

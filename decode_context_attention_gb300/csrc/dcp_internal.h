@@ -150,6 +150,10 @@ struct PrefixParams : ChunkParams {
     const int* prefix_lens;              // [groups]
     int max_pages;
     int4* plan;                          // [B][2]
+    int4* slim;                          // [requests][2]: own parts of few rows and tokens, which the plan leaves out
+    int* wide;                           // [plan_ctas]: whether a CTA of the plan has put own parts into it
+    int plan_ctas, plan_tpi;             // plan_tpi: new tokens of a block of rows
+    int slim_rows, slim_tokens;          // limits of a slim part
     float* wo;                           // [2][N][T][H][D]: common, own
     float* wl;                           // [2][N][T][H], base 2
 };

@@ -513,11 +513,13 @@ dcp_status_t dcp_extend_attention_paged(int dtype, int N, int B, int T, int H, i
  * Groups as for dcp_page_reserve: requests group_start[g] <= b < group_start[g + 1]
  * have their first prefix_lens[g] tokens in common, and their table entries of the
  * whole pages of it, S_g = floor(prefix_lens[g] / (N * page_size)) on every rank, name
- * pages that hold the same keys and values (the group's first request's entries are
- * read for all).  Requests outside of groups are attended as they are.  A group
- * shares no more than every new token of it sees: when one of its requests has fewer
- * than S_g * N * page_size tokens before its new ones (causal; or in all, not
- * causal), the common part ends at the last whole page before that.
+ * pages that hold the same keys and values.  Whose entries are read is not said: a
+ * common part is attended once for all where that is less work than each request's on
+ * its own (prompts' chunks, which read every tile for many rows, gain nothing).
+ * Requests outside of groups are attended as they are.  A group shares no more than
+ * every new token of it sees: when one of its requests has fewer than
+ * S_g * N * page_size tokens before its new ones (causal; or in all, not causal), the
+ * common part ends at the last whole page before that.
  *
  *   group_start [G + 1], prefix_lens [G] int32 (device), group_start non-decreasing;
  *           G = 0 makes this dcp_extend_attention_paged

@@ -44,7 +44,7 @@ class Shared(Batch):
                 for r in range(self.N):
                     if self.own_entries == "first":
                         self.block_table[r, b, :e] = self.block_table[r, lo, :e]
-                    elif self.own_entries == "bad":      # the first request's are read for all
+                    elif self.own_entries == "bad":      # no pages at all
                         self.block_table[r, b, :e] = -5
 
     def scores(self, b, r, h):
@@ -107,6 +107,37 @@ CASES = {
     "padding and strides": ([(1, 300), (3, 290), (1, 280)], [(0, 3, 270)], {"pad": 3, "strided": True}),
     "more than a block of rows": ([(1, 70 + b % 9) for b in range(150)], [(0, 150, 64)], {"H": 4, "Hkv": 2}),
     "chunks": ([(150, 420), (90, 380), (133, 500), (1, 300)], [(0, 4, 290)], {}),
+    # groups of enough requests and tokens for a common part of their own
+    "many": ([(1, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], {}),
+    "many, drafts": ([(1 + b % 4, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], {}),
+    "many, of two and of three row blocks": ([(b % 3 + 6, 700 + 3 * b) for b in range(12)], [(0, 12, 690)], {}),
+    "many, of four row blocks": ([(9 + b % 8, 700 + 3 * b) for b in range(12)], [(0, 12, 640)], {}),
+    "many, and wide ones": ([(1 + 16 * (b % 2), 1700 + 3 * b) for b in range(12)], [(0, 12, 1660)], {}),
+    "many, all wide": ([(17 + b, 2100 + 3 * b) for b in range(9)], [(0, 9, 2048)], {}),
+    "many, one rank": ([(1, 500 + 3 * b) for b in range(20)], [(0, 20, 490)], {"N": 1}),
+    "many, three ranks, loose ones": ([(1, 30)] + [(2, 900 + 3 * b) for b in range(20)] + [(1, 800), (70, 200)],
+                                      [(1, 21, 890)], {"N": 3}),
+    "many, D 64": ([(1 + b % 3, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], {"D": 64}),
+    "many, D 256": ([(1 + b % 3, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], {"D": 256}),
+    "many, D 256, 32 rows and more": ([(7 + b % 3, 900 + 3 * b) for b in range(14)], [(0, 14, 890)], {"D": 256}),
+    "many, D 256, cut": ([(1, 4100 + b) for b in range(8)], [(0, 8, 4096)], {"D": 256, "N": 1, "H": 4, "Hkv": 1}),
+    "many, a head each": ([(1 + b % 5, 900 + 3 * b) for b in range(20)], [(0, 20, 880)], {"H": 3, "Hkv": 3}),
+    "many, 64 tokens of a head each": ([(60 + b % 5, 1900 + 3 * b) for b in range(12)], [(0, 12, 1700)],
+                                       {"H": 2, "Hkv": 2, "N": 1}),
+    "many, five heads a group": ([(1 + b % 3, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], {"H": 5, "Hkv": 1}),
+    "many, 64 heads a group": ([(1, 700 + 3 * b) for b in range(12)], [(0, 12, 690)], {"H": 64, "Hkv": 1}),
+    "many, pages of four": ([(1 + b % 2, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], {"page": 4}),
+    "many, pages of one": ([(1 + b % 2, 400 + 3 * b) for b in range(20)], [(0, 20, 390)], {"page": 1, "Hkv": 1}),
+    "many, pages of 512": ([(1, 2500 + 3 * b) for b in range(12)], [(0, 12, 2490)], {"page": 512}),
+    "many, padding and strides": ([(1 + b % 3, 700 + 3 * b) for b in range(20)], [(0, 20, 690)],
+                                  {"pad": 3, "strided": True}),
+    "many, three groups": ([(1, 900 + 3 * b) for b in range(12)] + [(2, 640 + b) for b in range(14)]
+                           + [(1, 2000 + b) for b in range(10)], [(0, 12, 890), (12, 26, 512), (26, 36, 1999)], {}),
+    "many, a holder": ([(0, 768)] + [(1, 770 + 3 * b) for b in range(20)], [(0, 21, 768)], {}),
+    "many, cut over many CTAs": ([(1, 12100 + b) for b in range(9)], [(0, 9, 12000)],
+                                 {"H": 2, "Hkv": 1, "page": 64}),
+    "many, long own parts": ([(1, 700 + 900 * b) for b in range(9)], [(0, 9, 640)], {"H": 4, "Hkv": 1, "page": 64}),
+    "many, one shorter": ([(1, 900 + 3 * b) for b in range(19)] + [(1, 500)], [(0, 20, 880)], {}),
     "cut over many CTAs": ([(1, 12100), (1, 12050), (2, 12033)], [(0, 3, 12000)], {"H": 2, "Hkv": 1, "page": 64}),
     "cut, wide": ([(1, 9100), (1, 9050), (2, 9033)], [(0, 3, 9000)], {"H": 2, "Hkv": 1, "page": 64, "D": 256, "N": 1}),
     "own parts cut": ([(1, 9100), (1, 7050), (2, 8033)], [(0, 3, 128)], {"H": 2, "Hkv": 1, "page": 64, "N": 1}),
@@ -124,7 +155,9 @@ def test_shared_prefixes(name, dtype):
 
 
 @pytest.mark.parametrize("name", ["three groups", "a request shorter than the prefix", "a request of new tokens only",
-                                  "more new tokens than tokens", "chunks", "wide head dimension"])
+                                  "more new tokens than tokens", "chunks", "wide head dimension", "many, drafts",
+                                  "many, and wide ones", "many, D 256", "many, three ranks, loose ones",
+                                  "many, one shorter"])
 def test_not_causal_and_base_2(name):
     lens, groups, kw = CASES[name]
     bt = Shared(lens, groups, seed=5, **kw)
@@ -132,9 +165,13 @@ def test_not_causal_and_base_2(name):
     bt.check(o, lse, causal=False, base="2")
 
 
-@pytest.mark.parametrize("D", [128, 256])
-def test_the_first_requests_entries_are_read_for_all(D):
-    bt = Shared([(1, 200), (1, 190), (2, 180)], [(0, 3, 160)], own_entries="bad", D=D)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q", [1, 40])
+def test_a_large_groups_prefix_is_read_once(D, q):
+    """Members whose tables name no pages for the common part: only the first request's entries can have been read."""
+    n = 1250 if q == 1 else 6400      # (requests that fill blocks of rows alone share a longer one)
+    bt = Shared([(q if b < 24 else 1, n + 50 + 2 * b) for b in range(30)], [(0, 30, n)], own_entries="bad", D=D, H=4,
+                Hkv=2)
     o, lse = bt.run()
     bt.check(o, lse)
 
@@ -142,19 +179,25 @@ def test_the_first_requests_entries_are_read_for_all(D):
 @pytest.mark.parametrize("D", [64, 256])
 def test_negative_scale_and_large_scores(D):
     for scale, qs in ((-0.09, 1.0), (0.09, 60.0), (0.0, 1.0)):
-        bt = Shared([(1, 200), (1, 190), (2, 180)], [(0, 3, 160)], D=D, qscale=qs, dtype=torch.float16)
-        bt.scale = scale
-        o, lse = bt.run(scale=scale)
-        bt.check(o, lse)
+        for lens, groups in (([(1, 200), (1, 190), (2, 180)], [(0, 3, 160)]),
+                             ([(1 + b % 2, 700 + 3 * b) for b in range(20)], [(0, 20, 690)])):
+            bt = Shared(lens, groups, D=D, qscale=qs, dtype=torch.float16)
+            bt.scale = scale
+            o, lse = bt.run(scale=scale)
+            bt.check(o, lse)
 
 
-@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("where", ["prefix", "own", "future"])
-def test_values_that_are_not_finite(D, where):
-    bt = Shared([(2, 200), (1, 190), (3, 180)], [(0, 3, 160)], D=D, dtype=torch.float16, N=2)
-    g = {"prefix": 7, "own": 165, "future": 179}[where]
+@pytest.mark.parametrize("lens,n", [([(2, 200), (1, 190), (3, 180)], 160),
+                                    ([(2, 740), (1, 735)] * 9 + [(3, 720)], 690),
+                                    ([(2, 740), (1, 735)] * 9 + [(50, 720)], 660)])
+def test_values_that_are_not_finite(D, where, lens, n):
+    bt = Shared(lens, [(0, len(lens), n)], D=D, dtype=torch.float16, N=2)
+    last = lens[-1][1]
+    g = {"prefix": 7, "own": n + 5, "future": last - 1}[where]
     x = math.inf if where != "own" else math.nan
-    for b in range(3) if where == "prefix" else (2,):
+    for b in range(len(lens)) if where == "prefix" else (len(lens) - 1,):
         bt.v[b][g, 1, 5] = x
     bt.fill()
     o, lse = bt.run()
@@ -225,7 +268,8 @@ def test_captured_while_lengths_and_groups_change():
                                                            bt.seq_lens, bt.max_len, bt.group_start, bt.prefix_lens, *out,
                                                            bt.scale, workspace=ws)
             call2()
-    for lens, groups in ((big, [(0, 3, 600), (3, 5, 512)]),
+    for lens, groups in ((big, [(0, 3, 600), (3, 5, 512)]), ([(1, 790), (1, 780), (1, 770), (1, 765), (1, 760)],
+                                                              [(0, 5, 750), (5, 5, 0)]),
                          ([(2, 300), (1, 256), (0, 100), (1, 90), (4, 400)], [(0, 2, 256), (2, 5, 64)]),
                          ([(1, 10), (1, 20), (1, 5), (1, 1), (1, 3)], [(0, 5, 700), (5, 5, 9)])):
         x = Shared(lens, groups, max_len=800, pad=bt.T - sum(n for n, _ in lens), seed=8)
