@@ -141,8 +141,8 @@ struct ChunkParams {
     int stall_loads;                     // test of the bounded waits (tensor-core paths): no loads issued
 };
 
-// The chunk attention of a batch whose requests share prefixes: a batch of `groups`
-// common parts, then of every request's own part (B of both), as the plan lays them
+// The chunk attention of a batch whose requests share prefixes: a batch of every
+// request's own part, then of `groups` common parts (B of both), as the plan lays them
 // out.  Parts that are joined afterwards leave fp32 rows.
 struct PrefixParams : ChunkParams {
     int requests, groups;
@@ -151,9 +151,8 @@ struct PrefixParams : ChunkParams {
     int max_pages;
     int4* plan;                          // [B][2]
     int4* slim;                          // [requests][2]: own parts of few rows and tokens, which the plan leaves out
-    int* wide;                           // [plan_ctas]: whether a CTA of the plan has put own parts into it
-    int plan_ctas, plan_tpi;             // plan_tpi: new tokens of a block of rows
-    int slim_rows, slim_tokens;          // limits of a slim part
+    int plan_tpi;                        // new tokens of a block of rows
+    int slim_warps, slim_rows, slim_tokens;  // warps of a slim part, its limits
     float* wo;                           // [2][N][T][H][D]: common, own
     float* wl;                           // [2][N][T][H], base 2
 };

@@ -29,13 +29,12 @@ __device__ __forceinline__ void put(int4* at, int start, int n, int L, int b, in
     at[0] = make_int4(start, n, L, b);
     at[1] = make_int4(first, kind, common, 0);
 }
-// Request b's own part, L tokens from entry `first` on, to the one kernel or the other; whether it is a wide one.
-__device__ __forceinline__ bool put_own(const PrefixParams& p, const Request& q, int L, int b, int first, int kind,
+// Request b's own part, L tokens from entry `first` on, to the one kernel or the other.
+__device__ __forceinline__ void put_own(const PrefixParams& p, const Request& q, int L, int b, int first, int kind,
                                         int common) {
     const bool slim = q.n * p.gq <= p.slim_rows && rank_share(L, 0, p.N) <= p.slim_tokens;
-    put(p.plan + 2 * ((int64_t)p.groups + b), q.start, slim ? 0 : q.n, L, b, first, kind, common);
-    put(p.slim + 2 * (int64_t)b, q.start, slim ? q.n : 0, L, b, first, kind, common);
-    return !slim && q.n > 0;
+    put(p.plan + 2 * (int64_t)b, q.start, slim ? 0 : q.n, L, b, first, kind, p.requests + common);
+    put(p.slim + 2 * (int64_t)b, q.start, slim ? q.n : 0, L, b, first, kind, p.requests + common);
 }
 
 // One CTA a group, then CTAs for the requests outside of groups.  Every entry of the
@@ -45,16 +44,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     const ChunkParams& c = p;
     const Groups groups = {p.groups, p.group_start, p.prefix_lens, p.N, p.page_shift, p.max_seq_len, p.max_pages};
     const int tid = threadIdx.x;
-    bool wide = false;
     if ((int)blockIdx.x >= p.groups) {
         const int step = (gridDim.x - p.groups) * kPlanThreads;
         for (int b = (blockIdx.x - p.groups) * kPlanThreads + tid; b < p.requests; b += step) {
             if (group_of(groups, b) >= 0) continue;
             const Request q = load_request(c, b);
-            wide |= put_own(p, q, q.L, b, 0, kAlone, 0);
+            put_own(p, q, q.L, b, 0, kAlone, 0);
         }
-        wide = __syncthreads_or(wide);
-        if (tid == 0) p.wide[blockIdx.x] = wide;
         return;
     }
     __shared__ int least, tokens_new, blocks, slim, entries;
@@ -99,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
         if (blocks * (4 * tiles8 - 8 * 30) + 3 * tiles8 * slim <= shared * (8 * 13 + 4 * tiles8)) common = 0;
         entries = common;
         const Request x = load_request(c, min(b0, p.requests - 1)), y = load_request(c, max(b1 - 1, 0));
-        put(p.plan + 2 * (int64_t)g, x.start, common ? max(y.start + y.n - x.start, 0) : 0,
+        put(p.plan + 2 * ((int64_t)p.requests + g), x.start, common ? max(y.start + y.n - x.start, 0) : 0,
             (common << p.page_shift) * p.N, b0, 0, kCommon, 0);
     }
     __syncthreads();
@@ -108,10 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
         if (group_of(groups, b) != g) continue;
         const Request q = load_request(c, b);
         // (a request without new tokens may hold less than the common part, and asks for nothing)
-        wide |= put_own(p, q, max(q.L - tokens, 0), b, common, common ? kOwn : kAlone, g);
+        put_own(p, q, max(q.L - tokens, 0), b, common, common ? kOwn : kAlone, g);
     }
-    wide = __syncthreads_or(wide);
-    if (tid == 0) p.wide[g] = wide;
 }
 
 constexpr size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -128,7 +122,7 @@ size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, in
     const size_t parts = align256(chunk_attention_workspace(N, B, T, H, Hkv, D, max_seq_len));
     if (!G) return parts;
     const size_t rows = (size_t)2 * N * T * H;
-    return parts + align256((size_t)32 * ((size_t)G + 2 * (size_t)B)) + align256((size_t)4 * (G + plan_rest(B))) +
+    return parts + align256((size_t)32 * ((size_t)G + 2 * (size_t)B)) +
            align256(rows * D * 4) + align256(rows * 4);
 }
 
@@ -138,16 +132,13 @@ cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stre
     p.plan = reinterpret_cast<int4*>(at);
     p.slim = p.plan + 2 * ((size_t)p.groups + p.requests);
     at += align256((size_t)32 * ((size_t)p.groups + 2 * (size_t)p.requests));
-    p.plan_ctas = p.groups + plan_rest(p.requests);
-    p.wide = reinterpret_cast<int*>(at);
-    at += align256((size_t)4 * p.plan_ctas);
     const size_t rows = (size_t)2 * p.N * p.T * p.H;
     p.wo = reinterpret_cast<float*>(at);
     p.wl = reinterpret_cast<float*>(at + align256(rows * p.D * 4));
     p.B = p.groups + p.requests;
     slim_limits(p);
     p.plan_tpi = (p.D == 256 ? 64 : 2 * 128) / p.gq;
-    prefix_plan_kernel<<<p.plan_ctas, kPlanThreads, 0, stream>>>(p);
+    prefix_plan_kernel<<<p.groups + plan_rest(p.requests), kPlanThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_planned_attention(p, dtype, stream);
