@@ -613,8 +613,9 @@ dcp_status_t dcp_device_status(void) {
     const int s_gqa = dcp::attn_tc_device_status(true);
     const int s_chunk = dcp::chunk_attention_tc_status(true);
     const int s_weights = dcp::chunk_weights_tc_status(true);
+    const int s_finish = dcp::prefix_finish_status(true);
     int s = 0;
-    for (int x : {s_mla, s_gqa, s_chunk, s_weights}) s = x < 0 || s < 0 ? -1 : (s ? s : x);
+    for (int x : {s_mla, s_gqa, s_chunk, s_weights, s_finish}) s = x < 0 || s < 0 ? -1 : (s ? s : x);
     if (s < 0) return fail(DCP_ERR_CUDA, "dcp_device_status: the device status word could not be read");
     if (s) return fail((dcp_status_t)s, "dcp_device_status: a tensor-core kernel gave up on a bounded wait");
     return ok();

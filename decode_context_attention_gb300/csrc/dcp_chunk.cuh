@@ -383,7 +383,8 @@ cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, in
 // For a batch that shares prefixes: which own parts are slim, and what follows the chunk
 // kernel (rows of an item: tpi tokens x gq heads, at most `rows`): slim parts, and the
 // join of common and own parts.
-void slim_limits(PrefixParams& p);
+// (`maps`: room for two tensor maps, which the finish reads on the host.)
+void slim_limits(PrefixParams& p, int dtype, void* maps);
 cudaError_t launch_prefix_finish(const PrefixParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
                                  cudaStream_t stream);
 

@@ -153,6 +153,7 @@ struct PrefixParams : ChunkParams {
     int4* slim;                          // [requests][2]: own parts of few rows and tokens, which the plan leaves out
     int plan_tpi;                        // new tokens of a block of rows
     int slim_warps, slim_rows, slim_tokens;  // warps of a slim part, its limits
+    const void* slim_maps;               // tensor maps of the pools, on the host
     float* wo;                           // [2][N][T][H][D]: common, own
     float* wl;                           // [2][N][T][H], base 2
 };
@@ -258,6 +259,7 @@ cudaError_t launch_planned_attention(const PrefixParams& p, int dtype, cudaStrea
 bool launch_planned_attention_tc(const PrefixParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
 size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len, int G);
 cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stream);
+int prefix_finish_status(bool clear);
 int chunk_attention_tc_status(bool clear);
 cudaError_t launch_chunk_weights(const ChunkParams& p, int dtype, cudaStream_t stream);
 bool launch_chunk_weights_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);

@@ -16,6 +16,8 @@
 // A request's own part of few rows and tokens (a decode step's) is no work for the
 // tensor-core kernel, whose items cost 5 us of an SM each whatever their size: it is
 // left to the kernel of dcp_prefix_finish.cu, which joins it with its common part.
+#include <cuda.h>
+
 #include "dcp_chunk.cuh"
 #include "dcp_groups.cuh"
 
@@ -136,7 +138,8 @@ cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stre
     p.wo = reinterpret_cast<float*>(at);
     p.wl = reinterpret_cast<float*>(at + align256(rows * p.D * 4));
     p.B = p.groups + p.requests;
-    slim_limits(p);
+    CUtensorMap maps[2];
+    slim_limits(p, dtype, maps);
     p.plan_tpi = (p.D == 256 ? 64 : 2 * 128) / p.gq;
     prefix_plan_kernel<<<p.groups + plan_rest(p.requests), kPlanThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();

@@ -6,25 +6,33 @@
 //     z = log2 sum_i 2^z_i,  o = sum_i 2^(z_i - z) o_i.
 //
 // An own part of a decode step is a few rows (new tokens x heads of a group) over some
-// hundred tokens: 100 to 300 KB of keys and values and hardly any arithmetic.  One CTA
-// of four warps takes one (request, rank, KV head), a warp 16 rows at a time over every
-// fourth (second, or every) tile of 16 tokens.  Keys and values go from memory into the
-// registers of mma.sync's (m16n8k16) operands without a stop: the order of the elements
-// of a head's row along the products' sums is free as long as both operands have the
-// same one, so lane (g, c) takes 16 adjacent bytes of token g's key, eights of a 64-byte
-// group; and the order of the output's columns is free, so it takes 16 adjacent bytes of
-// four tokens' values and pairs them up by byte permutes.  What bounds it is the bytes in flight: a
-// warp has a tile's values under way while the scores are computed and the next tile's
-// keys while the value product is.
+// hundred tokens: 100 to 300 KB of keys and values and hardly any arithmetic, which has to
+// stream.  One to four warps take one (request, rank, KV head), 16 rows a warp, over every
+// (second, fourth) tile of 16 tokens.  TMA fills a ring of tiles in shared memory, a box a
+// page, so that a warp has two or more tiles under way and spends no instructions on them;
+// ldmatrix and mma.sync (m16n8k16) take them from there.  (The same from global memory
+// into the operands' registers, without shared memory: 60 us instead of XX for 64 single
+// tokens over 1024 of 4 ranks; a warp waited for every tile, and spent twice the
+// instructions on addresses and on pairing up values.)
 // One pass, an online softmax with the reference maximum moved when it is passed by 2^8,
-// as in the tensor-core kernel.
+// as in the tensor-core kernel.  The kernel's code has to fit the instruction cache: each
+// CTA runs through it once.
+#include <cuda.h>
+#include <stdlib.h>
+
 #include <type_traits>
 
 #include "dcp_chunk.cuh"
 #include "dcp_mma.cuh"
+#include "dcp_sm100.cuh"
 
 namespace dcp {
+
+using namespace sm100;
+
 namespace {
+
+__device__ int g_finish_status;  // first bounded wait that ran out (0 if none)
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kFinishThreads = 128;
@@ -36,15 +44,21 @@ constexpr float kGrow = 8.f;
 template <typename T>
 constexpr float kBias = std::is_same<T, __half>::value ? 7.f : 0.f;
 
+constexpr int kTileTokens = 16;
+constexpr int kMaxStages = 6;
 template <int D>
 struct Slim {
-    static constexpr int WD = D == 256 ? 2 : 1;       // warps that share a tile's columns
-    static constexpr int DW = D / WD;                 // columns of a warp
-    static constexpr int kPitch = D * 2 + 64;         // bytes of a staged query row: no bank conflicts
-    // of 16 rows: the queries, then the outputs
-    static constexpr int kRowBytes = 16 * D * 4;
-    static_assert(16 * kPitch <= kRowBytes, "queries lie where the outputs go");
-    static constexpr int kSmem = 4 / WD * kRowBytes;
+    static constexpr int WD = D == 256 ? 2 : 1;    // warps that share a tile's columns
+    static constexpr int DW = D / WD;              // columns of a warp
+    static constexpr int kBox = kTileTokens * 128;  // 64 columns of a tile, 128-byte swizzled
+    static constexpr int kTile = 2 * (D / 64) * kBox;  // keys, then values
+    static constexpr int kWarp = D == 64 ? 4 * kTile : 24 * 1024;  // of the ring, for each warp that shares it
+    static_assert(16 * D * 4 / WD <= kWarp, "outputs lie where the ring was");
+    static constexpr int kSmem = 4 * kWarp + 1024;
+};
+struct SlimBars {
+    uint64_t full[4][kMaxStages], empty[4][kMaxStages];  // by ring
+    int abort;
 };
 
 // Where the parts of a common item lie: slots of the chunk kernel's partials, or (n = -1) the plan's rows.
@@ -219,18 +233,15 @@ __device__ __forceinline__ float* out_lse(const PrefixParams& p, int r, int64_t 
 // slim own parts
 // ---------------------------------------------------------------------------
 
-// Rows of tokens that are not there, of a page outside of the pool or behind the last token.
-__device__ const uint4 g_zero_row[64] = {};
-
 __device__ __noinline__ int share_out_of_line(int n, int r, int N) { return rank_share(n, r, N); }
 
 // Item (request, rank, KV head) by 1 << wlog warps of the CTA, its group number `group`.
 template <typename T, int D>
-__device__ __forceinline__ void slim_part(const PrefixParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas,
-                                          int item, int group, int wlog, unsigned char* smem, Parts* parts) {
+__device__ __forceinline__ void slim_part(const PrefixParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                          const ChunkPartials& ws, int tpi, int rows, int ctas, int item, int group,
+                                          int wlog, uint8_t* smem, SlimBars* bars, Parts* parts) {
     using S = Slim<D>;
-    constexpr int WD = S::WD, DW = S::DW;
-    constexpr int KC = D / 32, VC = DW / 64;  // 16-byte pieces of a key and a value row that a lane takes
+    constexpr int WD = S::WD, DW = S::DW, NB = D / 64;
     __shared__ float row_m[64], row_l[64];
     __shared__ unsigned poisons[4][4];  // by group: tokens of the masked tiles whose V row is not finite
     const int wpi = 1 << wlog, threads = 32 << wlog;
@@ -249,25 +260,39 @@ __device__ __forceinline__ void slim_part(const PrefixParams& p, const ChunkPart
     auto seen = [&](int j) { return share_out_of_line(p.causal ? q.L - q.n + j + 1 : q.L, r, p.N); };
     const int lim0 = seen(0), lim_last = q.n == 1 ? lim0 : seen(q.n - 1);
     const int64_t table = table_at(p, q, r, b);
-    // row blocks (1 << rlog), and tiles between them
+    // row blocks (1 << rlog), and rings of tiles between them, each for a block's or all blocks' warps
     const int xlog = wlog - (WD - 1), wx_all = 1 << xlog;
     const int rlog = min(nrows <= 16 ? 0 : nrows <= 32 ? 1 : 2, xlog), wt = wx_all >> rlog;
     const int wd = warp >> xlog, wx = warp & (wx_all - 1), blk = wx & ((1 << rlog) - 1), first = wx >> rlog;
-    smem += group * (wx_all * S::kRowBytes);
+    const int sharers = WD << rlog, stages = min(sharers * S::kWarp / S::kTile, kMaxStages);
+    smem += group * (wpi * S::kWarp);
+    uint8_t* const ring = smem + first * (sharers * S::kWarp);
+    const int set = group * wx_all + first;
     float* const rm = row_m + group * (16 * wx_all);
     float* const rl = row_l + group * (16 * wx_all);
     unsigned* const poison = poisons[group];
-#pragma unroll 1
-    for (int id = tid; id < (16 << rlog) * (D / 8); id += threads) {
-        const int row = id / (D / 8), u = id % (D / 8);
-        const int j = row / p.gq;
-        const uint4* at = g_zero_row;
-        if (row < nrows)
-            at = reinterpret_cast<const uint4*>(p.q + (int64_t)(q.start + j) * p.q_st +
-                                                (int64_t)(hkv * p.gq + row - j * p.gq) * p.q_sh);
-        *reinterpret_cast<uint4*>(smem + row * S::kPitch + 16 * u) = __ldg(at + u);
+    if (lane == 0 && blk == 0 && wd == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&bars->full[set][i], 1);
+            mbar_init(&bars->empty[set][i], sharers);
+        }
+        fence_mbar_init();
     }
     if (tid < 4) poison[tid] = 0u;
+    // the rows' queries as A operands
+    unsigned qf[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int row = 16 * blk + g + 8 * e, j = row / p.gq;
+        const bool real = row < nrows;
+        const unsigned* at = reinterpret_cast<const unsigned*>(
+            p.q + (int64_t)(q.start + (real ? j : 0)) * p.q_st + (int64_t)(hkv * p.gq + (real ? row - j * p.gq : 0)) * p.q_sh) + c;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+            qf[x][e] = real ? __ldg(at + 8 * x) : 0u;
+            qf[x][2 + e] = real ? __ldg(at + 8 * x + 4) : 0u;
+        }
+    }
     // scores enter with the scale's sign, so that the maximum is that of the scaled ones
     const float sign = p.sm_scale < 0.f ? -1.f : 1.f, qs = fabsf(p.sm_scale) * kLog2e;
     int lim[2] = {lim0, lim0};
@@ -280,165 +305,175 @@ __device__ __forceinline__ void slim_part(const PrefixParams& p, const ChunkPart
         if (i) lim[1] = x;
         else lim[0] = x;
     }
-    // lane i (and i + 16) knows where the i-th token of a tile lies; a row's pieces are the lanes'
-    const unsigned char* const kbase = p.k + (int64_t)r * p.k_sn + (int64_t)hkv * p.k_sh;
-    const unsigned char* const vbase = p.v + (int64_t)r * p.v_sn + (int64_t)hkv * p.v_sh;
-    const unsigned char *krow, *vrow;
-    auto page_at = [&](int t) -> int {
-        const int i = t + (lane & 15);
-        return i < lim_last ? page_in(p, table, i) : -1;
+    sync();
+    const int tiles = (lim_last + kTileTokens - 1) / kTileTokens;
+    const int mine = max(tiles - first + wt - 1, 0) / wt;  // of this ring
+    const int pb = min(1 << p.page_shift, kTileTokens);    // rows of a box: a page, or a tile of one
+    const bool loads = blk == 0 && wd == 0;                // this warp fills the ring
+    volatile int* abort = &bars->abort;
+    auto token = [&](int i) { return kTileTokens * (first + i * wt); };
+    // page of the lane's box of tile i (a page outside of the pool reads zeros)
+    auto page_at = [&](int i) -> int {
+        const int t = token(i) + lane * pb;
+        if (i >= mine || lane * pb >= kTileTokens || t >= lim_last) return -1;
+        const int pg = __ldg(p.bt + table + (t >> p.page_shift));
+        return (unsigned)pg < (unsigned)p.num_pages ? pg : p.num_pages;
     };
-    auto rows_at = [&](int t, int page) {
-        const int slot = (t + (lane & 15)) & ((1 << p.page_shift) - 1);
-        const unsigned char* zero = reinterpret_cast<const unsigned char*>(g_zero_row);
-        krow = page < 0 ? zero : kbase + (int64_t)page * p.k_sp + (int64_t)slot * p.k_st;
-        vrow = page < 0 ? zero : vbase + (int64_t)page * p.v_sp + (int64_t)slot * p.v_st;
-    };
-    uint4 k[2][KC], v[4][VC];
-    auto load_k = [&]() {
+    auto load = [&](int i, int s, int page) {
+        if (lane == 0)
+            mbar_arrive_expect_tx(&bars->full[set][s],
+                                  (min(kTileTokens, lim_last - token(i)) + pb - 1) / pb * (pb * 4 * D));
+        __syncwarp();
+        if (page >= 0) {
+            uint8_t* dst = ring + s * S::kTile + lane * pb * 128;
+            const int slot = (token(i) + lane * pb) & ((1 << p.page_shift) - 1);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint4* at = reinterpret_cast<const uint4*>(shfl_ptr(krow, g + 8 * e)) + c;
-#pragma unroll
-            for (int x = 0; x < KC; ++x) k[e][x] = __ldg(at + 4 * x);
+            for (int x = 0; x < NB; ++x) {
+                tma_load_5d(dst + x * S::kBox, &kmap, &bars->full[set][s], 64 * x, hkv, slot, page, r);
+                tma_load_5d(dst + (NB + x) * S::kBox, &vmap, &bars->full[set][s], 64 * x, hkv, slot, page, r);
+            }
         }
+        __syncwarp();
     };
-    auto load_v = [&]() {
+    int issued = 0;
+    if (loads && !p.stall_loads)
+#pragma unroll 1
+        for (; issued < min(stages, mine); ++issued) load(issued, issued, page_at(issued));
+    int page = loads ? page_at(issued) : -1;  // of the next tile to be loaded
+    float o[DW / 8][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint4* at = reinterpret_cast<const uint4*>(shfl_ptr(vrow, 2 * c + (e & 1) + 8 * (e >> 1))) + DW / 8 * wd + g;
-#pragma unroll
-            for (int x = 0; x < VC; ++x) v[e][x] = __ldg(at + 8 * x);
-        }
-    };
-    float o[8 * VC][4];
-#pragma unroll
-    for (int i = 0; i < 8 * VC; ++i)
+    for (int i = 0; i < DW / 8; ++i)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
     float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int t = 16 * first;
-    rows_at(t, page_at(t));
-    load_k();
-    sync();
-    const unsigned char* qa = smem + (16 * blk + g) * S::kPitch + 16 * c;
+    bool ok = true;
+    const uint32_t k_lane = (uint32_t)(((lane & 7) + 8 * (lane >> 4)) * 128), k_xor = (uint32_t)((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+    const uint32_t v_lane = (uint32_t)((lane & 15) * 128), v_xor = (uint32_t)(((lane >> 4) ^ (lane & 7)) << 4);
+    int s = 0, phase = 0;
 #pragma unroll 1
-    while (t < lim_last) {
-        load_v();
-        const int next = t + 16 * wt;
-        const int page = page_at(next);
-        float s[2][4] = {};
+    for (int i = 0; i < mine; ++i) {
+        ok = __all_sync(kAll, mbar_wait(&bars->full[set][s], phase, &g_finish_status, DCP_ERR_TIMEOUT, abort));
+        if (!ok) break;
+        const int t = token(i);
+        uint8_t* tile = ring + s * S::kTile;
+        const uint32_t kt = smem_u32(tile), vt = kt + (NB + DW / 64 * wd) * S::kBox;
+        float x[2][4] = {};
 #pragma unroll
-        for (int x = 0; x < KC; ++x) {
-            const uint4 a = *reinterpret_cast<const uint4*>(qa + 64 * x);
-            const uint4 a8 = *reinterpret_cast<const uint4*>(qa + 8 * S::kPitch + 64 * x);
-            const unsigned lo[4] = {a.x, a8.x, a.y, a8.y}, hi[4] = {a.z, a8.z, a.w, a8.w};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mma16816<T>(s[e], lo, k[e][x].x, k[e][x].y);
-                mma16816<T>(s[e], hi, k[e][x].z, k[e][x].w);
-            }
+        for (int kk = 0; kk < D / 16; ++kk) {
+            unsigned w[4];
+            ldsm4(w, kt + (kk >> 2) * S::kBox + k_lane + (k_xor ^ (32 * (kk & 3))));
+            mma16816<T>(x[0], qf[kk], w[0], w[1]);
+            mma16816<T>(x[1], qf[kk], w[2], w[3]);
         }
-        rows_at(next, page);
-        load_k();  // (behind the last tile: of the zero row)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[e][x] *= sign;
-        const bool masked = t + 16 > lim0;
+            for (int y = 0; y < 4; ++y) x[e][y] *= sign;
+        const bool masked = t + kTileTokens > lim0;
         if (masked) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (t + 8 * e + 2 * c + (x & 1) >= lim[x >> 1]) s[e][x] = -INFINITY;
+                for (int y = 0; y < 4; ++y)
+                    if (t + 8 * e + 2 * c + (y & 1) >= lim[y >> 1]) x[e][y] = -INFINITY;
+            // values of no token are zeroed, and values that some rows may not see made finite: they must not
+            // reach those as 0 * inf (warps that share the tile write the same)
+#pragma unroll 1
+            for (int id = lane; id < kTileTokens * (D / 8); id += 32) {
+                const int row = id / (D / 8), u = id % (D / 8);
+                uint4* at = reinterpret_cast<uint4*>(tile + (NB + (u >> 3)) * S::kBox + row * 128 + (((u & 7) ^ (row & 7)) << 4));
+                if (t + row >= lim_last) {
+                    *at = make_uint4(0u, 0u, 0u, 0u);
+                } else if (lim0 < lim_last) {
+                    const uint4 w = *at;
+                    if (pair_nonfinite<T>(w.x) || pair_nonfinite<T>(w.y) || pair_nonfinite<T>(w.z) || pair_nonfinite<T>(w.w)) {
+                        *at = make_uint4(pair_finite<T>(w.x), pair_finite<T>(w.y), pair_finite<T>(w.z), pair_finite<T>(w.w));
+                        // below 96, as an item's rows are at most 64 tokens' and what they see differs by less
+                        const int n = t - (lim0 & ~15) + row;
+                        if (n < 128) atomicOr(&poison[n >> 5], 1u << (n & 31));
+                    }
+                }
+            }
+            fence_proxy_async_smem();  // before the next copy into the tile
+            __syncwarp();
         }
         float mx[2];
-        bool grow[2];
+        bool grow = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-            grow[i] = (mx[i] - ref[i]) * qs > kGrow || (ref[i] == -INFINITY && mx[i] > -INFINITY);
+        for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+            grow |= (mx[e] - ref[e]) * qs > kGrow || (ref[e] == -INFINITY && mx[e] > -INFINITY);
         }
         // (a row's maximum has grown only if that of one of its lanes' has)
-        if (__any_sync(kAll, grow[0] || grow[1])) {
+        if (__any_sync(kAll, grow)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(kAll, mx[i], 1));
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(kAll, mx[i], 2));
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(kAll, mx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(kAll, mx[e], 2));
                 // a row moves by its own maximum alone: rows of no query have no say in how others are rounded
                 float alpha = 1.f;
-                if ((mx[i] - ref[i]) * qs > kGrow || (ref[i] == -INFINITY && mx[i] > -INFINITY)) {
-                    alpha = ref[i] == -INFINITY ? 0.f : exp2_fast((ref[i] - mx[i]) * qs);
-                    ref[i] = mx[i];
+                if ((mx[e] - ref[e]) * qs > kGrow || (ref[e] == -INFINITY && mx[e] > -INFINITY)) {
+                    alpha = ref[e] == -INFINITY ? 0.f : exp2_fast((ref[e] - mx[e]) * qs);
+                    ref[e] = mx[e];
                 }
-                l[i] *= alpha;
+                l[e] *= alpha;
 #pragma unroll
-                for (int n = 0; n < 8 * VC; ++n) {
-                    o[n][2 * i] *= alpha;
-                    o[n][2 * i + 1] *= alpha;
+                for (int n = 0; n < DW / 8; ++n) {
+                    o[n][2 * e] *= alpha;
+                    o[n][2 * e + 1] *= alpha;
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float m = ref[i] == -INFINITY ? 0.f : ref[i];
+        for (int e = 0; e < 2; ++e) {
+            const float m = ref[e] == -INFINITY ? 0.f : ref[e];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int x = 2 * i; x < 2 * i + 2; ++x) {
+                for (int y = 2 * e; y < 2 * e + 2; ++y) {
                     // (-infinity times a scale of 0 is no weight)
-                    s[e][x] = s[e][x] == -INFINITY ? 0.f : exp2_fast(fmaf(s[e][x] - m, qs, kBias<T>));
-                    l[i] += s[e][x];
+                    x[n][y] = x[n][y] == -INFINITY ? 0.f : exp2_fast(fmaf(x[n][y] - m, qs, kBias<T>));
+                    l[e] += x[n][y];
                 }
-        }
-        if (masked && lim0 < lim_last) {
-            // a value that some rows may not see must not reach them as 0 * inf
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                bool bad = false;
-#pragma unroll
-                for (int x = 0; x < VC; ++x) {
-                    const uint4 w = v[e][x];
-                    bad |= pair_nonfinite<T>(w.x) || pair_nonfinite<T>(w.y) || pair_nonfinite<T>(w.z) ||
-                           pair_nonfinite<T>(w.w);
-                }
-                if (bad) {
-#pragma unroll
-                    for (int x = 0; x < VC; ++x) {
-                        const uint4 w = v[e][x];
-                        v[e][x] = make_uint4(pair_finite<T>(w.x), pair_finite<T>(w.y), pair_finite<T>(w.z),
-                                             pair_finite<T>(w.w));
-                    }
-                    // below 96, as an item's rows are at most 64 tokens' and what they see differs by less
-                    const int at = t - (lim0 & ~15) + 2 * c + (e & 1) + 8 * (e >> 1);
-                    if (at < 128) atomicOr(&poison[at >> 5], 1u << (at & 31));
-                }
-            }
         }
         // weights in the payload type (half a step a term); the row sums take them unrounded
-        const unsigned a[4] = {f32_to_pair(make_float2(s[0][0], s[0][1]), T()),
-                               f32_to_pair(make_float2(s[0][2], s[0][3]), T()),
-                               f32_to_pair(make_float2(s[1][0], s[1][1]), T()),
-                               f32_to_pair(make_float2(s[1][2], s[1][3]), T())};
+        const unsigned a[4] = {f32_to_pair(make_float2(x[0][0], x[0][1]), T()),
+                               f32_to_pair(make_float2(x[0][2], x[0][3]), T()),
+                               f32_to_pair(make_float2(x[1][0], x[1][1]), T()),
+                               f32_to_pair(make_float2(x[1][2], x[1][3]), T())};
 #pragma unroll
-        for (int x = 0; x < VC; ++x) {
-            auto word = [](const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; };
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const unsigned sel = j & 1 ? 0x7632u : 0x5410u;
-                mma16816<T>(o[8 * x + j], a, __byte_perm(word(v[0][x], j >> 1), word(v[1][x], j >> 1), sel),
-                            __byte_perm(word(v[2][x], j >> 1), word(v[3][x], j >> 1), sel));
+        for (int n = 0; n < DW / 16; ++n) {
+            unsigned w[4];
+            ldsm4_t(w, vt + (n >> 2) * S::kBox + v_lane + (v_xor ^ (32 * (n & 3))));
+            mma16816<T>(o[2 * n], a, w[0], w[1]);
+            mma16816<T>(o[2 * n + 1], a, w[2], w[3]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->empty[set][s]);
+        if (loads && issued < mine) {  // into the stage that is done with
+            ok = __all_sync(kAll, mbar_wait(&bars->empty[set][s], phase, &g_finish_status, DCP_ERR_TIMEOUT, abort));
+            if (!ok) break;
+            load(issued, s, page);
+            page = page_at(++issued);
+        }
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (!ok && loads && lane == 0) {  // copies still in flight land before the ring's memory goes
+        for (int i = max(issued - stages, 0); i < issued; ++i) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(&bars->full[set][i % stages], (i / stages) & 1) && global_timer_ns() - t0 < kWaitLimitNs / 100) {
             }
         }
-        t = next;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         l[i] += __shfl_xor_sync(kAll, l[i], 1);
         l[i] += __shfl_xor_sync(kAll, l[i], 2);
     }
-    sync();  // every warp is done with the queries
+    sync();  // every warp is done with the ring
     // the warps' shares of a row: wt of them, 16 << rlog rows apart
     float* os = reinterpret_cast<float*>(smem);  // [wx_all][16][D]
 #pragma unroll
@@ -448,15 +483,9 @@ __device__ __forceinline__ void slim_part(const PrefixParams& p, const ChunkPart
             rm[at] = ref[i] == -INFINITY ? -INFINITY : fmaf(ref[i], qs, -kBias<T>);
             rl[at] = l[i];
         }
-        // lane (g, c) holds columns 64 x + 16 c + [0, 16) of its warp's
 #pragma unroll
-        for (int x = 0; x < VC; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int j = 4 * (y & 1), z = 2 * i + (y >> 1);
-                *reinterpret_cast<float4*>(os + at * D + DW * wd + 64 * x + 16 * c + 4 * y) =
-                    make_float4(o[8 * x + j][z], o[8 * x + j + 1][z], o[8 * x + j + 2][z], o[8 * x + j + 3][z]);
-            }
+        for (int n = 0; n < DW / 8; ++n)
+            *reinterpret_cast<float2*>(os + at * D + DW * wd + 8 * n + 2 * c) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
     }
     sync();
     if ((poison[0] | poison[1] | poison[2] | poison[3]) != 0u) {
@@ -584,15 +613,21 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kFinishThreads, D == 64 ? 4 : D == 128 ? 3 : 2)
-    prefix_finish_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ ChunkPartials ws, int tpi, int rows, int ctas, int blocks, int wlog,
+__global__ void __launch_bounds__(kFinishThreads, D == 64 ? 3 : 2)
+    prefix_finish_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ PrefixParams p, const __grid_constant__ ChunkPartials ws, int tpi, int rows, int ctas, int blocks, int wlog,
                          int slices) {
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Parts parts[8];
+    __shared__ SlimBars bars;
     if ((int)blockIdx.x < blocks) {
+        if (threadIdx.x == 0) bars.abort = 0;
+        __syncthreads();
         const int group = (int)(threadIdx.x >> 5) >> wlog;
         const int item = (int)blockIdx.x * (4 >> wlog) + group;
-        if (item < p.requests * p.N * p.Hkv) slim_part<T, D>(p, ws, tpi, rows, ctas, item, group, wlog, smem, parts);
+        if (item < p.requests * p.N * p.Hkv) 
+            slim_part<T, D>(p, kmap, vmap, ws, tpi, rows, ctas, item, group, wlog, smem, &bars, parts);
     } else {
         const int k = blockIdx.x - blocks;
         join_rest<T, D>(p, ws, tpi, rows, ctas, k / slices, k % slices, slices, parts);
@@ -604,7 +639,10 @@ cudaError_t launch(const PrefixParams& p, const ChunkPartials& ws, int tpi, int 
     const auto kernel = prefix_finish_kernel<T, D>;
     const int64_t items = (int64_t)p.requests * p.N * p.Hkv;
     const int wpi = p.slim_warps;
-    const int64_t blocks = (items + 4 / wpi - 1) / (4 / wpi);
+    const int64_t blocks = p.slim_rows ? (items + 4 / wpi - 1) / (4 / wpi) : 0;
+    // the shared-memory opt-in is a per-device function attribute
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Slim<D>::kSmem);
+    if (e != cudaSuccess) return e;
     const int slices = 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks + ctas * slices));
@@ -618,7 +656,8 @@ cudaError_t launch(const PrefixParams& p, const ChunkPartials& ws, int tpi, int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, ws, tpi, rows, ctas, (int)blocks, wpi == 4 ? 2 : wpi - 1, slices);
+    const CUtensorMap* maps = static_cast<const CUtensorMap*>(p.slim_maps);
+    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], p, ws, tpi, rows, ctas, (int)blocks, wpi == 4 ? 2 : wpi - 1, slices);
 }
 
 template <typename T>
@@ -631,6 +670,30 @@ cudaError_t launch_d(const PrefixParams& p, const ChunkPartials& ws, int tpi, in
     }
 }
 
+// Boxes of 64 columns of a head and the rows of a tile, or of a page if that is shorter.
+bool page_maps(const PrefixParams& p, int dtype, CUtensorMap* maps) {
+    const EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const CUtensorMapDataType dt = dtype == DCP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    // a dimension of extent 1 is never stepped over: give it a nominal stride
+    auto stride = [](int64_t extent, int64_t bytes) -> cuuint64_t { return (cuuint64_t)(extent > 1 ? bytes : 256); };
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    const int64_t rows = (int64_t)1 << p.page_shift;
+    for (int m = 0; m < 2; ++m) {
+        const int64_t st = m ? p.v_st : p.k_st, sh = m ? p.v_sh : p.k_sh, sp = m ? p.v_sp : p.k_sp;
+        const cuuint64_t dims[5] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, (cuuint64_t)rows, (cuuint64_t)p.num_pages,
+                                    (cuuint64_t)p.N};
+        const cuuint64_t strides[4] = {stride(p.Hkv, sh), stride(rows, st), stride(p.num_pages, sp),
+                                       stride(p.N, m ? p.v_sn : p.k_sn)};
+        const cuuint32_t box[5] = {64, 1, (cuuint32_t)(rows < kTileTokens ? rows : kTileTokens), 1, 1};
+        if (enc(&maps[m], dt, 5, m ? p.v : p.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 // Warps of an item: alone, a warp streams longest for the set-up it pays; with fewer items
@@ -638,16 +701,35 @@ cudaError_t launch_d(const PrefixParams& p, const ChunkPartials& ws, int tpi, in
 // each 16.  An own part is slim up to the rows of its warps, and up to as many tokens of a
 // rank as keep them from outlasting the others: with fewer items, a long part is better
 // cut over the SMs.
-void slim_limits(PrefixParams& p) {
+void slim_limits(PrefixParams& p, int dtype, void* maps) {
     const int64_t items = (int64_t)p.requests * p.N * p.Hkv, sms = device_sm_count();
     const int64_t drafts = ((int64_t)p.T + p.requests - 1) / p.requests;  // new tokens of a request, about
     int warps = items >= 6 * sms ? 1 : items >= 3 * sms ? 2 : 4;
     if (drafts * p.gq > 16) warps = 4;
+#ifdef SLIM_W
+    warps = SLIM_W;
+#endif
     if (p.D == 256 && warps < 2) warps = 2;  // a row's columns are two warps'
     p.slim_warps = warps;
     p.slim_rows = 16 * warps / (p.D == 256 ? 2 : 1);
     const int64_t tokens = 512 * (1 + 2 * items / (3 * sms));
     p.slim_tokens = (int)(tokens < 8192 ? tokens : 8192);
+    // boxes hold whole 8-row swizzle atoms, and a tensor map describes the pools: without, the chunk kernel takes all
+    if (p.page_shift < 3 || !page_maps(p, dtype, static_cast<CUtensorMap*>(maps))) p.slim_rows = 0;
+    p.slim_maps = maps;
+    // DCP_TEST_STALL_LOADS=1 (tests of the failure path only): no loads are issued, so the first wait on them runs out
+    const char* stall = getenv("DCP_TEST_STALL_LOADS");
+    p.stall_loads = stall && stall[0] == '1';
+}
+
+int prefix_finish_status(bool clear) {
+    int s = 0;
+    if (cudaMemcpyFromSymbol(&s, g_finish_status, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && s) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_finish_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return s;
 }
 
 cudaError_t launch_prefix_finish(const PrefixParams& p, const ChunkPartials& ws, int tpi, int rows, int ctas, int dtype,
