@@ -48,7 +48,10 @@ template <typename T, int D, class Params>
 __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Params p, const ChunkPartials ws,
                                                                       int tpi) {
     constexpr bool kPlanned = std::is_same<Params, PrefixParams>::value;
-    if constexpr (kPlanned) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (kPlanned) {
+        chain_wait();     // the plan
+        chain_release();  // what follows, which reads the plan too
+    }
     constexpr int P = MmaShape<D>::kPitch;
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char* qs = smem;
@@ -275,13 +278,14 @@ cudaError_t launch_mma(const Params& p, int dtype, cudaStream_t stream) {
     const auto kernel = chunk_attention_kernel<T, D, Params>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, kThreadsMma, smem, stream>>>(p, ws, tpi);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if constexpr (std::is_same<Params, PrefixParams>::value)
-        return launch_prefix_finish(p, ws, tpi, kRows, ctas, dtype, stream);
-    else
-        return launch_chunk_merge(p, ws, tpi, kTile, kRows, ctas, dtype, stream);
+    if constexpr (std::is_same<Params, PrefixParams>::value) {
+        e = launch_chained(kernel, ctas, kThreadsMma, smem, stream, p, ws, tpi);
+        return e != cudaSuccess ? e : launch_prefix_finish(p, ws, tpi, kRows, ctas, dtype, stream);
+    } else {
+        kernel<<<ctas, kThreadsMma, smem, stream>>>(p, ws, tpi);
+        e = cudaGetLastError();
+        return e != cudaSuccess ? e : launch_chunk_merge(p, ws, tpi, kTile, kRows, ctas, dtype, stream);
+    }
 }
 
 template <typename T, class Params>

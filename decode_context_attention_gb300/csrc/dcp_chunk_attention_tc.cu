@@ -127,6 +127,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// 32 bytes, on a 32-byte boundary.
+__device__ __forceinline__ void st_global_v8(float* at, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // A volatile read from shared memory: the compiler keeps no copy of it.
 __device__ __forceinline__ int4 ld_shared4(const int4* at) {
     int4 x;
@@ -233,8 +240,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint8_t* ring = smem + 2 * kTileBytes;
     TcBars* bar = reinterpret_cast<TcBars*>(ring + kSlots * kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // what follows a plan's parts starts on the SMs that are done
-    if constexpr (kPlanned) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (kPlanned) {
+        chain_wait();     // the plan
+        chain_release();  // what follows, which reads the plan too, starts on the SMs that are done
+    }
     const int tj = tpi / 2;        // new tokens of a row block
     const int rblk = tj * p.gq;    // its rows (at most 128)
 
@@ -767,6 +776,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                                                                    __uint_as_float(o[8 * e + 2 * k + 1])), T());
                                 *reinterpret_cast<uint4*>(orow + 64 * c + 16 * e) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
+                        } else if constexpr (kPlanned) {
+                            // rows are 512 bytes or more apart, so a store's lanes have a line each: as few as can be
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) st_global_v8(part_o + prow * D + 32 * c + 8 * e, o + 8 * e);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
@@ -837,13 +850,14 @@ cudaError_t launch_tc(const Params& p, const CUtensorMap (&maps)[3], int dtype, 
     // the shared-memory opt-in is a per-device function attribute
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, kThreadsTc, TcShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, ws, tpi);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if constexpr (std::is_same<Params, PrefixParams>::value)
-        return launch_prefix_finish(p, ws, tpi, 2 * kM, ctas, dtype, stream);
-    else
-        return launch_chunk_merge(p, ws, tpi, kTT, 2 * kM, ctas, dtype, stream);
+    if constexpr (std::is_same<Params, PrefixParams>::value) {
+        e = launch_chained(kernel, ctas, kThreadsTc, TcShape<D>::kSmem, stream, maps[0], maps[1], maps[2], p, ws, tpi);
+        return e != cudaSuccess ? e : launch_prefix_finish(p, ws, tpi, 2 * kM, ctas, dtype, stream);
+    } else {
+        kernel<<<ctas, kThreadsTc, TcShape<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p, ws, tpi);
+        e = cudaGetLastError();
+        return e != cudaSuccess ? e : launch_chunk_merge(p, ws, tpi, kTT, 2 * kM, ctas, dtype, stream);
+    }
 }
 
 template <class Params>

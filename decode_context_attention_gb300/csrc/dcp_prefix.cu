@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     const ChunkParams& c = p;
     const Groups groups = {p.groups, p.group_start, p.prefix_lens, p.N, p.page_shift, p.max_seq_len, p.max_pages};
     const int tid = threadIdx.x;
+    chain_release();
     if ((int)blockIdx.x >= p.groups) {
         const int step = (gridDim.x - p.groups) * kPlanThreads;
         for (int b = (blockIdx.x - p.groups) * kPlanThreads + tid; b < p.requests; b += step) {
@@ -121,8 +122,9 @@ int plan_rest(int B) {
 
 // The chunk kernels' partials, the plan, and the rows that are joined.
 size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len, int G) {
-    const size_t parts = align256(chunk_attention_workspace(N, B, T, H, Hkv, D, max_seq_len));
-    if (!G) return parts;
+    const size_t chunk = chunk_attention_workspace(N, B, T, H, Hkv, D, max_seq_len);
+    if (!G) return chunk;
+    const size_t parts = align256(chunk) + 256;  // (from the workspace's first 256-byte boundary on)
     const size_t rows = (size_t)2 * N * T * H;
     return parts + align256((size_t)32 * ((size_t)G + 2 * (size_t)B)) +
            align256(rows * D * 4) + align256(rows * 4);
@@ -130,6 +132,7 @@ size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, in
 
 cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stream) {
     if (!p.groups) return launch_chunk_attention(p, dtype, stream);
+    p.ws = reinterpret_cast<unsigned char*>(align256((size_t)p.ws));
     unsigned char* at = p.ws + align256(chunk_attention_workspace(p.N, p.requests, p.T, p.H, p.Hkv, p.D, p.max_seq_len));
     p.plan = reinterpret_cast<int4*>(at);
     p.slim = p.plan + 2 * ((size_t)p.groups + p.requests);

@@ -107,29 +107,6 @@ __device__ __noinline__ void find_parts(const ChunkPos* pos, int ctas, const Chu
     if (lane == 0) parts->n = count;
 }
 
-// The joined row so far: base-2 log-sum-exp of the largest part, sum of the weights, and
-// this lane's share of the outputs.
-template <int NV>
-struct Joined {
-    float mx, sum;
-    float4 acc[NV];
-};
-template <int NV>
-__device__ __forceinline__ void join(Joined<NV>& a, float z, float weight, const float4 (&o)[NV]) {
-    // mx becomes finite, infinite or NaN with the parts: as the formula has it
-    const float m = fmaxf(a.mx, z), base = m == -INFINITY ? 0.f : m;
-    const float old = exp2_fast(a.mx - base), w = exp2_fast(z - base);
-    a.mx = m;
-    a.sum = fmaf(a.sum, old, w * weight);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        a.acc[v].x = fmaf(w, o[v].x, a.acc[v].x * old);
-        a.acc[v].y = fmaf(w, o[v].y, a.acc[v].y * old);
-        a.acc[v].z = fmaf(w, o[v].z, a.acc[v].z * old);
-        a.acc[v].w = fmaf(w, o[v].w, a.acc[v].w * old);
-    }
-}
-
 template <typename P>
 __device__ __forceinline__ P* shfl_ptr(P* p, int lane) {
     return reinterpret_cast<P*>(__shfl_sync(kAll, (unsigned long long)p, lane));
@@ -141,9 +118,8 @@ __device__ __forceinline__ float reciprocal(float x) {
     return y;
 }
 
-// What a lane k < kPlaces knows of row k & (count - 1) of the rows that its warp joins: where
-// the result goes (NULL: it is none), and how many parts it has.
-constexpr int kPlaces = 8;
+// What a lane knows of its row of those that its warp joins: where the result goes (NULL:
+// it is none), and how many parts it has.
 struct JoinRow {
     unsigned char* out;
     float* lse;
@@ -154,71 +130,98 @@ struct Part {
     const float* o;
     float z, weight;
 };
-// The join of a warp's `count` rows (a power of two up to kPlaces), kPlaces parts in flight:
-// kPlaces / count of every row's at a time.  part(n): where the lane's row's n-th part lies,
-// in global or shared memory.  (Each lane works out its own row's places, which all lanes
-// then read: the instructions of a part that are not its loads come once, not eight times.)
+// The join of a warp's `count` rows (a power of two up to 8): lane k has row k & (count - 1)
+// and the parts k / count, k / count + 32 / count, ... of it, part(n) saying where they lie
+// (in global or shared memory).  32 parts at a time: their weights are the lanes', one each,
+// so that what is left for all lanes is a load and an FMA an element.
 template <typename T, int D, class Get>
 __device__ __forceinline__ void join_rows(const PrefixParams& p, int count, const JoinRow& row, Get part) {
-    constexpr int NV = (D + 127) / 128;
+    constexpr int NV = (D + 127) / 128, kBatch = 16 / NV;  // parts in flight
     const int lane = threadIdx.x & 31;
+    const bool wide = 4 * lane < D;  // (half a warp holds a row of 64)
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    Joined<NV> a[kPlaces];
+    float4 a[8][NV];  // of the rows 0 to 7; with fewer, shares of them
 #pragma unroll
-    for (int e = 0; e < kPlaces; ++e) {
-        a[e].mx = -INFINITY;
-        a[e].sum = 0.f;
+    for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int v = 0; v < NV; ++v) a[e].acc[v] = none;
-    }
-    const int step = kPlaces / count, mine = lane / count;
-    const int most = (int)__reduce_max_sync(kAll, lane < kPlaces ? (unsigned)row.parts : 0u);
+        for (int v = 0; v < NV; ++v) a[e][v] = none;
+    float m = -INFINITY, sum = 0.f;
+    const int clog = count == 8 ? 3 : count >> 1, step = 32 >> clog;
+    const int most = (int)__reduce_max_sync(kAll, (unsigned)row.parts);
 #pragma unroll 1
     for (int i = 0; i < most; i += step) {
         Part x = {nullptr, -INFINITY, 0.f};
-        if (lane < kPlaces && i + mine < row.parts) x = part(i + mine);
-        float4 o[kPlaces][NV];
+        if (i + (lane >> clog) < row.parts) x = part(i + (lane >> clog));
+        float top = x.z;
+#pragma unroll 1
+        for (int d = count; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+        top = fmaxf(top, m);
+        // the reference becomes finite or infinite with the parts, and a NaN part's weight NaN: as the formula has it
+        const float base = top == -INFINITY ? 0.f : top;
+        const float old = exp2_fast(m - base), w = exp2_fast(x.z - base);
+        float part_sum = w * x.weight;
+#pragma unroll 1
+        for (int d = count; d < 32; d <<= 1) part_sum += __shfl_xor_sync(kAll, part_sum, d);
+        sum = fmaf(sum, old, part_sum);
+        m = top;
+        if (i > 0) {
 #pragma unroll
-        for (int e = 0; e < kPlaces; ++e) {
-            const float* at = shfl_ptr(x.o, e);
+            for (int e = 0; e < 8; ++e) {
+                const float f = __shfl_sync(kAll, old, e);
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                o[e][v] = at && 4 * lane + 128 * v < D ? *reinterpret_cast<const float4*>(at + 4 * lane + 128 * v) : none;
-        }
-#pragma unroll
-        for (int e = 0; e < kPlaces; ++e)
-            join<NV>(a[e], __shfl_sync(kAll, x.z, e), __shfl_sync(kAll, x.weight, e), o[e]);
-    }
-    if (count <= 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) join<NV>(a[e], a[e + 4].mx, a[e + 4].sum, a[e + 4].acc);
-    }
-    if (count <= 2) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) join<NV>(a[e], a[e + 2].mx, a[e + 2].sum, a[e + 2].acc);
-    }
-    if (count <= 1) join<NV>(a[0], a[1].mx, a[1].sum, a[1].acc);
-    float mx = 0.f, sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPlaces; ++e) {
-        unsigned char* out = shfl_ptr(row.out, e);
-        if (lane == e) {
-            mx = a[e].mx;
-            sum = a[e].sum;
-        }
-        if (e >= count || !out) continue;
-        const float inv = a[e].sum == 0.f ? 0.f : reciprocal(a[e].sum);
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (4 * lane + 128 * v < D) {
-                const float4 x = a[e].acc[v];
-                *reinterpret_cast<uint2*>(out + 2 * (4 * lane + 128 * v)) =
-                    make_uint2(f32_to_pair(make_float2(x.x * inv, x.y * inv), T()),
-                               f32_to_pair(make_float2(x.z * inv, x.w * inv), T()));
+                for (int v = 0; v < NV; ++v) a[e][v] = make_float4(a[e][v].x * f, a[e][v].y * f, a[e][v].z * f, a[e][v].w * f);
             }
+        }
+        const unsigned on = __ballot_sync(kAll, x.o != nullptr);
+#pragma unroll 1
+        for (int b = 0; b < 32; b += kBatch) {
+            if (!(on >> b)) break;
+            float4 o[kBatch][NV];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const float* at = shfl_ptr(x.o, b + e) + 4 * lane;
+                const bool ok = (on >> (b + e) & 1) && wide;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) o[e][v] = ok ? *reinterpret_cast<const float4*>(at + 128 * v) : none;
+            }
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const float f = __shfl_sync(kAll, w, b + e);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    float4& y = a[e & 7][v];
+                    y = make_float4(fmaf(f, o[e][v].x, y.x), fmaf(f, o[e][v].y, y.y), fmaf(f, o[e][v].z, y.z),
+                                    fmaf(f, o[e][v].w, y.w));
+                }
+            }
+        }
+    }
+    auto add = [](float4& x, const float4& y) { x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        if (count <= 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) add(a[e][v], a[e + 4][v]);
+        if (count <= 2)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) add(a[e][v], a[e + 2][v]);
+        if (count <= 1) add(a[0][v], a[1][v]);
+    }
+    const float inv = sum == 0.f ? 0.f : reciprocal(sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        unsigned char* out = shfl_ptr(row.out, e);
+        const float f = __shfl_sync(kAll, inv, e);
+        if (e >= count || !out || !wide) continue;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const float4 x = a[e][v];
+            *reinterpret_cast<uint2*>(out + 2 * (4 * lane + 128 * v)) =
+                make_uint2(f32_to_pair(make_float2(x.x * f, x.y * f), T()), f32_to_pair(make_float2(x.z * f, x.w * f), T()));
+        }
     }
     if (lane < count && row.out) {
-        const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
+        const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
         *row.lse = p.base2 ? lse2 : lse2 * kLn2;
     }
 }
@@ -503,7 +506,7 @@ __device__ __forceinline__ void slim_part(const PrefixParams& p, const CUtensorM
         sync();
     }
     // what follows reads what the chunk kernel left
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_wait();
     joined = joined && q.start >= common.start && q.start + q.n <= common.start + common.n;  // (groups out of order)
     int qt0 = 0;
     if (joined) {
@@ -517,7 +520,7 @@ __device__ __forceinline__ void slim_part(const PrefixParams& p, const CUtensorM
         sync();
     }
 #pragma unroll 1
-    for (int row0 = warp; row0 < nrows; row0 += kPlaces * wpi) {
+    for (int row0 = warp; row0 < nrows; row0 += 8 * wpi) {
         const int left = (nrows - row0 + wpi - 1) >> wlog;
         const int count = left > 4 ? 8 : left > 2 ? 4 : left;
         const int row = row0 + wpi * (lane & (count - 1));
@@ -555,7 +558,7 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
     constexpr int kWarps = kFinishThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the next kernel of the stream waits for this one only: it must not end before the chunk kernel has
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_wait();
     ChunkPos x = ws.pos[c];
     const ChunkPos end = ws.pos[c + 1];
     if (x.b >= p.requests) return;  // common parts follow the requests' own
@@ -563,19 +566,30 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
         if (same_item(x, end)) return;
         x = next_item(p, x, tpi);
     }
-#pragma unroll 1
-    for (; x.b < p.requests && !(same_item(x, end) && end.tile == 0); x = next_item(p, x, tpi)) {
+    while (x.b < p.requests && !(same_item(x, end) && end.tile == 0)) {
         const Planned q = load_request(p, x.b);
+        if (q.kind == kAlone && !same_item(x, end)) {
+            // written by the chunk kernel itself, as all of its request but what the range's end cuts
+            if (x.b == end.b) {
+                if (end.tile == 0) return;
+                x = end;
+                x.tile = 0;
+            } else {
+                x.rh = p.N * p.Hkv - 1;
+                x.qt = (q.n - 1) / tpi;
+                x = next_item(p, x, tpi);
+                continue;
+            }
+        }
         const int r = x.rh / p.Hkv, hkv = x.rh % p.Hkv, j0 = x.qt * tpi;
         const int nrows = min(tpi, q.n - j0) * p.gq;
-        const bool cut = same_item(x, end);
+        const bool cut = same_item(x, end);  // (end.tile > 0)
         bool joined = q.kind == kOwn;
         Planned common;
         if (joined) {
             common = load_request(p, q.common);
             joined = q.start >= common.start && q.start + q.n <= common.start + common.n;  // (groups out of order)
         }
-        if (!joined && q.kind == kAlone && !cut) continue;  // written by the chunk kernel itself
         const int qt0 = joined ? (q.start + j0 - common.start) / tpi : 0;
         __syncthreads();  // the item before is done with `parts`
         if (warp == 0) find_parts(ws.pos, ctas, x, &parts[0]);
@@ -586,8 +600,8 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
         __syncthreads();
         const int own_n = parts[0].n < 0 ? 1 : parts[0].n;
 #pragma unroll 1
-        for (int row0 = (slice * kWarps + warp) * kPlaces; row0 < nrows; row0 += slices * kWarps * kPlaces) {
-            const int row = row0 + (lane & (kPlaces - 1));
+        for (int row0 = (slice * kWarps + warp) * 8; row0 < nrows; row0 += slices * kWarps * 8) {
+            const int row = row0 + (lane & 7);
             const bool real = row < nrows;
             const int j = real ? row / p.gq : 0, h = hkv * p.gq + (real ? row - j * p.gq : 0), tok = q.start + j0 + j;
             const int block = joined ? (tok - common.start) / tpi - qt0 : 0;
@@ -597,7 +611,7 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
             g.out = real ? out_row(p, r, tok, h) : nullptr;
             g.lse = out_lse(p, r, tok, h);
             g.parts = !real ? 0 : own_n + (!joined ? 0 : parts[1 + block].n < 0 ? 1 : parts[1 + block].n);
-            join_rows<T, D>(p, kPlaces, g, [&](int n) -> Part {
+            join_rows<T, D>(p, 8, g, [&](int n) -> Part {
                 const bool own = n < own_n;
                 const Parts& from = parts[own ? 0 : 1 + block];
                 if (from.n < 0) {  // (own rows lie behind the common ones)
@@ -609,6 +623,7 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
             });
         }
         if (cut) break;  // the range ends inside it
+        x = next_item(p, x, tpi);
     }
 }
 
@@ -644,20 +659,10 @@ cudaError_t launch(const PrefixParams& p, const ChunkPartials& ws, int tpi, int 
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Slim<D>::kSmem);
     if (e != cudaSuccess) return e;
     const int slices = 4;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks + ctas * slices));
-    cfg.blockDim = dim3(kFinishThreads);
-    cfg.dynamicSmemBytes = Slim<D>::kSmem;
-    cfg.stream = stream;
-    // the chunk kernel lets this one start as soon as an SM is free of it: slim parts need nothing of its results
-    // until their join (griddepcontrol.wait)
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    // starts as soon as an SM is free of the chunk kernel: slim parts need nothing of its results until their join
     const CUtensorMap* maps = static_cast<const CUtensorMap*>(p.slim_maps);
-    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], p, ws, tpi, rows, ctas, (int)blocks, wpi == 4 ? 2 : wpi - 1, slices);
+    return launch_chained(kernel, (unsigned)(blocks + ctas * slices), kFinishThreads, Slim<D>::kSmem, stream, maps[0],
+                          maps[1], p, ws, tpi, rows, ctas, (int)blocks, wpi == 4 ? 2 : wpi - 1, slices);
 }
 
 template <typename T>
