@@ -118,6 +118,8 @@ __device__ __forceinline__ float reciprocal(float x) {
     return y;
 }
 
+__device__ const float4 g_zero_row[64] = {};  // of a part that is not there
+
 // What a lane knows of its row of those that its warp joins: where the result goes (NULL:
 // it is none), and how many parts it has.
 struct JoinRow {
@@ -139,6 +141,7 @@ __device__ __forceinline__ void join_rows(const PrefixParams& p, int count, cons
     constexpr int NV = (D + 127) / 128, kBatch = 16 / NV;  // parts in flight
     const int lane = threadIdx.x & 31;
     const bool wide = 4 * lane < D;  // (half a warp holds a row of 64)
+    const float* const zeros = reinterpret_cast<const float*>(g_zero_row);
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 a[8][NV];  // of the rows 0 to 7; with fewer, shares of them
 #pragma unroll
@@ -150,8 +153,13 @@ __device__ __forceinline__ void join_rows(const PrefixParams& p, int count, cons
     const int most = (int)__reduce_max_sync(kAll, (unsigned)row.parts);
 #pragma unroll 1
     for (int i = 0; i < most; i += step) {
-        Part x = {nullptr, -INFINITY, 0.f};
-        if (i + (lane >> clog) < row.parts) x = part(i + (lane >> clog));
+        Part x = {zeros, -INFINITY, 0.f};
+        const bool there = i + (lane >> clog) < row.parts;
+        if (there) x = part(i + (lane >> clog));
+        // all the rows' lines on their way at once (of shared memory: no operation)
+        if (there)
+#pragma unroll
+            for (int l = 0; l < D; l += 32) asm volatile("prefetch.L2 [%0];" ::"l"(x.o + l));
         float top = x.z;
 #pragma unroll 1
         for (int d = count; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
@@ -172,17 +180,18 @@ __device__ __forceinline__ void join_rows(const PrefixParams& p, int count, cons
                 for (int v = 0; v < NV; ++v) a[e][v] = make_float4(a[e][v].x * f, a[e][v].y * f, a[e][v].z * f, a[e][v].w * f);
             }
         }
-        const unsigned on = __ballot_sync(kAll, x.o != nullptr);
+        const unsigned on = __ballot_sync(kAll, there);
 #pragma unroll 1
         for (int b = 0; b < 32; b += kBatch) {
             if (!(on >> b)) break;
             float4 o[kBatch][NV];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
-                const float* at = shfl_ptr(x.o, b + e) + 4 * lane;
-                const bool ok = (on >> (b + e) & 1) && wide;
+                // (no branch around a load: each would wait for the one before)
+                const float* row = shfl_ptr(x.o, b + e);
+                const float* at = wide ? row + 4 * lane : zeros;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) o[e][v] = ok ? *reinterpret_cast<const float4*>(at + 128 * v) : none;
+                for (int v = 0; v < NV; ++v) o[e][v] = *reinterpret_cast<const float4*>(at + 128 * v);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
