@@ -17,6 +17,7 @@
 // results entry by entry.
 #include "dcp_groups.cuh"
 #include "dcp_internal.h"
+#include "dcp_sm100.cuh"
 
 namespace dcp {
 namespace {
@@ -71,12 +72,11 @@ __device__ __forceinline__ int last_at_or_before(const I* at, int n, I x) {
 }
 
 // Lengths, and rank r's new pages.  One CTA.
-__device__ void reserve_rank(const PageParams& p, int r, bool lengths) {
+__device__ void reserve_rank(const PageParams& p, const Groups& groups, int r, bool lengths) {
     __shared__ int64_t warps[32];
     __shared__ int64_t off[kThreadsPages];
     __shared__ int have[kThreadsPages];
     const int tid = threadIdx.x;
-    const Groups groups = groups_of(p);
     const int left = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
     const int* free = p.free_pages + (int64_t)r * p.fp_sn;
     int* row = p.bt + (int64_t)r * p.bt_sn;
@@ -122,8 +122,8 @@ __device__ void reserve_rank(const PageParams& p, int r, bool lengths) {
 
 // Common entries and the tokens' arrays, by worker `worker` of `workers` threads (whole
 // warps), from what reserve_rank left in memory.
-__device__ __forceinline__ void reserve_rest(const PageParams& p, int64_t worker, int64_t workers) {
-    const Groups groups = groups_of(p);
+__device__ __forceinline__ void reserve_rest(const PageParams& p, const Groups& groups, int64_t worker,
+                                             int64_t workers) {
     if (p.G) {
         const int lane = worker & 31;
         for (int64_t pair = worker >> 5; pair < (int64_t)p.N * p.B; pair += workers >> 5) {
@@ -157,11 +157,23 @@ __device__ __forceinline__ void reserve_rest(const PageParams& p, int64_t worker
     }
 }
 
+// All of a small call by one cluster, whose barrier stands between the two steps.
+constexpr int kCluster = 8;
+__global__ void __launch_bounds__(kThreadsPages) reserve_small_kernel(const PageParams p) {
+    __shared__ GroupsHeld held;
+    const Groups groups = hold_groups(groups_of(p), &held);
+    const int cta = blockIdx.x;
+    for (int r = cta; r < p.N; r += kCluster) reserve_rank(p, groups, r, r == 0);
+    sm100::cluster_sync();
+    reserve_rest(p, groups, cta * kThreadsPages + threadIdx.x, kCluster * kThreadsPages);
+}
 __global__ void __launch_bounds__(kThreadsPages) reserve_pages_kernel(const PageParams p) {
-    reserve_rank(p, blockIdx.x, blockIdx.x == 0);
+    __shared__ GroupsHeld held;
+    reserve_rank(p, hold_groups(groups_of(p), &held), blockIdx.x, blockIdx.x == 0);
 }
 __global__ void __launch_bounds__(256) reserve_rest_kernel(const PageParams p) {
-    reserve_rest(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+    __shared__ GroupsHeld held;
+    reserve_rest(p, hold_groups(groups_of(p), &held), (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // Rank r's pages of the entries that requests give up, onto its stack in order.  The
@@ -172,9 +184,10 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
     __shared__ int64_t warps[32];
     __shared__ int64_t off[kReleaseRequests + 1];
     __shared__ int low[kReleaseRequests];
+    __shared__ GroupsHeld held;
     constexpr int kPer = kReleaseRequests / kThreadsPages;
     const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Groups groups = groups_of(p);
+    const Groups groups = hold_groups(groups_of(p), &held);
     const int have = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
     int* free = p.free_pages + (int64_t)r * p.fp_sn;
     const int* row = p.bt + (int64_t)r * p.bt_sn;
@@ -205,21 +218,33 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
         const int64_t per = ((total + kThreadsPages - 1) / kThreadsPages) * 32;  // entries of a warp
         const int64_t e0 = min(warp * per, total), e1 = min(e0 + per, total);
         auto page_at = [&](int64_t e) {
-            if (e >= e1) return -1;
-            const int i = last_at_or_before(off, nb, e);
-            const int pg = __ldg(row + (int64_t)(b0 + i) * p.bt_sb + low[i] + (e - off[i]));
-            return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
+            const int64_t at = min(e, e1 - 1);  // (no branch around the load)
+            const int i = last_at_or_before(off, nb, at);
+            const int pg = __ldg(row + (int64_t)(b0 + i) * p.bt_sb + low[i] + (at - off[i]));
+            return e < e1 && (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
         };
+        // four steps' loads at a time, which wait for one another no longer
         int64_t valid = 0;
-        for (int64_t e = e0; e < e1; e += 32) valid += __popc(__ballot_sync(0xffffffffu, page_at(e + lane) >= 0));
+        for (int64_t e = e0; e < e1; e += 128) {
+            int pg[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pg[k] = page_at(e + 32 * k + lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) valid += __popc(__ballot_sync(0xffffffffu, pg[k] >= 0));
+        }
         const int64_t upto = block_scan(lane == 0 ? valid : 0, warps, &total);
         int64_t at = pushed + __shfl_sync(0xffffffffu, upto, 0) - valid;
-        for (int64_t e = e0; e < e1; e += 32) {
-            const int pg = page_at(e + lane);
-            const unsigned on = __ballot_sync(0xffffffffu, pg >= 0);
-            const int64_t to = at + __popc(on & ((1u << lane) - 1u));
-            if (pg >= 0 && to < p.free_capacity) free[to] = pg;
-            at += __popc(on);
+        for (int64_t e = e0; e < e1; e += 128) {
+            int pg[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pg[k] = page_at(e + 32 * k + lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const unsigned on = __ballot_sync(0xffffffffu, pg[k] >= 0);
+                const int64_t to = at + __popc(on & ((1u << lane) - 1u));
+                if (pg[k] >= 0 && to < p.free_capacity) free[to] = pg[k];
+                at += __popc(on);
+            }
         }
         pushed += total;
         __syncthreads();
@@ -231,6 +256,21 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
 }  // namespace
 
 cudaError_t launch_page_reserve(const PageParams& p, cudaStream_t stream) {
+    // One launch instead of two while its eight CTAs are enough (XX).
+    if ((int64_t)p.N * p.B <= 4096 && p.T <= 65536) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kCluster);
+        cfg.blockDim = dim3(kThreadsPages);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kCluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, reserve_small_kernel, p);
+    }
     reserve_pages_kernel<<<p.N, kThreadsPages, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -52,9 +52,12 @@ struct Slim {
     static constexpr int DW = D / WD;              // columns of a warp
     static constexpr int kBox = kTileTokens * 128;  // 64 columns of a tile, 128-byte swizzled
     static constexpr int kTile = 2 * (D / 64) * kBox;  // keys, then values
-    static constexpr int kWarp = D == 64 ? 4 * kTile : 24 * 1024;  // of the ring, for each warp that shares it
-    static_assert(16 * D * 4 / WD <= kWarp, "outputs lie where the ring was");
-    static constexpr int kSmem = 4 * kWarp + 1024;
+    // bytes of the ring for each warp that shares it.  With CTAs to spare three are on an SM, with two tiles a
+    // warp (256 requests behind 2048 tokens 80 us; with three tiles and two CTAs 86); where two on each SM are
+    // all there are, larger ones keep a third off an SM that is free first (64 behind 32768: 86, otherwise 90).
+    static constexpr int kRingMany = D == 256 ? 24 * 1024 : 16 * 1024, kRingFew = D == 64 ? 16 * 1024 : 24 * 1024;
+    static_assert(16 * D * 4 / WD <= kRingMany, "outputs lie where the ring was");
+    static_assert(WD * kRingMany % kTile == 0 && WD * kRingFew % kTile == 0, "whole tiles");
 };
 struct SlimBars {
     uint64_t full[4][kMaxStages], empty[4][kMaxStages];  // by ring
@@ -251,7 +254,7 @@ __device__ __noinline__ int share_out_of_line(int n, int r, int N) { return rank
 template <typename T, int D>
 __device__ __forceinline__ void slim_part(const PrefixParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                           const ChunkPartials& ws, int tpi, int rows, int ctas, int item, int group,
-                                          int wlog, uint8_t* smem, SlimBars* bars, Parts* parts) {
+                                          int wlog, int ring_bytes, uint8_t* smem, SlimBars* bars, Parts* parts) {
     using S = Slim<D>;
     constexpr int WD = S::WD, DW = S::DW, NB = D / 64;
     __shared__ float row_m[64], row_l[64];
@@ -276,9 +279,9 @@ __device__ __forceinline__ void slim_part(const PrefixParams& p, const CUtensorM
     const int xlog = wlog - (WD - 1), wx_all = 1 << xlog;
     const int rlog = min(nrows <= 16 ? 0 : nrows <= 32 ? 1 : 2, xlog), wt = wx_all >> rlog;
     const int wd = warp >> xlog, wx = warp & (wx_all - 1), blk = wx & ((1 << rlog) - 1), first = wx >> rlog;
-    const int sharers = WD << rlog, stages = min(sharers * S::kWarp / S::kTile, kMaxStages);
-    smem += group * (wpi * S::kWarp);
-    uint8_t* const ring = smem + first * (sharers * S::kWarp);
+    const int sharers = WD << rlog, stages = min(sharers * ring_bytes / S::kTile, kMaxStages);
+    smem += group * (wpi * ring_bytes);
+    uint8_t* const ring = smem + first * (sharers * ring_bytes);
     const int set = group * wx_all + first;
     float* const rm = row_m + group * (16 * wx_all);
     float* const rl = row_l + group * (16 * wx_all);
@@ -637,10 +640,10 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kFinishThreads, D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kFinishThreads, D == 256 ? 2 : 3)
     prefix_finish_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ PrefixParams p, const __grid_constant__ ChunkPartials ws, int tpi, int rows, int ctas, int blocks, int wlog,
-                         int slices) {
+                         int ring_bytes, int slices) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Parts parts[8];
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(kFinishThreads, D == 64 ? 3 : 2)
         const int group = (int)(threadIdx.x >> 5) >> wlog;
         const int item = (int)blockIdx.x * (4 >> wlog) + group;
         if (item < p.requests * p.N * p.Hkv) 
-            slim_part<T, D>(p, kmap, vmap, ws, tpi, rows, ctas, item, group, wlog, smem, &bars, parts);
+            slim_part<T, D>(p, kmap, vmap, ws, tpi, rows, ctas, item, group, wlog, ring_bytes, smem, &bars, parts);
     } else {
         const int k = blockIdx.x - blocks;
         join_rest<T, D>(p, ws, tpi, rows, ctas, k / slices, k % slices, slices, parts);
@@ -664,14 +667,15 @@ cudaError_t launch(const PrefixParams& p, const ChunkPartials& ws, int tpi, int 
     const int64_t items = (int64_t)p.requests * p.N * p.Hkv;
     const int wpi = p.slim_warps;
     const int64_t blocks = p.slim_rows ? (items + 4 / wpi - 1) / (4 / wpi) : 0;
+    const int ring = blocks > 2 * device_sm_count() ? Slim<D>::kRingMany : Slim<D>::kRingFew, smem = 4 * ring + 1024;
     // the shared-memory opt-in is a per-device function attribute
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Slim<D>::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int slices = 4;
     // starts as soon as an SM is free of the chunk kernel: slim parts need nothing of its results until their join
     const CUtensorMap* maps = static_cast<const CUtensorMap*>(p.slim_maps);
-    return launch_chained(kernel, (unsigned)(blocks + ctas * slices), kFinishThreads, Slim<D>::kSmem, stream, maps[0],
-                          maps[1], p, ws, tpi, rows, ctas, (int)blocks, wpi == 4 ? 2 : wpi - 1, slices);
+    return launch_chained(kernel, (unsigned)(blocks + ctas * slices), kFinishThreads, smem, stream, maps[0], maps[1],
+                          p, ws, tpi, rows, ctas, (int)blocks, wpi == 4 ? 2 : wpi - 1, ring, slices);
 }
 
 template <typename T>
