@@ -6,6 +6,7 @@
 
 #include <math.h>
 
+#include "dcp_chain.cuh"
 #include "dcp_device.cuh"
 
 namespace dcp {
@@ -379,27 +380,6 @@ ChunkPartials chunk_partials_in(unsigned char* ws, int ctas, int rows, int D);
 // to do, and no launch, when no item is long enough to be cut.
 cudaError_t launch_chunk_merge(const ChunkParams& p, const ChunkPartials& ws, int tpi, int tt, int rows, int ctas,
                                int dtype, cudaStream_t stream);
-
-// A kernel of a chain whose launch and start overlap the one before (programmatic stream
-// serialisation): chain_wait() returns when that one is done and its writes are visible, and
-// chain_release() lets the next one start.  Every kernel of the chain waits, so that the
-// last one's end is the end of all.
-__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <class... P, class... A>
-cudaError_t launch_chained(void (*kernel)(P...), unsigned ctas, int threads, size_t smem, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // For a batch that shares prefixes: which own parts are slim, and what follows the chunk
 // kernel (rows of an item: tpi tokens x gq heads, at most `rows`): slim parts, and the

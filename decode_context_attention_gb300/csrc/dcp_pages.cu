@@ -12,9 +12,10 @@
 //     [max(ceil(share(cached, r) / page), S), ceil(share(cached + n, r) / page))
 // of rank r's row.  The k-th entry of a rank, counted over the requests in order, takes
 // the k-th page from the top of the rank's stack.  Entry numbers are sums over the
-// requests before: one scan of the new tokens, then one of the entries, by one CTA for
-// a rank.  Everything else (common entries, the tokens' arrays) follows from the scans'
-// results entry by entry.
+// requests before: one scan of the new tokens, then one of the entries, by the CTAs of a
+// cluster for a rank.  Everything else (common entries, the tokens' arrays) follows from
+// the scans' results entry by entry.
+#include "dcp_chain.cuh"
 #include "dcp_groups.cuh"
 #include "dcp_internal.h"
 #include "dcp_sm100.cuh"
@@ -59,6 +60,30 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t
     return v;
 }
 
+// The sum of `v` over the CTAs of this one's cluster before it, and over all `ctas`.  All
+// threads; `turn` counts the calls, whose barriers keep a value until everyone has it.
+struct Exchange {
+    int64_t of[2];
+};
+__device__ __forceinline__ int64_t sum_before(int64_t v, Exchange* x, int ctas, int turn, int64_t* total) {
+    *total = v;
+    if (ctas == 1) return 0;
+    if (threadIdx.x == 0) x->of[turn & 1] = v;
+    sm100::cluster_sync();
+    const int me = (int)sm100::cluster_ctarank();
+    int64_t before = 0, all = 0;
+    for (int k = 0; k < ctas; ++k) {
+        int64_t y;
+        asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.b64 %0, [a];\n}"
+                     : "=l"(y)
+                     : "r"(sm100::smem_u32(&x->of[turn & 1])), "r"(k));
+        all += y;
+        if (k < me) before += y;
+    }
+    *total = all;
+    return before;
+}
+
 // The last index i of [0, n) with at[i] <= x, for at[0] <= x and `at` non-decreasing.
 template <typename I>
 __device__ __forceinline__ int last_at_or_before(const I* at, int n, I x) {
@@ -71,25 +96,30 @@ __device__ __forceinline__ int last_at_or_before(const I* at, int n, I x) {
     return lo;
 }
 
-// Lengths, and rank r's new pages.  One CTA.
-__device__ void reserve_rank(const PageParams& p, const Groups& groups, int r, bool lengths) {
+// Lengths, and rank r's new pages, by CTA `cta` of `ctas`: a cluster's, or one alone.
+__device__ void reserve_rank(const PageParams& p, const Groups& groups, int r, bool lengths, int cta, int ctas) {
     __shared__ int64_t warps[32];
     __shared__ int64_t off[kThreadsPages];
     __shared__ int have[kThreadsPages];
+    __shared__ Exchange exchange;
     const int tid = threadIdx.x;
     const int left = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
     const int* free = p.free_pages + (int64_t)r * p.fp_sn;
     int* row = p.bt + (int64_t)r * p.bt_sn;
     int64_t rows = 0, used = 0;  // new tokens and entries of the requests before
-    if (lengths && tid == 0) p.query_start[0] = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreadsPages) {
-        const int b = b0 + tid;
-        const bool there = b < p.B;
-        const int cached = there ? cached_of(p, b) : 0;
+    int turn = 0;
+    if (lengths && cta == 0 && tid == 0) p.query_start[0] = 0;
+    // requests of a CTA at a time, so that all have some
+    const int per = min((p.B + ctas - 1) / ctas, kThreadsPages);
+    for (int64_t first = 0; first < p.B; first += (int64_t)per * ctas) {
+        const int64_t b0 = first + (int64_t)cta * per, b = b0 + tid;
+        const bool there = tid < per && b < p.B;
+        const int cached = there ? cached_of(p, (int)b) : 0;
         int n = there ? min(max(__ldg(p.new_lens + b), 0), p.max_seq_len - cached) : 0;
         int64_t total;
         // token rows end at T: what does not fit is cut off
-        const int64_t end = rows + block_scan(n, warps, &total);
+        int64_t end = rows + block_scan(n, warps, &total);
+        end += sum_before(total, &exchange, ctas, turn++, &total);
         const int s1 = (int)min(end, (int64_t)p.T), s0 = (int)min(end - n, (int64_t)p.T);
         n = s1 - s0;
         rows = min(rows + total, (int64_t)p.T);
@@ -99,25 +129,28 @@ __device__ void reserve_rank(const PageParams& p, const Groups& groups, int r, b
         }
         int low = 0, count = 0;
         if (there) {
-            low = max(entries_of(p, cached, r), p.G ? member_of(groups, b).entries : 0);
+            low = max(entries_of(p, cached, r), p.G ? member_of(groups, (int)b).entries : 0);
             count = max(entries_of(p, cached + n, r) - low, 0);
         }
         const int64_t upto = block_scan(count, warps, &total);
         off[tid] = upto - count;
         have[tid] = low;
+        const int64_t mine = total;
+        const int64_t before = used + sum_before(total, &exchange, ctas, turn++, &total);
         __syncthreads();
-        for (int64_t k = tid; k < total; k += kThreadsPages) {
+        for (int64_t k = tid; k < mine; k += kThreadsPages) {
             const int i = last_at_or_before(off, kThreadsPages, k);
-            const int64_t at = left - 1 - (used + k);
-            row[(int64_t)(b0 + i) * p.bt_sb + have[i] + (k - off[i])] = at >= 0 ? __ldg(free + at) : -1;
+            const int64_t at = left - 1 - (before + k);
+            row[(b0 + i) * p.bt_sb + have[i] + (k - off[i])] = at >= 0 ? __ldg(free + at) : -1;
         }
         used += total;
         __syncthreads();
     }
-    if (tid == 0) {
+    if (cta == 0 && tid == 0) {
         p.free_out[r] = (int)max(left - used, (int64_t)0);
         p.missing[r] = (int)min(max(used - left, (int64_t)0), (int64_t)0x7fffffff);
     }
+    if (ctas > 1) sm100::cluster_sync();  // a CTA's sums are read until here
 }
 
 // Common entries and the tokens' arrays, by worker `worker` of `workers` threads (whole
@@ -163,47 +196,57 @@ __global__ void __launch_bounds__(kThreadsPages) reserve_small_kernel(const Page
     __shared__ GroupsHeld held;
     const Groups groups = hold_groups(groups_of(p), &held);
     const int cta = blockIdx.x;
-    for (int r = cta; r < p.N; r += kCluster) reserve_rank(p, groups, r, r == 0);
+    for (int r = cta; r < p.N; r += kCluster) reserve_rank(p, groups, r, r == 0, 0, 1);
     sm100::cluster_sync();
     reserve_rest(p, groups, cta * kThreadsPages + threadIdx.x, kCluster * kThreadsPages);
 }
-__global__ void __launch_bounds__(kThreadsPages) reserve_pages_kernel(const PageParams p) {
+__global__ void __launch_bounds__(kThreadsPages) reserve_pages_kernel(const PageParams p, int ctas) {
     __shared__ GroupsHeld held;
-    reserve_rank(p, hold_groups(groups_of(p), &held), blockIdx.x, blockIdx.x == 0);
+    chain_release();
+    const int r = blockIdx.x / ctas;
+    reserve_rank(p, hold_groups(groups_of(p), &held), r, r == 0, blockIdx.x - r * ctas, ctas);
 }
 __global__ void __launch_bounds__(256) reserve_rest_kernel(const PageParams p) {
     __shared__ GroupsHeld held;
-    reserve_rest(p, hold_groups(groups_of(p), &held), (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+    const Groups groups = hold_groups(groups_of(p), &held);
+    chain_wait();
+    reserve_rest(p, groups, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // Rank r's pages of the entries that requests give up, onto its stack in order.  The
 // requests' entries, end to end, are dealt to the warps in equal shares: each counts
-// its valid pages, the counts' sums say where it writes.  One CTA for a rank.
+// its valid pages, the counts' sums say where it writes.  A cluster of `ctas` for a rank,
+// each with a share of the requests.
 constexpr int kReleaseRequests = 2048;  // requests whose entries are dealt at once
-__global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const PageParams p) {
+__global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const PageParams p, int ctas) {
     __shared__ int64_t warps[32];
     __shared__ int64_t off[kReleaseRequests + 1];
     __shared__ int low[kReleaseRequests];
     __shared__ GroupsHeld held;
     constexpr int kPer = kReleaseRequests / kThreadsPages;
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ Exchange exchange;
+    const int r = blockIdx.x / ctas, cta = blockIdx.x - r * ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Groups groups = hold_groups(groups_of(p), &held);
     const int have = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
     int* free = p.free_pages + (int64_t)r * p.fp_sn;
     const int* row = p.bt + (int64_t)r * p.bt_sn;
     int64_t pushed = have;
-    for (int b0 = 0; b0 < p.B; b0 += kReleaseRequests) {
-        const int nb = min(kReleaseRequests, p.B - b0);
+    int turn = 0;
+    const int per = min((p.B + ctas - 1) / ctas, kReleaseRequests);
+    for (int64_t from = 0; from < p.B; from += (int64_t)per * ctas) {
+        const int64_t b0 = from + (int64_t)cta * per;
+        const int nb = (int)min(max(p.B - b0, (int64_t)0), (int64_t)per);
         int64_t sum = 0, mine[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = kPer * tid + e, b = b0 + i;
+            const int i = kPer * tid + e;
+            const int64_t b = b0 + i;
             int count = 0;
             if (i < nb) {
                 const int L = min(max(__ldg(p.lens + b), 0), p.max_seq_len);
                 int keep = __ldg(p.keep_lens + b);
                 keep = keep < 0 ? L : min(keep, L);
-                low[i] = max(entries_of(p, keep, r), p.G ? member_of(groups, b).entries : 0);
+                low[i] = max(entries_of(p, keep, r), p.G ? member_of(groups, (int)b).entries : 0);
                 count = max(entries_of(p, L, r) - low[i], 0);
                 if (p.lens_out && r == 0) p.lens_out[b] = keep;
             }
@@ -215,12 +258,12 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
 #pragma unroll
         for (int e = 0; e < kPer; ++e) off[kPer * tid + e] = before + mine[e];
         __syncthreads();
-        const int64_t per = ((total + kThreadsPages - 1) / kThreadsPages) * 32;  // entries of a warp
-        const int64_t e0 = min(warp * per, total), e1 = min(e0 + per, total);
+        const int64_t share = ((total + kThreadsPages - 1) / kThreadsPages) * 32;  // entries of a warp
+        const int64_t e0 = min(warp * share, total), e1 = min(e0 + share, total);
         auto page_at = [&](int64_t e) {
             const int64_t at = min(e, e1 - 1);  // (no branch around the load)
             const int i = last_at_or_before(off, nb, at);
-            const int pg = __ldg(row + (int64_t)(b0 + i) * p.bt_sb + low[i] + (at - off[i]));
+            const int pg = __ldg(row + (b0 + i) * p.bt_sb + low[i] + (at - off[i]));
             return e < e1 && (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
         };
         // four steps' loads at a time, which wait for one another no longer
@@ -233,7 +276,8 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
             for (int k = 0; k < 4; ++k) valid += __popc(__ballot_sync(0xffffffffu, pg[k] >= 0));
         }
         const int64_t upto = block_scan(lane == 0 ? valid : 0, warps, &total);
-        int64_t at = pushed + __shfl_sync(0xffffffffu, upto, 0) - valid;
+        const int64_t others = sum_before(total, &exchange, ctas, turn++, &total);
+        int64_t at = pushed + others + __shfl_sync(0xffffffffu, upto, 0) - valid;
         for (int64_t e = e0; e < e1; e += 128) {
             int pg[4];
 #pragma unroll
@@ -250,41 +294,51 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
         __syncthreads();
     }
     __syncthreads();  // free_out may be free_count
-    if (tid == 0) p.free_out[r] = (int)min(pushed, (int64_t)p.free_capacity);
+    if (ctas > 1) sm100::cluster_sync();
+    if (cta == 0 && tid == 0) p.free_out[r] = (int)min(pushed, (int64_t)p.free_capacity);
+}
+
+}  // namespace
+
+namespace {
+
+// A cluster of `ctas` for each of `clusters`.
+template <class... A>
+cudaError_t launch_clusters(void (*kernel)(A...), int clusters, int ctas, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)clusters * ctas);
+    cfg.blockDim = dim3(kThreadsPages);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
 cudaError_t launch_page_reserve(const PageParams& p, cudaStream_t stream) {
-    // One launch instead of two while its eight CTAs are enough (XX).
-    if ((int64_t)p.N * p.B <= 4096 && p.T <= 65536) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kCluster);
-        cfg.blockDim = dim3(kThreadsPages);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kCluster;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, reserve_small_kernel, p);
-    }
-    reserve_pages_kernel<<<p.N, kThreadsPages, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    // One launch instead of two while its eight CTAs are enough (64 requests: 8.2 us in a graph, XX).
+    if ((int64_t)p.N * p.B <= 4096 && p.T <= 65536) return launch_clusters(reserve_small_kernel, 1, kCluster, stream, p);
+    const cudaError_t e = launch_clusters(reserve_pages_kernel, p.N, p.B > 512 ? kCluster : 1, stream, p,
+                                          p.B > 512 ? kCluster : 1);
     if (e != cudaSuccess) return e;
     const bool arrays = p.positions || p.slots || p.requests;
-    if (p.B == 0 || (!p.G && (!arrays || p.T == 0))) return cudaSuccess;
+    if (!p.G && (!arrays || p.T == 0)) return cudaSuccess;
     const int64_t copies = p.G ? (int64_t)p.N * p.B * 32 : 0, tokens = arrays ? p.T : 0;
     const int64_t blocks = ((copies > tokens ? copies : tokens) + 255) / 256, most = 8ll * device_sm_count();
-    reserve_rest_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(reserve_rest_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, stream, p);
 }
 
 cudaError_t launch_page_release(const PageParams& p, cudaStream_t stream) {
-    release_pages_kernel<<<p.N, kThreadsPages, 0, stream>>>(p);
-    return cudaGetLastError();
+    // entries that a rank's requests may give up
+    const int64_t cap = (((int64_t)p.max_seq_len + p.N - 1) / p.N + (1 << p.page_shift) - 1) >> p.page_shift;
+    const int ctas = p.B > 512 || p.B * cap > 16384 ? kCluster : 1;
+    return launch_clusters(release_pages_kernel, p.N, ctas, stream, p, ctas);
 }
 
 }  // namespace dcp

@@ -105,7 +105,8 @@ def batch(B, N, page, max_len, q, seed, groups):
 CASES = [(B, N, page, max_len, q, groups) for B, N, page, max_len, q, groups in (
     (1, 1, 16, 100, 1, 0), (1, 3, 1, 33, 40, 0), (7, 2, 16, 300, 5, 2), (64, 4, 64, 3000, 1, 1), (33, 8, 8, 500, 70, 4),
     (9, 5, 128, 4000, 900, 3), (1023, 2, 16, 90, 3, 9), (1024, 3, 4, 40, 2, 0), (1025, 1, 2, 30, 7, 17),
-    (2600, 2, 8, 64, 2, 70), (17, 16, 32, 2000, 33, 5), (3, 1, 65536, 200000, 1000, 1))]
+    (2600, 2, 8, 64, 2, 70), (17, 16, 32, 2000, 33, 5), (3, 1, 65536, 200000, 1000, 1), (513, 9, 16, 600, 5, 3), (9000, 1, 8, 50, 2, 40),
+    (8193, 2, 4, 20, 1, 1100))]
 
 
 @pytest.mark.parametrize("B,N,page,max_len,q,groups", CASES)
@@ -187,7 +188,7 @@ def test_odd_groups(gs, pl):
 
 RELEASE = [(B, N, page, max_len, groups, bad) for B, N, page, max_len, groups, bad in (
     (1, 1, 16, 100, 0, 0.0), (5, 3, 1, 70, 2, 0.3), (64, 4, 64, 3000, 1, 0.0), (33, 8, 8, 500, 4, 0.1),
-    (2047, 2, 8, 64, 9, 0.05), (2048, 1, 4, 40, 0, 0.0), (4500, 2, 16, 90, 31, 0.2), (3, 2, 2, 9000, 1, 0.01))]
+    (2047, 2, 8, 64, 9, 0.05), (2048, 1, 4, 40, 0, 0.0), (4500, 2, 16, 90, 31, 0.2), (3, 2, 2, 9000, 1, 0.01), (20, 1, 1, 3000, 2, 0.02), (16390, 1, 4, 20, 3, 0.1))]
 
 
 @pytest.mark.parametrize("B,N,page,max_len,groups,bad", RELEASE)
