@@ -126,7 +126,7 @@ __device__ __forceinline__ void add2(Pair& a, Pair b) { asm("add.rn.f32x2 %0, %0
 // (the classical reduction, as in Graham, Knuth, Patashnik, "Concrete Mathematics",
 // chapter 3, and in the sum-of-floors routines of algorithm collections).  32-bit
 // divisions where the terms fit.
-static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
     auto div = [](int64_t x, int64_t y) -> int64_t {
         return ((x | y) >> 32) ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
     };

@@ -157,21 +157,36 @@ __device__ void reserve_rank(const PageParams& p, const Groups& groups, int r, b
 // warps), from what reserve_rank left in memory.
 __device__ __forceinline__ void reserve_rest(const PageParams& p, const Groups& groups, int64_t worker,
                                              int64_t workers) {
+    const int lane = (int)(worker & 31);
     if (p.G) {
-        const int lane = worker & 31;
-        for (int64_t pair = worker >> 5; pair < (int64_t)p.N * p.B; pair += workers >> 5) {
+        // eight lanes a (request, rank): its common entries are some tens
+        for (int64_t pair = worker >> 3; pair < (int64_t)p.N * p.B; pair += workers >> 3) {
             const int b = (int)(pair / p.N), r = (int)(pair - (int64_t)b * p.N);
             const Member m = member_of(groups, b);
             const int* from = p.bt + (int64_t)r * p.bt_sn + (int64_t)m.first * p.bt_sb;
             int* to = p.bt + (int64_t)r * p.bt_sn + (int64_t)b * p.bt_sb;
-            for (int j = lane; j < m.entries; j += 32) to[j] = from[j];
+            for (int j = lane & 7; j < m.entries; j += 8) to[j] = from[j];
         }
     }
     if (!p.positions && !p.slots && !p.requests) return;
     const int n = p.query_start[p.B];
-    for (int64_t t = worker; t < n; t += workers) {
-        const int b = last_at_or_before(p.query_start, p.B + 1, (int)t);
-        const int g = cached_of(p, b) + (int)t - p.query_start[b];
+    for (int64_t t0 = worker - lane; t0 < n; t0 += workers) {
+        // the requests of the warp's first and last token, by 32 places at a time; between them each lane's own
+        auto request_of = [&](int token, int lo) {
+            int hi = p.B;  // query_start[lo] <= token; requests from hi on start behind it
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+                const int before = __popc(__ballot_sync(0xffffffffu, at < hi && p.query_start[min(at, p.B)] <= token));
+                hi = min(hi, lo + (before + 1) * step);
+                lo += before * step;
+            }
+            return lo;
+        };
+        const int first = request_of((int)t0, 0), last = request_of(min((int)t0 + 31, n - 1), first);
+        const int t = (int)t0 + lane;
+        if (t >= n) continue;
+        const int b = first + last_at_or_before(p.query_start + first, last - first + 1, t);
+        const int g = cached_of(p, b) + t - p.query_start[b];
         if (p.positions) p.positions[t] = g;
         if (p.requests) p.requests[t] = b;
         if (p.slots) {
@@ -260,18 +275,24 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
         __syncthreads();
         const int64_t share = ((total + kThreadsPages - 1) / kThreadsPages) * 32;  // entries of a warp
         const int64_t e0 = min(warp * share, total), e1 = min(e0 + share, total);
-        auto page_at = [&](int64_t e) {
-            const int64_t at = min(e, e1 - 1);  // (no branch around the load)
-            const int i = last_at_or_before(off, nb, at);
-            const int pg = __ldg(row + (b0 + i) * p.bt_sb + low[i] + (at - off[i]));
-            return e < e1 && (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
-        };
-        // four steps' loads at a time, which wait for one another no longer
-        int64_t valid = 0;
-        for (int64_t e = e0; e < e1; e += 128) {
-            int pg[4];
+        // four steps' entries, -1 behind the last one; what they name is looked at when all are on their way
+        auto pages_at = [&](int64_t e, int (&pg)[4]) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pg[k] = page_at(e + 32 * k + lane);
+            for (int k = 0; k < 4; ++k) {
+                pg[k] = -1;
+                if (e + 32 * k >= e1) continue;  // the whole warp
+                const int64_t at = min(e + 32 * k + lane, e1 - 1);
+                const int i = last_at_or_before(off, nb, at);
+                pg[k] = __ldg(row + (b0 + i) * p.bt_sb + low[i] + (at - off[i]));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + 32 * k + lane >= e1 || (unsigned)pg[k] >= (unsigned)p.num_pages) pg[k] = -1;
+        };
+        int64_t valid = 0;
+        int pg[4];
+        for (int64_t e = e0; e < e1; e += 128) {
+            pages_at(e, pg);
 #pragma unroll
             for (int k = 0; k < 4; ++k) valid += __popc(__ballot_sync(0xffffffffu, pg[k] >= 0));
         }
@@ -279,9 +300,7 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
         const int64_t others = sum_before(total, &exchange, ctas, turn++, &total);
         int64_t at = pushed + others + __shfl_sync(0xffffffffu, upto, 0) - valid;
         for (int64_t e = e0; e < e1; e += 128) {
-            int pg[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) pg[k] = page_at(e + 32 * k + lane);
+            if (e1 - e0 > 128) pages_at(e, pg);  // (else they are still there)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const unsigned on = __ballot_sync(0xffffffffu, pg[k] >= 0);
