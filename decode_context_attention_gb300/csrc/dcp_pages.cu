@@ -15,6 +15,11 @@
 // requests before: one scan of the new tokens, then one of the entries, by the CTAs of a
 // cluster for a rank.  Everything else (common entries, the tokens' arrays) follows from
 // the scans' results entry by entry.
+//
+// All of it is latency: a launch, and a chain of loads, scans and barriers.  Replayed,
+// 64 requests of one token take 8.2 us, 16384 tokens of 8 requests 10.3, 4096 requests on
+// 8 ranks 16.4 (one CTA a rank: 27); pages of 64 requests given back 8.2, of a fifth of
+// 4096 10.6 (one CTA a rank: 25).  A call from Python takes 12 to 20, its arguments' checks.
 #include "dcp_chain.cuh"
 #include "dcp_groups.cuh"
 #include "dcp_internal.h"
@@ -341,7 +346,8 @@ cudaError_t launch_clusters(void (*kernel)(A...), int clusters, int ctas, cudaSt
 }  // namespace
 
 cudaError_t launch_page_reserve(const PageParams& p, cudaStream_t stream) {
-    // One launch instead of two while its eight CTAs are enough (64 requests: 8.2 us in a graph, XX).
+    // One launch instead of two while its eight CTAs are enough (64 requests: 15 us a call and 8.2 replayed,
+    // a call with two 18).
     if ((int64_t)p.N * p.B <= 4096 && p.T <= 65536) return launch_clusters(reserve_small_kernel, 1, kCluster, stream, p);
     const cudaError_t e = launch_clusters(reserve_pages_kernel, p.N, p.B > 512 ? kCluster : 1, stream, p,
                                           p.B > 512 ? kCluster : 1);

@@ -1,5 +1,5 @@
 // dcp_prefix.cu -- the attention of a batch whose requests share long prefixes: the
-// plan in front of the chunk-attention kernels, and the join behind them.
+// plan in front of the chunk-attention kernels.
 //
 // sglang PR #34213 report, "功能与动机": partial results over disjoint tokens are
 // joined by their log-sum-exps; what that merge does over ranks is done here over the
@@ -12,10 +12,14 @@
 // left of a request is again a request over round-robin pages, from a later entry of
 // its table on.  Common keys and values are so read once for up to 256 rows, instead of
 // once a request; both kinds of parts go through one launch, cut into equal ranges.
-// Parts that are joined leave fp32 rows.
+// Parts that are joined leave fp32 rows; a request that shares nothing is written as
+// the chunk attention writes it.
 // A request's own part of few rows and tokens (a decode step's) is no work for the
 // tensor-core kernel, whose items cost 5 us of an SM each whatever their size: it is
 // left to the kernel of dcp_prefix_finish.cu, which joins it with its common part.
+// (64 single tokens behind 32768 on 4 ranks: 164 us without that kernel, 87 with it; 256
+// behind 2048: 313 and 79.)
+// Plan, parts and join are three kernels, each started while the one before ends.
 #include <cuda.h>
 
 #include "dcp_chunk.cuh"
