@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreadsMma) chunk_attention_kernel(const Para
     if constexpr (kPlanned) {
         chain_wait();     // the plan
         chain_release();  // what follows, which reads the plan too
+        if (*p.nothing) return;
     }
     constexpr int P = MmaShape<D>::kPitch;
     extern __shared__ __align__(16) unsigned char smem[];

@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if constexpr (kPlanned) {
         chain_wait();     // the plan
         chain_release();  // what follows, which reads the plan too, starts on the SMs that are done
+        if (*p.nothing) return;
     }
     const int tj = tpi / 2;        // new tokens of a row block
     const int rblk = tj * p.gq;    // its rows (at most 128)

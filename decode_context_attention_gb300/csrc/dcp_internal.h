@@ -151,6 +151,7 @@ struct PrefixParams : ChunkParams {
     int max_pages;
     int4* plan;                          // [B][2]
     int4* slim;                          // [requests][2]: own parts of few rows and tokens, which the plan leaves out
+    int* nothing;                        // whether that is all of them, and nothing is left in the plan
     int plan_tpi;                        // new tokens of a block of rows
     int slim_warps, slim_rows, slim_tokens;  // warps of a slim part, its limits
     const void* slim_maps;               // tensor maps of the pools, on the host

@@ -37,10 +37,38 @@ __device__ __forceinline__ void put(int4* at, int start, int n, int L, int b, in
 }
 // Request b's own part, L tokens from entry `first` on, to the one kernel or the other.
 __device__ __forceinline__ void put_own(const PrefixParams& p, const Request& q, int L, int b, int first, int kind,
-                                        int common) {
-    const bool slim = q.n * p.gq <= p.slim_rows && rank_share(L, 0, p.N) <= p.slim_tokens;
+                                        int common, int slim_tokens) {
+    const bool slim = q.n * p.gq <= p.slim_rows && rank_share(L, 0, p.N) <= slim_tokens;
     put(p.plan + 2 * (int64_t)b, q.start, slim ? 0 : q.n, L, b, first, kind, p.requests + common);
     put(p.slim + 2 * (int64_t)b, q.start, slim ? q.n : 0, L, b, first, kind, p.requests + common);
+}
+
+// Whether the whole batch is so little work that the kernel of the slim parts does all of it
+// sooner, prefixes read once a request, than the chunk kernel starts and ends: requests of
+// few rows, up to kSmallTokens of a rank each, and kSmallTiles tiles of 128 tokens and up to
+// 128 columns in all (a tile is 1.2 us of an SM).  All CTAs come to the same answer.
+// Replayed: 23 requests behind up to 1850 tokens on 3 ranks 33 us with the chunk kernel, 25
+// without; 18 behind 157 19 and 15; but 91 behind 998, of 2900 tiles, 36 and 42.
+constexpr int kSmallRequests = 4096;
+constexpr int kSmallTokens = 1024;
+constexpr int64_t kSmallTiles = 1900;
+__device__ __forceinline__ bool small_batch(const PrefixParams& p, int* scratch) {
+    if (p.slim_rows == 0 || p.requests > kSmallRequests) return false;
+    const ChunkParams& c = p;
+    if (threadIdx.x == 0) *scratch = 0;
+    __syncthreads();
+    int tiles = 0, wide = 0;
+    for (int b = threadIdx.x; b < p.requests; b += kPlanThreads) {
+        const Request q = load_request(c, b);
+        const int tokens = rank_share(q.L, 0, p.N);
+        if (q.n == 0) continue;
+        wide |= q.n * p.gq > p.slim_rows || tokens > kSmallTokens;
+        tiles += tokens / 128 + 1;  // at most 9 a request
+    }
+    tiles = (int)__reduce_add_sync(kAll, (unsigned)tiles);
+    if ((threadIdx.x & 31) == 0) atomicAdd(scratch, tiles);
+    wide = __syncthreads_or(wide);
+    return !wide && (int64_t)*scratch * p.N * p.Hkv * (p.D == 256 ? 2 : 1) <= kSmallTiles;
 }
 
 // One CTA a group, then CTAs for the requests outside of groups.  Every entry of the
@@ -50,13 +78,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     const ChunkParams& c = p;
     const Groups groups = {p.groups, p.group_start, p.prefix_lens, p.N, p.page_shift, p.max_seq_len, p.max_pages};
     const int tid = threadIdx.x;
+    __shared__ int scratch;
     chain_release();
+    const bool small = small_batch(p, &scratch);
+    const int slim_tokens = small ? kSmallTokens : p.slim_tokens;
+    if (blockIdx.x == 0 && tid == 0) *p.nothing = small;
     if ((int)blockIdx.x >= p.groups) {
         const int step = (gridDim.x - p.groups) * kPlanThreads;
         for (int b = (blockIdx.x - p.groups) * kPlanThreads + tid; b < p.requests; b += step) {
             if (group_of(groups, b) >= 0) continue;
             const Request q = load_request(c, b);
-            put_own(p, q, q.L, b, 0, kAlone, 0);
+            put_own(p, q, q.L, b, 0, kAlone, 0, slim_tokens);
         }
         return;
     }
@@ -99,7 +131,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
         // 796 alone; 64 single tokens: 118 shared, 541 alone.
         const int64_t tiles8 = ((int64_t)common << p.page_shift) / 16;  // in eighths
         const int64_t shared = (tokens_new + p.plan_tpi - 1) / p.plan_tpi;
-        if (blocks * (4 * tiles8 - 8 * 30) + 3 * tiles8 * slim <= shared * (8 * 13 + 4 * tiles8)) common = 0;
+        if (blocks * (4 * tiles8 - 8 * 30) + 3 * tiles8 * slim <= shared * (8 * 13 + 4 * tiles8) || small)
+            common = 0;
         entries = common;
         const Request x = load_request(c, min(b0, p.requests - 1)), y = load_request(c, max(b1 - 1, 0));
         put(p.plan + 2 * ((int64_t)p.requests + g), x.start, common ? max(y.start + y.n - x.start, 0) : 0,
@@ -111,7 +144,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
         if (group_of(groups, b) != g) continue;
         const Request q = load_request(c, b);
         // (a request without new tokens may hold less than the common part, and asks for nothing)
-        put_own(p, q, max(q.L - tokens, 0), b, common, common ? kOwn : kAlone, g);
+        put_own(p, q, max(q.L - tokens, 0), b, common, common ? kOwn : kAlone, g,
+                slim_tokens);
     }
 }
 
@@ -130,7 +164,7 @@ size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, in
     if (!G) return chunk;
     const size_t parts = align256(chunk) + 256;  // (from the workspace's first 256-byte boundary on)
     const size_t rows = (size_t)2 * N * T * H;
-    return parts + align256((size_t)32 * ((size_t)G + 2 * (size_t)B)) +
+    return parts + align256((size_t)32 * ((size_t)G + 2 * (size_t)B) + 32) +
            align256(rows * D * 4) + align256(rows * 4);
 }
 
@@ -140,7 +174,8 @@ cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stre
     unsigned char* at = p.ws + align256(chunk_attention_workspace(p.N, p.requests, p.T, p.H, p.Hkv, p.D, p.max_seq_len));
     p.plan = reinterpret_cast<int4*>(at);
     p.slim = p.plan + 2 * ((size_t)p.groups + p.requests);
-    at += align256((size_t)32 * ((size_t)p.groups + 2 * (size_t)p.requests));
+    p.nothing = reinterpret_cast<int*>(p.slim + 2 * (size_t)p.requests);
+    at += align256((size_t)32 * ((size_t)p.groups + 2 * (size_t)p.requests) + 32);
     const size_t rows = (size_t)2 * p.N * p.T * p.H;
     p.wo = reinterpret_cast<float*>(at);
     p.wl = reinterpret_cast<float*>(at + align256(rows * p.D * 4));

@@ -575,6 +575,7 @@ __device__ void join_rest(const PrefixParams& p, const ChunkPartials& ws, int tp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the next kernel of the stream waits for this one only: it must not end before the chunk kernel has
     chain_wait();
+    if (*p.nothing) return;
     ChunkPos x = ws.pos[c];
     const ChunkPos end = ws.pos[c + 1];
     if (x.b >= p.requests) return;  // common parts follow the requests' own

@@ -145,6 +145,16 @@ CASES = {
 }
 
 
+# the same behind prefixes that are longer by more than the tokens of a rank up to which a batch counts as small
+for name in [n for n in CASES if n.startswith("many")]:
+    lens, groups, kw = CASES[name]
+    more = 1040 * kw.get("N", 2)
+    inside = {b for lo, hi, n in groups for b in range(lo, hi)}
+    CASES[name.replace("many", "many, long")] = (
+        [(n, l + more if b in inside else l) for b, (n, l) in enumerate(lens)], [(lo, hi, n + more) for lo, hi, n in groups],
+        kw)
+
+
 @pytest.mark.parametrize("name", CASES)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_shared_prefixes(name, dtype):
@@ -157,7 +167,8 @@ def test_shared_prefixes(name, dtype):
 @pytest.mark.parametrize("name", ["three groups", "a request shorter than the prefix", "a request of new tokens only",
                                   "more new tokens than tokens", "chunks", "wide head dimension", "many, drafts",
                                   "many, and wide ones", "many, D 256", "many, three ranks, loose ones",
-                                  "many, one shorter"])
+                                  "many, one shorter", "many, long, drafts", "many, long, and wide ones",
+                                  "many, long, D 256", "many, long, three ranks, loose ones", "many, long, one shorter"])
 def test_not_causal_and_base_2(name):
     lens, groups, kw = CASES[name]
     bt = Shared(lens, groups, seed=5, **kw)
@@ -169,7 +180,7 @@ def test_not_causal_and_base_2(name):
 @pytest.mark.parametrize("q", [1, 40])
 def test_a_large_groups_prefix_is_read_once(D, q):
     """Members whose tables name no pages for the common part: only the first request's entries can have been read."""
-    n = 1250 if q == 1 else 6400      # (requests that fill blocks of rows alone share a longer one)
+    n = 2200 if q == 1 else 6400      # (less is done sooner by each request on its own)
     bt = Shared([(q if b < 24 else 1, n + 50 + 2 * b) for b in range(30)], [(0, 30, n)], own_entries="bad", D=D, H=4,
                 Hkv=2)
     o, lse = bt.run()
@@ -180,7 +191,8 @@ def test_a_large_groups_prefix_is_read_once(D, q):
 def test_negative_scale_and_large_scores(D):
     for scale, qs in ((-0.09, 1.0), (0.09, 60.0), (0.0, 1.0)):
         for lens, groups in (([(1, 200), (1, 190), (2, 180)], [(0, 3, 160)]),
-                             ([(1 + b % 2, 700 + 3 * b) for b in range(20)], [(0, 20, 690)])):
+                             ([(1 + b % 2, 700 + 3 * b) for b in range(20)], [(0, 20, 690)]),
+                             ([(1 + b % 2, 2900 + 3 * b) for b in range(20)], [(0, 20, 2890)])):
             bt = Shared(lens, groups, D=D, qscale=qs, dtype=torch.float16)
             bt.scale = scale
             o, lse = bt.run(scale=scale)
@@ -191,6 +203,7 @@ def test_negative_scale_and_large_scores(D):
 @pytest.mark.parametrize("where", ["prefix", "own", "future"])
 @pytest.mark.parametrize("lens,n", [([(2, 200), (1, 190), (3, 180)], 160),
                                     ([(2, 740), (1, 735)] * 9 + [(3, 720)], 690),
+                                    ([(2, 2940), (1, 2935)] * 9 + [(3, 2920)], 2890),
                                     ([(2, 740), (1, 735)] * 9 + [(50, 720)], 660)])
 def test_values_that_are_not_finite(D, where, lens, n):
     bt = Shared(lens, [(0, len(lens), n)], D=D, dtype=torch.float16, N=2)
@@ -206,7 +219,7 @@ def test_values_that_are_not_finite(D, where, lens, n):
 
 @pytest.mark.parametrize("D", [128, 256])
 def test_equal_calls_give_equal_bits_and_padding_changes_none(D):
-    lens, groups = [(1, 700 + 7 * b) for b in range(20)] + [(40, 900)], [(0, 12, 640), (12, 21, 300)]
+    lens, groups = [(1, 2900 + 7 * b) for b in range(20)] + [(40, 900)], [(0, 12, 2840), (12, 21, 300)]
     bt = Shared(lens, groups, pad=4, D=D)
     o, lse = bt.run()
     ws = torch.full((binding.prefix_workspace_bytes(bt.N, bt.B, bt.T, bt.H, bt.Hkv, D, bt.max_len, 2),), 255,

@@ -32,7 +32,7 @@ def draw(seed):
         for _ in range(r.choice((0, 0, 1, 3))):                # loose ones
             n = r.randint(0, 5)
             lens.append((n, n + r.randint(0, 200)))
-        size, prefix, q = r.choice((1, 2, 8, 20)), r.choice((0, 30, 200, 700, 1500)), r.choice((1, 1, 4, 30))
+        size, prefix, q = r.choice((1, 2, 8, 20)), r.choice((0, 30, 200, 700, 1500, 1100 * N)), r.choice((1, 1, 4, 30))
         lo = len(lens)
         for _ in range(size):
             n = r.choice((0, 1, r.randint(1, q)))
@@ -61,7 +61,7 @@ def test_random_batches(seed):
 @pytest.mark.parametrize("D", [128, 256])
 def test_pools_beyond_four_gigabytes(D):
     """The same batch in the last pages of pools of more than 2^31 elements."""
-    small = Shared([(1 + b % 2, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], N=2, D=D, H=4, Hkv=1)
+    small = Shared([(1 + b % 2, 2900 + 3 * b) for b in range(20)], [(0, 20, 2890)], N=2, D=D, H=4, Hkv=1)
     o, lse = small.run()
     n = small.k_pages.shape[1]
     pages = (1 << 31) // (small.page * D) + n + 3

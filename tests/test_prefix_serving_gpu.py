@@ -219,16 +219,17 @@ import torch
 from decode_context_attention_gb300 import binding
 from test_prefix_attention_gpu import Shared
 for D, page in ((64, 16), (128, 16), (256, 16)):
-    bt = Shared([(1 + b % 2, 700 + 3 * b) for b in range(20)], [(0, 20, 690)], D=D, page=page)
-    o, lse = bt.outputs()
-    os.environ["DCP_TEST_STALL_LOADS"] = "1"
-    binding.prefix_attention_paged(bt.q, bt.k_pages, bt.v_pages, bt.block_table, bt.query_start, bt.seq_lens, bt.max_len,
-                                   bt.group_start, bt.prefix_lens, o, lse, bt.scale)
-    torch.cuda.synchronize()
-    assert binding.device_status() == 7, "expected DCP_ERR_TIMEOUT"
-    assert binding.device_status() == 0, "the status must clear once read"
-    del os.environ["DCP_TEST_STALL_LOADS"]
-    bt.check(*bt.run())
+    for more in (0, 2200):
+        bt = Shared([(1 + b % 2, more + 700 + 3 * b) for b in range(20)], [(0, 20, more + 690)], D=D, page=page)
+        o, lse = bt.outputs()
+        os.environ["DCP_TEST_STALL_LOADS"] = "1"
+        binding.prefix_attention_paged(bt.q, bt.k_pages, bt.v_pages, bt.block_table, bt.query_start, bt.seq_lens, bt.max_len,
+                                       bt.group_start, bt.prefix_lens, o, lse, bt.scale)
+        torch.cuda.synchronize()
+        assert binding.device_status() == 7, "expected DCP_ERR_TIMEOUT"
+        assert binding.device_status() == 0, "the status must clear once read"
+        del os.environ["DCP_TEST_STALL_LOADS"]
+        bt.check(*bt.run())
 print("timeouts reported, context usable")
 """
 
