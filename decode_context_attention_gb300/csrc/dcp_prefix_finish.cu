@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kFinishThreads, D == 256 ? 2 : 3)
         __syncthreads();
         const int group = (int)(threadIdx.x >> 5) >> wlog;
         const int item = (int)blockIdx.x * (4 >> wlog) + group;
-        if (item < p.requests * p.N * p.Hkv) 
+        if (item < p.requests * p.N * p.Hkv)
             slim_part<T, D>(p, kmap, vmap, ws, tpi, rows, ctas, item, group, wlog, ring_bytes, smem, &bars, parts);
     } else {
         const int k = blockIdx.x - blocks;
@@ -729,9 +729,6 @@ void slim_limits(PrefixParams& p, int dtype, void* maps) {
     const int64_t drafts = ((int64_t)p.T + p.requests - 1) / p.requests;  // new tokens of a request, about
     int warps = items >= 6 * sms ? 1 : items >= 3 * sms ? 2 : 4;
     if (drafts * p.gq > 16) warps = 4;
-#ifdef SLIM_W
-    warps = SLIM_W;
-#endif
     if (p.D == 256 && warps < 2) warps = 2;  // a row's columns are two warps'
     p.slim_warps = warps;
     p.slim_rows = 16 * warps / (p.D == 256 ? 2 : 1);

@@ -648,7 +648,7 @@ dcp_status_t dcp_cache_evict_paged(int dtype, int N, int B, int Hkv, int D,
  *   positions, requests [T] int32, slots [T] int64: each may be NULL; rows from
  *           query_start[B] on are not written
  * Everything is a sum of integers in a fixed order: equal calls give equal results.
- * page_size a power of two up to 65536.  No workspace.
+ * page_size a power of two up to 65536.  No workspace.  With B = 0 nothing is written.
  */
 dcp_status_t dcp_page_reserve(int N, int B, int T, int page_size, int num_pages, int max_seq_len,
                               const int* cached_lens, const int* new_lens,
@@ -671,7 +671,7 @@ dcp_status_t dcp_page_reserve(int N, int B, int T, int page_size, int num_pages,
  * dropped.  free_count_out[r] (may be free_count) is the new number.  The table is
  * not written: its entries behind a request's tokens mean nothing.  A group's
  * common pages go back when its first request gives them up: that is the caller's
- * to do last.
+ * to do last.  With B = 0 nothing is written.
  */
 dcp_status_t dcp_page_release(int N, int B, int page_size, int num_pages, int max_seq_len,
                               const int* seq_lens, const int* keep_lens,
