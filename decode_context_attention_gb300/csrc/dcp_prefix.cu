@@ -48,7 +48,8 @@ __device__ __forceinline__ void put_own(const PrefixParams& p, const Request& q,
 // few rows, up to kSmallTokens of a rank each, and kSmallTiles tiles of 128 tokens and up to
 // 128 columns in all (a tile is 1.2 us of an SM).  All CTAs come to the same answer.
 // Replayed: 23 requests behind up to 1850 tokens on 3 ranks 33 us with the chunk kernel, 25
-// without; 18 behind 157 19 and 15; but 91 behind 998, of 2900 tiles, 36 and 42.
+// without; 18 behind 157 19 and 15; but 91 behind 998, of 2900 tiles, 36 and 42, and with
+// 2048 tokens of a rank one request's tiles outlast the chunk kernel (8 behind 1300 27 and 37).
 constexpr int kSmallRequests = 4096;
 constexpr int kSmallTokens = 1024;
 constexpr int64_t kSmallTiles = 1900;

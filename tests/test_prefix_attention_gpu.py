@@ -300,6 +300,61 @@ def test_captured_while_lengths_and_groups_change():
         x.check(*out)
 
 
+# on both sides of what counts as a small batch: tokens of a rank, rows of a request, tiles in all, requests
+EDGES = {
+    "1024 tokens of a rank": ([(1, 1024)] * 3 + [(1, 900)], [(0, 4, 880)], {"N": 1}),
+    "1025 tokens of a rank": ([(1, 1024)] * 3 + [(1, 1025)], [(0, 4, 880)], {"N": 1}),
+    "1025 tokens of the second rank's": ([(1, 2048), (1, 2049)] * 2, [(0, 4, 1900)], {"N": 2}),
+    "rows of four warps": ([(8, 300), (8, 310), (1, 290)], [(0, 3, 270)], {"H": 8, "Hkv": 1}),
+    "a row more": ([(8, 300), (9, 310), (1, 290)], [(0, 3, 270)], {"H": 8, "Hkv": 1}),
+    "1900 tiles": ([(1, 1024 - 128 * 4 - 20)] * 25, [(0, 25, 480)], {"N": 1, "H": 19, "Hkv": 19, "D": 64, "page": 8}),
+    "more than 1900 tiles": ([(1, 1024 - 128 * 4 - 20)] * 26, [(0, 26, 480)],
+                             {"N": 1, "H": 19, "Hkv": 19, "D": 64, "page": 8}),
+    "D 256, half of them": ([(1, 500)] * 12 + [(1, 100)], [(0, 12, 480)],
+                            {"N": 1, "H": 19, "Hkv": 19, "D": 256, "page": 8}),
+    "4096 places": ([(1, 110 + b // 100) if b % 400 == 0 else (0, 0) for b in range(4096)], [(0, 4096, 96)], {"N": 1}),
+    "4097 places": ([(1, 110 + b // 100) if b % 400 == 0 else (0, 0) for b in range(4097)], [(0, 4097, 96)], {"N": 1}),
+}
+
+
+@pytest.mark.parametrize("name", EDGES)
+def test_edges_of_small_batches(name):
+    lens, groups, kw = EDGES[name]
+    bt = Shared(lens, groups, seed=len(name), **kw)
+    bt.check(*bt.run())
+
+
+def test_captured_while_a_batch_grows_out_of_being_small():
+    """One graph, one workspace: replays whose batch the last kernel does alone, and such that share, in turn."""
+    N = 2
+    of = lambda n, own, q: ([(1 + (b + q) % 2, n + own + 3 * b) for b in range(12)], [(0, 12, n)])
+    big, small = of(2400, 90, 0), of(300, 70, 1)
+    bt = Shared(*big, pad=2, max_len=2700)
+    out = bt.outputs()
+    ws = torch.full((binding.prefix_workspace_bytes(N, bt.B, bt.T, bt.H, bt.Hkv, bt.D, bt.max_len, 1),), 255,
+                    dtype=torch.uint8, device=DEV)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        call = binding.prepare_prefix_attention_paged(bt.q, bt.k_pages, bt.v_pages, bt.block_table, bt.query_start,
+                                                      bt.seq_lens, bt.max_len, bt.group_start, bt.prefix_lens, *out,
+                                                      bt.scale, workspace=ws)
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    for k, (lens, groups) in enumerate((small, big, big, small, of(1500, 40, 1), small, of(2048, 200, 0))):
+        x = Shared(lens, groups, max_len=2700, pad=bt.T - sum(n for n, _ in lens), seed=20 + k)
+        assert x.k_pages.shape == bt.k_pages.shape and x.block_table.shape == bt.block_table.shape
+        for name in ("q", "k_pages", "v_pages", "block_table", "query_start", "seq_lens", "group_start", "prefix_lens"):
+            getattr(bt, name).copy_(getattr(x, name))
+        for t in out:
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert binding.device_status() == 0
+        x.check(*out)
+
+
 def test_two_calls_at_once_on_their_own_workspaces():
     a = Shared([(1, 900 + b) for b in range(30)], [(0, 30, 880)], seed=1)
     b = Shared([(1, 700 + b) for b in range(9)] + [(50, 800)], [(0, 9, 640)], D=64, dtype=torch.float16, seed=2)
