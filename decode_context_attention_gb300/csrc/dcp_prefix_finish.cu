@@ -673,8 +673,10 @@ cudaError_t launch(const PrefixParams& p, const ChunkPartials& ws, int tpi, int 
     const int wpi = p.slim_warps;
     const int64_t blocks = p.slim_rows ? (items + 4 / wpi - 1) / (4 / wpi) : 0;
     const int ring = blocks > 2 * device_sm_count() ? Slim<D>::kRingMany : Slim<D>::kRingFew, smem = 4 * ring + 1024;
-    // the shared-memory opt-in is a per-device function attribute
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the shared-memory opt-in is the function's on the device, not the call's: always that of the larger ring, as
+    // another host thread's call may come between this line and the launch
+    constexpr int most = 4 * (Slim<D>::kRingMany > Slim<D>::kRingFew ? Slim<D>::kRingMany : Slim<D>::kRingFew) + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     const int slices = 4;
     // starts as soon as an SM is free of the chunk kernel: slim parts need nothing of its results until their join
