@@ -46,8 +46,10 @@ template <>
 struct RequestOf<PrefixParams> {
     using type = Planned;
 };
+// (Plain loads: the kernel that reads the plan starts before the one that writes it ends, and what is read through
+// the read-only path must not change while a kernel runs; such a load may also move over the wait.)
 __device__ __forceinline__ Planned load_planned(const int4* at) {
-    const int4 a = __ldg(at), b = __ldg(at + 1);
+    const int4 a = at[0], b = at[1];
     Planned q;
     q.start = a.x; q.n = a.y; q.L = a.z; q.b = a.w;
     q.first = b.x; q.kind = b.y; q.common = b.z;
