@@ -41,6 +41,11 @@ __device__ __forceinline__ Groups groups_of(const PageParams& p) {
 __device__ __forceinline__ int cached_of(const PageParams& p, int b) {
     return min(max(__ldg(p.cached_lens + b), 0), p.max_seq_len);
 }
+// Pages on rank r's stack.  (A plain load: free_out may be free_count, and a read-only one may be made again after
+// the count has been written.)
+__device__ __forceinline__ int pages_free(const PageParams& p, int r) {
+    return min(max(p.free_count[r], 0), p.free_capacity);
+}
 
 // Inclusive sum over the block's threads; `warps` holds 33 numbers, free again
 // after the next barrier.  Ends behind a barrier.
@@ -108,7 +113,7 @@ __device__ void reserve_rank(const PageParams& p, const Groups& groups, int r, b
     __shared__ int have[kThreadsPages];
     __shared__ Exchange exchange;
     const int tid = threadIdx.x;
-    const int left = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
+    const int left = pages_free(p, r);
     const int* free = p.free_pages + (int64_t)r * p.fp_sn;
     int* row = p.bt + (int64_t)r * p.bt_sn;
     int64_t rows = 0, used = 0;  // new tokens and entries of the requests before
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(kThreadsPages) release_pages_kernel(const Page
     __shared__ Exchange exchange;
     const int r = blockIdx.x / ctas, cta = blockIdx.x - r * ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Groups groups = hold_groups(groups_of(p), &held);
-    const int have = min(max(__ldg(p.free_count + r), 0), p.free_capacity);
+    const int have = pages_free(p, r);
     int* free = p.free_pages + (int64_t)r * p.fp_sn;
     const int* row = p.bt + (int64_t)r * p.bt_sn;
     int64_t pushed = have;

@@ -45,3 +45,14 @@ def test_the_plan_of_the_prefix_attention():
     for name in sorted(os.listdir(build.CSRC)):
         for x in read_only_loads(code(name)):
             assert not re.search(r"\b(plan|slim|nothing|pos|wo|wl)\b(?!\s*\()", x), (name, x)
+
+
+def test_the_numbers_of_free_pages():
+    # a call may write the new numbers where the old ones were; the table and the starts are written before they are read
+    loads = read_only_loads(code("dcp_pages.cu"))
+    assert loads
+    for x in loads:
+        assert not re.search(r"\b(free_count|free_out|missing|query_start|seq_lens|positions|slots|requests)\b", x), x
+    text = code("dcp_pages.cu")
+    for head in ("void reserve_rank(", "void reserve_rest("):
+        assert not any(re.search(r"\bbt\b|\brow\b", x) for x in read_only_loads(body(text, head))), head
