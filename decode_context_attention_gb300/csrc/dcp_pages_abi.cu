@@ -12,6 +12,7 @@ namespace {
 struct Named {
     const char* name;
     View view;
+    bool counts = false;  // free_count and free_count_out, which may be one array
 };
 
 // What both entry points share: sizes, and the table against them.
@@ -32,8 +33,7 @@ dcp_status_t check_sizes(const char* who, int N, int B, int page_size, int num_p
     return DCP_OK;
 }
 
-dcp_status_t check_operands(const char* who, std::initializer_list<Named> in, std::initializer_list<Named> out,
-                            const int* free_count, const int* free_out) {
+dcp_status_t check_operands(const char* who, std::initializer_list<Named> in, std::initializer_list<Named> out) {
     for (const auto* l : {&in, &out})
         for (const Named& x : *l) {
             if (!x.view.fits())
@@ -47,8 +47,7 @@ dcp_status_t check_operands(const char* who, std::initializer_list<Named> in, st
             if (overlap(a->view, b->view)) return fail(DCP_ERR_ALIAS, "%s: %s and %s overlap", who, a->name, b->name);
         for (const Named& b : in) {
             // a rank's count is read and written by the same block
-            if (b.view.base == (uintptr_t)free_count && a->view.base == (uintptr_t)free_out && free_out == free_count)
-                continue;
+            if (a->counts && b.counts && a->view.base == b.view.base) continue;
             if (overlap(a->view, b.view)) return fail(DCP_ERR_ALIAS, "%s: %s overlaps %s", who, a->name, b.name);
         }
     }
@@ -90,13 +89,12 @@ dcp_status_t dcp_page_reserve(int N, int B, int T, int page_size, int num_pages,
             {{"cached_lens", row4(cached_lens, B)}, {"new_lens", row4(new_lens, B)},
              {"group_start", row4(G ? group_start : nullptr, g + 1)}, {"prefix_lens", row4(G ? prefix_lens : nullptr, g)},
              {"free_pages", View(free_pages, (int64_t)free_capacity * 4).dim(N, fp_sn * 4)},
-             {"free_count", row4(free_count, N)}},
+             {"free_count", row4(free_count, N), true}},
             {{"block_table", View(block_table, (int64_t)max_pages * 4).dim(N, bt_sn * 4).dim(B, bt_sb * 4)},
-             {"free_count_out", row4(free_count_out, N)}, {"missing", row4(missing, N)},
+             {"free_count_out", row4(free_count_out, N), true}, {"missing", row4(missing, N)},
              {"query_start", row4(query_start, (int64_t)B + 1)}, {"seq_lens", row4(seq_lens, B)},
              {"positions", row4(positions, T)}, {"slots", View(slots, slots ? 8 : 0).dim(T, 8)},
-             {"requests", row4(requests, T)}},
-            free_count, free_count_out))
+             {"requests", row4(requests, T)}}))
         return s;
     PageParams p{};
     p.N = N; p.B = B; p.T = T; p.page_shift = shift_of(page_size); p.num_pages = num_pages; p.max_seq_len = max_seq_len;
@@ -131,10 +129,9 @@ dcp_status_t dcp_page_release(int N, int B, int page_size, int num_pages, int ma
             {{"seq_lens", row4(seq_lens, B)}, {"keep_lens", row4(keep_lens, B)},
              {"group_start", row4(G ? group_start : nullptr, g + 1)}, {"prefix_lens", row4(G ? prefix_lens : nullptr, g)},
              {"block_table", View(block_table, (int64_t)max_pages * 4).dim(N, bt_sn * 4).dim(B, bt_sb * 4)},
-             {"free_count", row4(free_count, N)}},
+             {"free_count", row4(free_count, N), true}},
             {{"free_pages", View(free_pages, (int64_t)free_capacity * 4).dim(N, fp_sn * 4)},
-             {"free_count_out", row4(free_count_out, N)}, {"lens_out", row4(lens_out, B)}},
-            free_count, free_count_out))
+             {"free_count_out", row4(free_count_out, N), true}, {"lens_out", row4(lens_out, B)}}))
         return s;
     PageParams p{};
     p.N = N; p.B = B; p.page_shift = shift_of(page_size); p.num_pages = num_pages; p.max_seq_len = max_seq_len;

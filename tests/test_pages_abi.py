@@ -90,3 +90,10 @@ def test_torch_layer_checks_devices():
 def test_symbols_are_exported(lib):
     for name in ("dcp_page_reserve", "dcp_page_release"):
         assert isinstance(getattr(lib, name), ctypes._CFuncPtr)
+
+
+@pytest.mark.parametrize("call,names", [(reserve, ("lens", "new", "gs", "pl", "fp")), (release, ("lens", "keep", "gs", "pl", "bt"))])
+def test_only_the_counts_themselves_may_be_written_in_place(call, names):
+    for name in names:
+        # another array where both counts are (every call is refused before a launch)
+        assert call(**{name: FC, "fo": FC}) == ALIAS, name
