@@ -93,31 +93,35 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
         }
         return;
     }
-    __shared__ int least, tokens_new, blocks, slim, entries;
+    __shared__ int least, tokens_new, blocks, slim, entries, asks;
     const int g = blockIdx.x;
     const int b0 = min(max(__ldg(p.group_start + g), 0), p.requests);
     const int b1 = min(max(__ldg(p.group_start + g + 1), b0), p.requests);
     if (tid == 0) {
         least = p.max_seq_len;
         tokens_new = blocks = slim = 0;
+        asks = p.requests;
     }
     __syncthreads();
-    // tokens that every new token of the group sees, the blocks of rows that its requests are alone, and
-    // the requests of few rows
-    int low = p.max_seq_len, sums[3] = {0, 0, 0};
+    // tokens that every new token of the group sees, the first request that brings one, the blocks of rows that
+    // the requests are alone, and the requests of few rows
+    int low = p.max_seq_len, at = p.requests, sums[3] = {0, 0, 0};
     for (int b = b0 + tid; b < b1; b += kPlanThreads) {
         const Request q = load_request(c, b);
         if (q.n == 0 || group_of(groups, b) != g) continue;
         low = min(low, p.causal ? q.L - q.n : q.L);
+        at = min(at, b);
         sums[0] += q.n;
         if (q.n * p.gq <= p.slim_rows) ++sums[2];
         else sums[1] += (q.n + p.plan_tpi - 1) / p.plan_tpi;
     }
     low = __reduce_min_sync(kAll, low);
+    at = __reduce_min_sync(kAll, at);
 #pragma unroll
     for (int e = 0; e < 3; ++e) sums[e] = (int)__reduce_add_sync(kAll, (unsigned)sums[e]);
     if ((tid & 31) == 0) {
         atomicMin(&least, low);
+        atomicMin(&asks, at);
         atomicAdd(&tokens_new, sums[0]);
         atomicAdd(&blocks, sums[1]);
         atomicAdd(&slim, sums[2]);
@@ -136,8 +140,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
             common = 0;
         entries = common;
         const Request x = load_request(c, min(b0, p.requests - 1)), y = load_request(c, max(b1 - 1, 0));
-        put(p.plan + 2 * ((int64_t)p.requests + g), x.start, common ? max(y.start + y.n - x.start, 0) : 0,
-            (common << p.page_shift) * p.N, b0, 0, kCommon, 0);
+        // by the entries of the group's first request if it holds that many tokens, else of the first that asks,
+        // which does: a request without new tokens may hold less, and its entries then name nothing
+        const int tokens = (common << p.page_shift) * p.N;
+        put(p.plan + 2 * ((int64_t)p.requests + g), x.start, common ? max(y.start + y.n - x.start, 0) : 0, tokens,
+            x.L < tokens ? min(asks, p.requests - 1) : b0, 0, kCommon, 0);
     }
     __syncthreads();
     const int common = entries, tokens = (common << p.page_shift) * p.N;

@@ -517,9 +517,10 @@ dcp_status_t dcp_extend_attention_paged(int dtype, int N, int B, int T, int H, i
  * common part is attended once for all where that is less work than each request's on
  * its own (prompts' chunks, which read every tile for many rows, gain nothing).
  * Requests outside of groups are attended as they are.  A group shares no more than
- * every new token of it sees: when one of its requests has fewer than
- * S_g * N * page_size tokens before its new ones (causal; or in all, not causal), the
- * common part ends at the last whole page before that.
+ * every new token of it sees: when one of its requests with new tokens has fewer than
+ * S_g * N * page_size tokens before them (causal; or in all, not causal), the common
+ * part ends at the last whole page before that.  Requests without new tokens may hold
+ * fewer, the group's first one too; entries behind a request's tokens are not read.
  *
  *   group_start [G + 1], prefix_lens [G] int32 (device), group_start non-decreasing;
  *           G = 0 makes this dcp_extend_attention_paged
