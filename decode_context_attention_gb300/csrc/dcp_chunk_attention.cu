@@ -273,7 +273,7 @@ int mma_ctas(int D) { return device_sm_count() * (D == 256 ? 2 : 3); }
 
 template <typename T, int D, class Params>
 cudaError_t launch_mma(const Params& p, int dtype, cudaStream_t stream) {
-    const int ctas = mma_ctas(D), tpi = kRows / p.gq;
+    const int ctas = mma_ctas(D), tpi = chunk_attention_mma_tokens(p.gq);
     const ChunkPartials ws = chunk_partials_in(p.ws, ctas, kRows, D);
     constexpr int smem = MmaShape<D>::kSmem;
     const auto kernel = chunk_attention_kernel<T, D, Params>;
@@ -312,9 +312,10 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t
     return dtype == DCP_F16 ? launch_mma_d<__half>(p, dtype, stream) : launch_mma_d<__nv_bfloat16>(p, dtype, stream);
 }
 
-cudaError_t launch_planned_attention(const PrefixParams& p, int dtype, cudaStream_t stream) {
-    cudaError_t e;
-    if (launch_planned_attention_tc(p, dtype, stream, &e)) return e;
+int chunk_attention_mma_tokens(int gq) { return kRows / gq; }
+
+cudaError_t launch_planned_attention(const PrefixParams& p, const void* tc_maps, int dtype, cudaStream_t stream) {
+    if (tc_maps) return launch_planned_attention_tc(p, tc_maps, dtype, stream);
     return dtype == DCP_F16 ? launch_mma_d<__half>(p, dtype, stream) : launch_mma_d<__nv_bfloat16>(p, dtype, stream);
 }
 

@@ -844,8 +844,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 }
 
 template <typename T, int D, class Params>
-cudaError_t launch_tc(const Params& p, const CUtensorMap (&maps)[3], int dtype, cudaStream_t stream) {
-    const int ctas = device_sm_count(), tpi = 2 * (kM / p.gq);
+cudaError_t launch_tc(const Params& p, const CUtensorMap* maps, int dtype, cudaStream_t stream) {
+    const int ctas = device_sm_count(), tpi = chunk_attention_tc_tokens(p.gq);
     const ChunkPartials ws = chunk_partials_in(p.ws, ctas, 2 * kM, D);
     const auto kernel = chunk_attention_tc_kernel<T, D, Params>;
     // the shared-memory opt-in is a per-device function attribute
@@ -861,8 +861,8 @@ cudaError_t launch_tc(const Params& p, const CUtensorMap (&maps)[3], int dtype, 
     }
 }
 
-template <class Params>
-bool launch_tc_any(const Params& p, int dtype, cudaStream_t stream, cudaError_t* err) {
+// Whether the kernel can run these operands, and their tensor maps (queries, keys, values).
+bool tc_maps(const ChunkParams& p, int dtype, CUtensorMap* maps) {
     // the maximum of the scaled scores is that of the scores for a positive scale
     // only; boxes hold whole 8-row swizzle atoms.  Where both kernels can run this one
     // takes 199 against 326 us (drafts), 144 against 358 (mixed, D = 64), 353 against
@@ -878,7 +878,6 @@ bool launch_tc_any(const Params& p, int dtype, cudaStream_t stream, cudaError_t*
     const CUtensorMapDataType dt = dtype == DCP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     // a dimension of extent 1 is never stepped over: give it a nominal stride
     auto stride = [](int64_t extent, int64_t bytes) -> cuuint64_t { return (cuuint64_t)(extent > 1 ? bytes : 256); };
-    CUtensorMap maps[3];
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
     {
         const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.T};
@@ -902,18 +901,21 @@ bool launch_tc_any(const Params& p, int dtype, cudaStream_t stream, cudaError_t*
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;  // strides a tensor map cannot describe: the register-tiled kernel takes it
     }
+    return true;
+}
+
+template <class Params>
+cudaError_t launch_tc_any(const Params& p, const CUtensorMap* maps, int dtype, cudaStream_t stream) {
     Params q = p;
     // DCP_TEST_STALL_LOADS=1 (tests of the failure path only): no loads are
     // issued, so the first wait on them runs out.  Unset in normal use.
     const char* stall = getenv("DCP_TEST_STALL_LOADS");
     q.stall_loads = stall && stall[0] == '1';
     if (p.D == 128)
-        *err = dtype == DCP_F16 ? launch_tc<__half, 128>(q, maps, dtype, stream)
+        return dtype == DCP_F16 ? launch_tc<__half, 128>(q, maps, dtype, stream)
                                 : launch_tc<__nv_bfloat16, 128>(q, maps, dtype, stream);
-    else
-        *err = dtype == DCP_F16 ? launch_tc<__half, 64>(q, maps, dtype, stream)
-                                : launch_tc<__nv_bfloat16, 64>(q, maps, dtype, stream);
-    return true;
+    return dtype == DCP_F16 ? launch_tc<__half, 64>(q, maps, dtype, stream)
+                            : launch_tc<__nv_bfloat16, 64>(q, maps, dtype, stream);
 }
 
 }  // namespace
@@ -922,11 +924,19 @@ size_t chunk_attention_tc_workspace(int D) {
     return D == 64 || D == 128 ? chunk_partials_bytes(device_sm_count(), 2 * kM, D) : 0;
 }
 
+int chunk_attention_tc_tokens(int gq) { return 2 * (kM / gq); }
+
 bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
-    return launch_tc_any(p, dtype, stream, err);
+    CUtensorMap maps[3];
+    if (!tc_maps(p, dtype, maps)) return false;
+    *err = launch_tc_any(p, maps, dtype, stream);
+    return true;
 }
-bool launch_planned_attention_tc(const PrefixParams& p, int dtype, cudaStream_t stream, cudaError_t* err) {
-    return launch_tc_any(p, dtype, stream, err);
+bool planned_attention_tc_maps(const PrefixParams& p, int dtype, void* maps) {
+    return tc_maps(p, dtype, static_cast<CUtensorMap*>(maps));
+}
+cudaError_t launch_planned_attention_tc(const PrefixParams& p, const void* maps, int dtype, cudaStream_t stream) {
+    return launch_tc_any(p, static_cast<const CUtensorMap*>(maps), dtype, stream);
 }
 
 int chunk_attention_tc_status(bool clear) {

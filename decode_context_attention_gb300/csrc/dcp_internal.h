@@ -152,7 +152,7 @@ struct PrefixParams : ChunkParams {
     int4* plan;                          // [B][2]
     int4* slim;                          // [requests][2]: own parts of few rows and tokens, which the plan leaves out
     int* nothing;                        // whether that is all of them, and nothing is left in the plan
-    int plan_tpi;                        // new tokens of a block of rows
+    int plan_tpi;                        // new tokens of a block of rows of the chunk kernel
     int slim_warps, slim_rows, slim_tokens;  // warps of a slim part, its limits
     const void* slim_maps;               // tensor maps of the pools, on the host
     float* wo;                           // [2][N][T][H][D]: common, own
@@ -254,10 +254,15 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, cudaStream_t
 // describe): false without launching anything otherwise.
 size_t chunk_attention_tc_workspace(int D);
 bool launch_chunk_attention_tc(const ChunkParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
+// New tokens of a block of rows, of `gq` query heads a KV head: of the tcgen05 kernel, of the register-tiled one.
+int chunk_attention_tc_tokens(int gq);
+int chunk_attention_mma_tokens(int gq);
 // The same kernels over the plan of a batch that shares prefixes (p.ws: their partials), and
-// the plan and the join around them.
-cudaError_t launch_planned_attention(const PrefixParams& p, int dtype, cudaStream_t stream);
-bool launch_planned_attention_tc(const PrefixParams& p, int dtype, cudaStream_t stream, cudaError_t* err);
+// the plan and the join around them.  Which of the two runs is known before the plan is made:
+// with the tcgen05 kernel's three tensor maps in `maps`, or none (NULL) where it cannot.
+bool planned_attention_tc_maps(const PrefixParams& p, int dtype, void* maps);
+cudaError_t launch_planned_attention(const PrefixParams& p, const void* tc_maps, int dtype, cudaStream_t stream);
+cudaError_t launch_planned_attention_tc(const PrefixParams& p, const void* maps, int dtype, cudaStream_t stream);
 size_t prefix_attention_workspace(int N, int B, int T, int H, int Hkv, int D, int max_seq_len, int G);
 cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stream);
 int prefix_finish_status(bool clear);

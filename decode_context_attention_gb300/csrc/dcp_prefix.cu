@@ -10,9 +10,9 @@
 // rows of a whole group over the common pages, not causal, and every request's rows
 // over its own pages.  A common part is a multiple of N * page_size tokens, so what is
 // left of a request is again a request over round-robin pages, from a later entry of
-// its table on.  Common keys and values are so read once for up to 256 rows, instead of
-// once a request; both kinds of parts go through one launch, cut into equal ranges.
-// Parts that are joined leave fp32 rows; a request that shares nothing is written as
+// its table on.  Common keys and values are so read once for up to 256 rows (64 in the
+// register-tiled kernel), instead of once a request; both kinds of parts go through one
+// launch, cut into equal ranges.  Parts that are joined leave fp32 rows; a request that shares nothing is written as
 // the chunk attention writes it.
 // A request's own part of few rows and tokens (a decode step's) is no work for the
 // tensor-core kernel, whose items cost 5 us of an SM each whatever their size: it is
@@ -188,13 +188,15 @@ cudaError_t launch_prefix_attention(PrefixParams p, int dtype, cudaStream_t stre
     p.wo = reinterpret_cast<float*>(at);
     p.wl = reinterpret_cast<float*>(at + align256(rows * p.D * 4));
     p.B = p.groups + p.requests;
-    CUtensorMap maps[2];
+    CUtensorMap maps[2], tc_maps[3];
     slim_limits(p, dtype, maps);
-    p.plan_tpi = (p.D == 256 ? 64 : 2 * 128) / p.gq;
+    // the sharing rule counts blocks of rows as the kernel cuts them that will run
+    const bool tc = planned_attention_tc_maps(p, dtype, tc_maps);
+    p.plan_tpi = tc ? chunk_attention_tc_tokens(p.gq) : chunk_attention_mma_tokens(p.gq);
     prefix_plan_kernel<<<p.groups + plan_rest(p.requests), kPlanThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_planned_attention(p, dtype, stream);
+    return launch_planned_attention(p, tc ? tc_maps : nullptr, dtype, stream);
 }
 
 }  // namespace dcp
