@@ -179,7 +179,25 @@ __device__ __forceinline__ int item_tiles(const P& p, const R& q, int r, int qt,
     return (visible(p, q, last, r) + tt - 1) / tt;
 }
 
-// The first position of the item after `x`.
+// The first request from b on that has new tokens, or B.  Whole warps, the same b in all lanes.
+__device__ __forceinline__ int next_request(const ChunkParams& p, int b) {
+    while (b < p.B && load_request(p, b).n == 0) ++b;
+    return b;
+}
+// In a plan all slim requests have none: they are passed 32 at a time.  (One by one they took 0.3 us each, in the chunk
+// kernel and again in the join: a chunk of 300 in front of 255 single tokens 163 us, now 47; behind some millions the
+// other warps' waits for the next part ran out.  The extend, which rarely meets one, is 1% slower with this.)
+__device__ __forceinline__ int next_request(const PrefixParams& p, int b) {
+    const int lane = threadIdx.x & 31;
+    while (b < p.B) {
+        const unsigned on = __ballot_sync(0xffffffffu, load_request(p, min(b + lane, p.B - 1)).n > 0);
+        if (on) return b + __ffs(on) - 1;  // (lanes behind the last request see what its lane, before them, sees)
+        b += 32;
+    }
+    return p.B;
+}
+
+// The first position of the item after `x`; as above.
 template <class P>
 __device__ __forceinline__ ChunkPos next_item(const P& p, const ChunkPos& x, int tpi) {
     ChunkPos y = x;
@@ -188,8 +206,7 @@ __device__ __forceinline__ ChunkPos next_item(const P& p, const ChunkPos& x, int
     y.qt = 0;
     if (++y.rh < p.N * p.Hkv) return y;
     y.rh = 0;
-    do ++y.b;
-    while (y.b < p.B && load_request(p, y.b).n == 0);
+    y.b = next_request(p, y.b + 1);
     return y;
 }
 
