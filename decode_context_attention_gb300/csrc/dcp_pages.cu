@@ -18,8 +18,8 @@
 //
 // All of it is latency: a launch, and a chain of loads, scans and barriers.  Replayed,
 // 64 requests of one token take 8.2 us, 16384 tokens of 8 requests 10.3, 4096 requests on
-// 8 ranks 16.4 (one CTA a rank: 27); pages of 64 requests given back 8.2, of a fifth of
-// 4096 10.6 (one CTA a rank: 25).  A call from Python takes 12 to 20, its arguments' checks.
+// 8 ranks 16.5 (one CTA a rank: 27); pages of 64 requests given back 8.2, of a fifth of
+// 4096 10.5 (one CTA a rank: 25).  A call from Python takes 12 to 22, its arguments' checks.
 #include "dcp_chain.cuh"
 #include "dcp_groups.cuh"
 #include "dcp_internal.h"
@@ -47,7 +47,7 @@ __device__ __forceinline__ int pages_free(const PageParams& p, int r) {
     return min(max(p.free_count[r], 0), p.free_capacity);
 }
 
-// Inclusive sum over the block's threads; `warps` holds 33 numbers, free again
+// Inclusive sum over the block's threads; `warps` holds 32 numbers, free again
 // after the next barrier.  Ends behind a barrier.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

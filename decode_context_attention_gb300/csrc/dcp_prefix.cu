@@ -12,13 +12,13 @@
 // left of a request is again a request over round-robin pages, from a later entry of
 // its table on.  Common keys and values are so read once for up to 256 rows (64 in the
 // register-tiled kernel), instead of once a request; both kinds of parts go through one
-// launch, cut into equal ranges.  Parts that are joined leave fp32 rows; a request that shares nothing is written as
-// the chunk attention writes it.
+// launch, cut into equal ranges.  Parts that are joined leave fp32 rows; a request that
+// shares nothing is written as the chunk attention writes it.
 // A request's own part of few rows and tokens (a decode step's) is no work for the
 // tensor-core kernel, whose items cost 5 us of an SM each whatever their size: it is
 // left to the kernel of dcp_prefix_finish.cu, which joins it with its common part.
-// (64 single tokens behind 32768 on 4 ranks: 164 us without that kernel, 87 with it; 256
-// behind 2048: 313 and 79.)
+// (64 single tokens behind 32768 on 4 ranks: 164 us without that kernel, 88 with it; 256
+// behind 2048: 313 and 80.)
 // Plan, parts and join are three kernels, each started while the one before ends.
 #include <cuda.h>
 
@@ -46,7 +46,8 @@ __device__ __forceinline__ void put_own(const PrefixParams& p, const Request& q,
 // Whether the whole batch is so little work that the kernel of the slim parts does all of it
 // sooner, prefixes read once a request, than the chunk kernel starts and ends: requests of
 // few rows, up to kSmallTokens of a rank each, and kSmallTiles tiles of 128 tokens and up to
-// 128 columns in all (a tile is 1.2 us of an SM).  All CTAs come to the same answer.
+// 128 columns in all (a tile is 1.2 us of an SM; chosen on 152 SMs, and not scaled with
+// their number).  All CTAs come to the same answer.
 // Replayed: 23 requests behind up to 1850 tokens on 3 ranks 33 us with the chunk kernel, 25
 // without; 18 behind 157 19 and 15; but 91 behind 998, of 2900 tiles, 36 and 42, and with
 // 2048 tokens of a rank one request's tiles outlast the chunk kernel (8 behind 1300 27 and 37).
