@@ -19,7 +19,7 @@
 // All of it is latency: a launch, and a chain of loads, scans and barriers.  Replayed,
 // 64 requests of one token take 8.2 us, 16384 tokens of 8 requests 10.3, 4096 requests on
 // 8 ranks 16.5 (one CTA a rank: 27); pages of 64 requests given back 8.2, of a fifth of
-// 4096 10.5 (one CTA a rank: 25).  A call from Python takes 12 to 22, its arguments' checks.
+// 4096 10.5 (one CTA a rank: 25).  A call from Python takes 12 to 24, its arguments' checks.
 #include "dcp_chain.cuh"
 #include "dcp_groups.cuh"
 #include "dcp_internal.h"
